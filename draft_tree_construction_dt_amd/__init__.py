@@ -8,7 +8,8 @@ machines where the library has not been built yet.
 
 _BINDING_NAMES = {
     "dt_build_tree", "dt_workspace_size", "dt_status_string", "dt_position_topk",
-    "DtError", "DeviceProblem", "upload_problem", "alloc_tree_out", "library_path",
+    "dt_rope_frequencies", "dt_kv_append", "dt_tree_attention", "dt_attention_workspace", "dt_process_logits",
+    "dt_commit_path", "KVCache", "Chunk", "DtError", "DeviceProblem", "upload_problem", "alloc_tree_out", "library_path",
 }
 
 

@@ -21,9 +21,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libdt.so")
 
 DT_OK, DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED, DT_ERR_WORKSPACE, DT_ERR_HIP = 0, 1, 2, 3, 4
-DT_DTYPE_F32, DT_DTYPE_BF16 = 0, 1
+DT_DTYPE_F32, DT_DTYPE_BF16, DT_DTYPE_F16 = 0, 1, 2
 DT_MODE_DART, DT_MODE_DARTREE, DT_MODE_DARTREE_FULL = 0, 1, 2
 DT_NGRAM_NONE, DT_NGRAM_DENSE_BIGRAM, DT_NGRAM_CSR_BIGRAM, DT_NGRAM_HASH_TRIGRAM = 0, 1, 2, 3
+DT_ROPE_NONE, DT_ROPE_LINEAR, DT_ROPE_WAVELENGTH, DT_ROPE_YARN = 0, 1, 2, 3
 
 
 class DtError(RuntimeError):
@@ -61,6 +62,43 @@ class _Params(ctypes.Structure):
     ]
 
 
+def _fields(spec):
+    kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int32, "l": ctypes.c_int64, "f": ctypes.c_float,
+             "z": ctypes.c_size_t}
+    return [(name, kinds[kind]) for kind, names in spec for name in names.split()]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = _fields([("p", "k v page_table"), ("l", "layer_stride page_stride slot_stride head_stride"),
+                        ("i", "layers num_pages page_size max_pages Hkv D dtype")])
+
+
+class _Chunk(ctypes.Structure):
+    _fields_ = _fields([("i", "B lead n_max"), ("p", "ctx_len n_nodes mask depths")])
+
+
+class _AppendParams(ctypes.Structure):
+    _fields_ = _fields([("p", "q k v q_out"), ("l", "q_stride k_stride v_stride q_out_stride"), ("i", "Hq"),
+                        ("p", "q_norm k_norm"), ("f", "eps"), ("p", "freqs"), ("i", "rot_dim interleaved"),
+                        ("f", "rot_scale"), ("i", "layer"), ("p", "stream")])
+
+
+class _AttentionParams(ctypes.Structure):
+    _fields_ = _fields([("p", "q out"), ("l", "q_stride out_stride"), ("i", "Hq"), ("f", "scale"), ("p", "lse"),
+                        ("i", "layer"), ("p", "workspace"), ("z", "workspace_bytes"), ("p", "stream")])
+
+
+class _LogitsParams(ctypes.Structure):
+    _fields_ = _fields([("p", "logits out"), ("i", "B lead n_max V dtype"), ("p", "n_nodes history"),
+                        ("i", "history_max"), ("p", "history_len prompt_len node_tokens node_mask repetition "
+                                                    "frequency presence bias_ids bias"),
+                        ("i", "n_bias"), ("p", "allow allow_index"), ("i", "allow_rows"), ("p", "stream")])
+
+
+class _CommitParams(ctypes.Structure):
+    _fields_ = _fields([("p", "tokens parents target"), ("i", "L"), ("p", "accepted lengths nodes stream")])
+
+
 class _TreeOut(ctypes.Structure):
     _fields_ = [("n_nodes", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
                 ("parents", ctypes.c_void_p), ("depths", ctypes.c_void_p),
@@ -68,7 +106,8 @@ class _TreeOut(ctypes.Structure):
 
 
 EXPORTED = ("dt_build_tree", "dt_build_tree_noalloc", "dt_workspace_size", "dt_status_string", "dt_position_topk",
-            "dt_ngram_update", "dt_verify_length")
+            "dt_ngram_update", "dt_verify_length", "dt_rope_frequencies", "dt_kv_append", "dt_tree_attention",
+            "dt_attention_workspace", "dt_process_logits", "dt_commit_path")
 DT_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _lib = None
@@ -104,6 +143,21 @@ def _load():
         lib.dt_verify_length.restype = ctypes.c_int
         lib.dt_verify_length.argtypes = [ctypes.POINTER(_TreeOut), ctypes.c_int32, ctypes.c_int32, ctypes.c_double,
                                          ctypes.c_double, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+        lib.dt_rope_frequencies.restype = ctypes.c_int
+        lib.dt_rope_frequencies.argtypes = [ctypes.c_int32, ctypes.c_int32] + [ctypes.c_double] * 5 + \
+            [ctypes.c_void_p, ctypes.POINTER(ctypes.c_float)]
+        lib.dt_kv_append.restype = ctypes.c_int
+        lib.dt_kv_append.argtypes = [ctypes.POINTER(_KVCache), ctypes.POINTER(_Chunk), ctypes.POINTER(_AppendParams)]
+        lib.dt_tree_attention.restype = ctypes.c_int
+        lib.dt_tree_attention.argtypes = [ctypes.POINTER(_KVCache), ctypes.POINTER(_Chunk),
+                                          ctypes.POINTER(_AttentionParams)]
+        lib.dt_attention_workspace.restype = ctypes.c_size_t
+        lib.dt_attention_workspace.argtypes = [ctypes.POINTER(_KVCache), ctypes.POINTER(_Chunk), ctypes.c_int32]
+        lib.dt_process_logits.restype = ctypes.c_int
+        lib.dt_process_logits.argtypes = [ctypes.POINTER(_LogitsParams)]
+        lib.dt_commit_path.restype = ctypes.c_int
+        lib.dt_commit_path.argtypes = [ctypes.POINTER(_KVCache), ctypes.POINTER(_Chunk),
+                                       ctypes.POINTER(_CommitParams)]
         _lib = lib
     return _lib
 
@@ -274,6 +328,242 @@ def dt_position_topk(logits: torch.Tensor, params: Params, lse: torch.Tensor, to
     st = _load().dt_position_topk(_ptr(logits), ctypes.byref(p), _ptr(lse), _ptr(topk_tok), _ptr(topk_val))
     if st != DT_OK:
         raise DtError(st, "dt_position_topk")
+
+
+# ---------------------------------------------------------------------------
+# the verification pass over a tree (second part of dt.h)
+# ---------------------------------------------------------------------------
+
+_HEAD_TYPES = {torch.bfloat16: DT_DTYPE_BF16, torch.float16: DT_DTYPE_F16}
+_LOGIT_TYPES = {torch.float32: DT_DTYPE_F32, torch.bfloat16: DT_DTYPE_BF16}
+
+
+def _need(ok: bool, where: str, what: str) -> None:
+    """The C ABI sees addresses only: shapes, types and layouts are checked here."""
+    if not ok:
+        raise DtError(DT_ERR_INVALID_ARG, f"{where}: {what}")
+
+
+def _check(t: Optional[torch.Tensor], shape, dtype, device, where: str, name: str) -> Optional[int]:
+    """Address of a contiguous tensor of this shape and type (None: no tensor)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise DtError(DT_ERR_INVALID_ARG,
+                      f"{where}: {name} must be contiguous {dtype} {tuple(shape)} on {device}, "
+                      f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _stream_of(stream, device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream if device.type == "cuda" else 0
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+class KVCache:
+    """A paged cache of keys and values (dt_kv_cache): k and v of shape
+    [pages][page_size][Hkv][D], or [layers][pages][page_size][Hkv][D] for one
+    allocation of all layers, bf16 or f16, with equal strides and contiguous
+    heads (a [pages][Hkv][page_size][D] pool is passed as its
+    ``transpose(-3, -2)``); page_table int32 [B][max_pages].  Holds the
+    tensors; make another for other tensors."""
+
+    __slots__ = ("k", "v", "page_table", "device", "dtype", "Hkv", "D", "layers", "_struct", "_ref")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor):
+        w = "KVCache"
+        _need(k.dim() in (4, 5), w, "k must be [pages][page_size][Hkv][D] or [layers][pages][page_size][Hkv][D]")
+        _need(v.shape == k.shape and v.stride() == k.stride(), w, "v must have k's shape and strides")
+        _need(k.dtype in _HEAD_TYPES and v.dtype == k.dtype, w, "k and v must be bfloat16 or float16")
+        _need(k.stride(-1) == 1, w, "heads must be contiguous")
+        _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.is_contiguous(), w,
+              "page_table must be contiguous int32 [B][max_pages]")
+        _need(v.device == k.device and page_table.device == k.device, w, "k, v and page_table on one device")
+        self.k, self.v, self.page_table = k, v, page_table
+        self.device, self.dtype, self.Hkv, self.D = k.device, k.dtype, int(k.shape[-2]), int(k.shape[-1])
+        self.layers = int(k.shape[0]) if k.dim() == 5 else 1
+        self._struct = _KVCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), k.stride(0) if k.dim() == 5 else 0,
+                                k.stride(-4), k.stride(-3), k.stride(-2), self.layers, k.shape[-4], k.shape[-3],
+                                page_table.shape[1], self.Hkv, self.D, _HEAD_TYPES[k.dtype])
+        self._ref = ctypes.byref(self._struct)
+
+
+class Chunk:
+    """The new tokens of a batch (dt_chunk): per request `lead` committed
+    tokens and up to n_max tree nodes.  ctx_len and n_nodes int32 [B]; mask
+    and depths as dt_build_tree wrote them for a budget of n_max
+    (``Chunk.of_tree``).  Holds the tensors, whose values may change between
+    calls; make another for other tensors."""
+
+    __slots__ = ("ctx_len", "n_nodes", "mask", "depths", "B", "lead", "n_max", "rows", "device", "_struct", "_ref")
+
+    def __init__(self, ctx_len: torch.Tensor, lead: int = 1, n_max: int = 0, n_nodes: Optional[torch.Tensor] = None,
+                 mask: Optional[torch.Tensor] = None, depths: Optional[torch.Tensor] = None):
+        w, dev = "Chunk", ctx_len.device
+        _need(ctx_len.dim() == 1, w, "ctx_len must be int32 [B]")
+        B, n_max, lead = int(ctx_len.shape[0]), int(n_max), int(lead)
+        _check(ctx_len, (B,), torch.int32, dev, w, "ctx_len")
+        _check(n_nodes, (B,), torch.int32, dev, w, "n_nodes")
+        _check(mask, (B, n_max, (n_max + 31) // 32), torch.int32, dev, w, "mask")
+        _check(depths, (B, n_max), torch.int32, dev, w, "depths")
+        self.ctx_len, self.n_nodes, self.mask, self.depths = ctx_len, n_nodes, mask, depths
+        self.B, self.lead, self.n_max, self.rows, self.device = B, lead, n_max, lead + n_max, dev
+        self._struct = _Chunk(B, lead, n_max, _ptr(ctx_len), _ptr(n_nodes), _ptr(mask), _ptr(depths))
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def of_tree(cls, ctx_len: torch.Tensor, tree: TreeOut, lead: int = 1) -> "Chunk":
+        """The chunk of built trees behind `lead` committed tokens."""
+        return cls(ctx_len, lead, int(tree.tokens.shape[1]), tree.n_nodes, tree.mask, tree.depths)
+
+
+def _row_heads(t: torch.Tensor, chunk: Chunk, H: Optional[int], kv: KVCache, where: str, name: str) -> int:
+    """Row stride of a [B][rows][H][D] tensor whose rows' heads are contiguous."""
+    sh, st = t.shape, t.stride()
+    _need(len(sh) == 4 and sh[0] == chunk.B and sh[1] == chunk.rows and (H is None or sh[2] == H) and sh[3] == kv.D,
+          where, f"{name} must be [B][lead + n_max][heads][D], not {tuple(sh)}")
+    _need(t.dtype == kv.dtype and t.device == kv.device, where, f"{name} must have the cache's type and device")
+    _need(st[3] == 1 and (sh[2] == 1 or st[2] == kv.D), where, f"the heads of a row of {name} must be contiguous")
+    if sh[0] == 1:
+        return st[1]
+    if sh[1] == 1:
+        return st[0]
+    _need(st[0] == sh[1] * st[1], where, f"the rows of {name} must be evenly spaced over the batch")
+    return st[1]
+
+
+def _pass_devices(kv: Optional[KVCache], chunk: Chunk, where: str) -> None:
+    _need(kv is None or (chunk.device == kv.device and kv.page_table.shape[0] >= chunk.B), where,
+          "the chunk and the cache must be on one device, with a row of page_table for every request")
+
+
+def dt_rope_frequencies(rot_dim: int, base: float, kind: int = DT_ROPE_NONE, factor: float = 1.0, low: float = 1.0,
+                        high: float = 32.0, original: float = 4096.0):
+    """(float64 CPU tensor [rot_dim / 2] of radians a position, rot_scale) of
+    rotary positions, scaled for long contexts by `kind`."""
+    freqs = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
+    scale = ctypes.c_float()
+    st = _load().dt_rope_frequencies(int(kind), int(rot_dim), float(base), float(factor), float(low), float(high),
+                                     float(original), freqs.data_ptr(), ctypes.byref(scale))
+    if st != DT_OK:
+        raise DtError(st, "dt_rope_frequencies")
+    return freqs, scale.value
+
+
+def dt_kv_append(kv: KVCache, chunk: Chunk, k: torch.Tensor, v: torch.Tensor, q: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, q_norm: Optional[torch.Tensor] = None,
+                 k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6, freqs: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, rot_scale: float = 1.0, layer: int = 0, stream=None) -> None:
+    """Norm and turn the chunk's queries and keys, put keys and values into
+    the cache (see dt_kv_append in dt.h).  q, k, v, q_out [B][lead + n_max]
+    [heads][D], evenly spaced rows (slices of one projection); q_norm and
+    k_norm [D]; freqs float64 [rot_dim / 2] on the device."""
+    w = "dt_kv_append"
+    _pass_devices(kv, chunk, w)
+    Hq = int(q.shape[2]) if q is not None and q.dim() == 4 else None
+    p = _AppendParams(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out),
+                      0 if q is None else _row_heads(q, chunk, None, kv, w, "q"),
+                      _row_heads(k, chunk, kv.Hkv, kv, w, "k"), _row_heads(v, chunk, kv.Hkv, kv, w, "v"),
+                      0 if q_out is None else _row_heads(q_out, chunk, Hq, kv, w, "q_out"), Hq or 0,
+                      _check(q_norm, (kv.D,), kv.dtype, kv.device, w, "q_norm"),
+                      _check(k_norm, (kv.D,), kv.dtype, kv.device, w, "k_norm"), eps,
+                      None if freqs is None else _check(freqs, (freqs.numel(),), torch.float64, kv.device, w, "freqs"),
+                      0 if freqs is None else 2 * freqs.numel(), bool(interleaved), rot_scale, layer,
+                      _stream_of(stream, kv.device))
+    st = _load().dt_kv_append(kv._ref, chunk._ref, ctypes.byref(p))
+    if st != DT_OK:
+        raise DtError(st, w)
+
+
+def dt_attention_workspace(kv: KVCache, chunk: Chunk, Hq: int) -> int:
+    return int(_load().dt_attention_workspace(kv._ref, chunk._ref, int(Hq)))
+
+
+def dt_tree_attention(kv: KVCache, chunk: Chunk, q: torch.Tensor, out: torch.Tensor, scale: Optional[float] = None,
+                      lse: Optional[torch.Tensor] = None, layer: int = 0, workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """Attention of the chunk's rows over the cache (see dt_tree_attention in
+    dt.h).  q and out [B][lead + n_max][Hq][D]; scale defaults to D^-1/2; lse
+    float32 [B][lead + n_max][Hq] or None; workspace of
+    dt_attention_workspace() bytes."""
+    w = "dt_tree_attention"
+    _pass_devices(kv, chunk, w)
+    q_stride = _row_heads(q, chunk, None, kv, w, "q")
+    Hq = int(q.shape[2])
+    p = _AttentionParams(q.data_ptr(), out.data_ptr(), q_stride, _row_heads(out, chunk, Hq, kv, w, "out"), Hq,
+                         kv.D ** -0.5 if scale is None else scale,
+                         _check(lse, (chunk.B, chunk.rows, Hq), torch.float32, kv.device, w, "lse"), layer,
+                         _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                         _stream_of(stream, kv.device))
+    _need(workspace is None or workspace.device == kv.device, w, "workspace must be on the cache's device")
+    st = _load().dt_tree_attention(kv._ref, chunk._ref, ctypes.byref(p))
+    if st != DT_OK:
+        raise DtError(st, w)
+
+
+def dt_process_logits(logits: torch.Tensor, out: torch.Tensor, history: Optional[torch.Tensor] = None,
+                      history_len: Optional[torch.Tensor] = None, prompt_len: Optional[torch.Tensor] = None,
+                      repetition: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                      presence: Optional[torch.Tensor] = None, bias_ids: Optional[torch.Tensor] = None,
+                      bias: Optional[torch.Tensor] = None, allow: Optional[torch.Tensor] = None,
+                      allow_index: Optional[torch.Tensor] = None, lead: Optional[int] = None,
+                      n_nodes: Optional[torch.Tensor] = None, node_tokens: Optional[torch.Tensor] = None,
+                      node_mask: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Penalties, biases and grammar masks on logits [B][lead + n_max][V]
+    (see dt_process_logits in dt.h).  lead defaults to every row (draft
+    positions, no tree).  history int32 [B][history_max]; bias_ids int32 and
+    bias float32 [B][n_bias]; allow int32 [allow_rows][ceil(V/32)];
+    allow_index int32 [B][lead + n_max]; the rest [B]."""
+    w, dev = "dt_process_logits", logits.device
+    _need(logits.dim() == 3 and logits.dtype in _LOGIT_TYPES, w, "logits must be float32 or bfloat16 [B][rows][V]")
+    B, rows, V = (int(x) for x in logits.shape)
+    lead = rows if lead is None else int(lead)
+    n_max, i32, f32 = rows - lead, torch.int32, torch.float32
+    _need(0 <= lead <= rows, w, "lead must be 0..rows")
+    for t, name in ((history, "history"), (bias_ids, "bias_ids"), (allow, "allow")):
+        _need(t is None or t.dim() == 2, w, f"{name} must have two axes")
+    hmax = 0 if history is None else int(history.shape[1])
+    nb = 0 if bias_ids is None else int(bias_ids.shape[1])
+    arows = 0 if allow is None else int(allow.shape[0])
+    p = _LogitsParams(
+        _check(logits, logits.shape, logits.dtype, dev, w, "logits"),
+        _check(out, logits.shape, logits.dtype, dev, w, "out"), B, lead, n_max, V, _LOGIT_TYPES[logits.dtype],
+        _check(n_nodes, (B,), i32, dev, w, "n_nodes"), _check(history, (B, hmax), i32, dev, w, "history"), hmax,
+        _check(history_len, (B,), i32, dev, w, "history_len"), _check(prompt_len, (B,), i32, dev, w, "prompt_len"),
+        _check(node_tokens, (B, n_max), i32, dev, w, "node_tokens"),
+        _check(node_mask, (B, n_max, (n_max + 31) // 32), i32, dev, w, "node_mask"),
+        _check(repetition, (B,), f32, dev, w, "repetition"), _check(frequency, (B,), f32, dev, w, "frequency"),
+        _check(presence, (B,), f32, dev, w, "presence"), _check(bias_ids, (B, nb), i32, dev, w, "bias_ids"),
+        _check(bias, (B, nb), f32, dev, w, "bias"), nb,
+        _check(allow, (arows, (V + 31) // 32), i32, dev, w, "allow"),
+        _check(allow_index, (B, rows), i32, dev, w, "allow_index"), arows, _stream_of(stream, dev))
+    st = _load().dt_process_logits(ctypes.byref(p))
+    if st != DT_OK:
+        raise DtError(st, w)
+
+
+def dt_commit_path(kv: Optional[KVCache], chunk: Chunk, tokens: Optional[torch.Tensor],
+                   parents: Optional[torch.Tensor], target: torch.Tensor, accepted: torch.Tensor,
+                   lengths: torch.Tensor, nodes: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Accept each tree's path along the target's choices and move its keys
+    and values, in every layer, to the front of the chunk's slots (see
+    dt_commit_path in dt.h).  tokens and parents int32 [B][n_max] as
+    dt_build_tree wrote them; target int32 [B][lead + n_max]; accepted and
+    nodes int32 [B][L], lengths int32 [B] are written."""
+    w, dev, i32 = "dt_commit_path", chunk.device, torch.int32
+    _pass_devices(kv, chunk, w)
+    _need(accepted.dim() == 2, w, "accepted must be int32 [B][L]")
+    L = int(accepted.shape[1])
+    p = _CommitParams(_check(tokens, (chunk.B, chunk.n_max), i32, dev, w, "tokens"),
+                      _check(parents, (chunk.B, chunk.n_max), i32, dev, w, "parents"),
+                      _check(target, (chunk.B, chunk.rows), i32, dev, w, "target"), L,
+                      _check(accepted, (chunk.B, L), i32, dev, w, "accepted"),
+                      _check(lengths, (chunk.B,), i32, dev, w, "lengths"),
+                      _check(nodes, (chunk.B, L), i32, dev, w, "nodes"), _stream_of(stream, dev))
+    st = _load().dt_commit_path(None if kv is None else kv._ref, chunk._ref, ctypes.byref(p))
+    if st != DT_OK:
+        raise DtError(st, w)
 
 
 # ---------------------------------------------------------------------------

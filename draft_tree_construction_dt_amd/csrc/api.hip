@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "common.h"
+#include "pass.h"
 
 namespace dt {
 
@@ -586,5 +587,318 @@ extern "C" dt_status dt_verify_length(const dt_tree_out* tree, int32_t B, int32_
     a.n_verify = n_verify;
     a.rank = rank;
     if (launch_verify(a, (hipStream_t)stream) != hipSuccess) return DT_ERR_HIP;
+    return DT_OK;
+}
+
+// ---------------------------------------------------------------------------
+// the verification pass (dt.h, second part)
+// ---------------------------------------------------------------------------
+namespace dt {
+
+// Makes the stream's device current for the launches of one call.
+class DeviceScope {
+public:
+    explicit DeviceScope(hipStream_t stream) {
+        int dev = 0;
+        if (hipGetDevice(&cur_) != hipSuccess) return;
+        if (stream ? hipStreamGetDevice(stream, &dev) != hipSuccess : false) return;
+        if (stream && dev != cur_) {
+            if (hipSetDevice(dev) != hipSuccess) return;
+            moved_ = true;
+        }
+        ok_ = true;
+    }
+    ~DeviceScope() {
+        if (moved_) (void)hipSetDevice(cur_);
+    }
+    DeviceScope(const DeviceScope&) = delete;
+    DeviceScope& operator=(const DeviceScope&) = delete;
+    bool ok() const { return ok_; }
+
+private:
+    int cur_ = 0;
+    bool moved_ = false, ok_ = false;
+};
+
+static bool misaligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
+static bool bad_stride(int64_t s) { return s < 0 || (s & 7) != 0; }
+
+// A cache's shape; its pointers too where `pointers` is set.
+static dt_status check_cache(const dt_kv_cache* kv, bool pointers) {
+    if (!kv) return DT_ERR_INVALID_ARG;
+    if (kv->layers < 1 || kv->num_pages < 1 || kv->page_size < 1 || kv->max_pages < 1 || kv->Hkv < 1 || kv->D < 1)
+        return DT_ERR_INVALID_ARG;
+    if (kv->dtype != DT_DTYPE_BF16 && kv->dtype != DT_DTYPE_F16) return DT_ERR_INVALID_ARG;
+    if ((kv->layers > 1 && bad_stride(kv->layer_stride)) || (kv->num_pages > 1 && bad_stride(kv->page_stride)) ||
+        (kv->page_size > 1 && bad_stride(kv->slot_stride)) || (kv->Hkv > 1 && bad_stride(kv->head_stride)))
+        return DT_ERR_INVALID_ARG;
+    if (kv->D != 64 && kv->D != 128 && kv->D != 256) return DT_ERR_UNSUPPORTED;
+    if (kv->Hkv > kMaxPassHeads || (int64_t)kv->max_pages * kv->page_size > kMaxSlots) return DT_ERR_UNSUPPORTED;
+    if (pointers && (!kv->k || !kv->v || !kv->page_table || misaligned(kv->k, 16) || misaligned(kv->v, 16) ||
+                     misaligned(kv->page_table, 4)))
+        return DT_ERR_INVALID_ARG;
+    return DT_OK;
+}
+
+static dt_status check_chunk(const dt_chunk* c, bool pointers) {
+    if (!c || c->B < 0 || c->lead < 0 || c->n_max < 0) return DT_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)c->lead + c->n_max;
+    if (rows < 1) return DT_ERR_INVALID_ARG;
+    if (c->B > 65535 || rows > kMaxChunkRows) return DT_ERR_UNSUPPORTED;
+    if (pointers && c->B > 0 && (!c->ctx_len || misaligned(c->ctx_len, 4) || misaligned(c->n_nodes, 4) ||
+                                 misaligned(c->mask, 4) || misaligned(c->depths, 4)))
+        return DT_ERR_INVALID_ARG;
+    return DT_OK;
+}
+
+static ChunkArgs chunk_args(const dt_chunk* c) {
+    ChunkArgs a{};
+    a.B = c->B;
+    a.lead = c->lead;
+    a.n_max = c->n_max;
+    a.rows = c->lead + c->n_max;
+    a.mask_words = (c->n_max + 31) / 32;
+    a.ctx_len = c->ctx_len;
+    a.n_nodes = c->n_nodes;
+    a.mask = c->n_max ? c->mask : nullptr;
+    a.depths = c->n_max ? c->depths : nullptr;
+    return a;
+}
+
+static CacheArgs cache_args(const dt_kv_cache* kv, int layer) {
+    CacheArgs a{};
+    const int64_t at = kv->layers > 1 ? layer * kv->layer_stride : 0;
+    a.k = (uint16_t*)kv->k + at;
+    a.v = (uint16_t*)kv->v + at;
+    a.page_table = kv->page_table;
+    a.page_stride = kv->num_pages > 1 ? kv->page_stride : 0;
+    a.slot_stride = kv->page_size > 1 ? kv->slot_stride : 0;
+    a.head_stride = kv->Hkv > 1 ? kv->head_stride : 0;
+    a.num_pages = kv->num_pages;
+    a.page_size = kv->page_size;
+    a.max_pages = kv->max_pages;
+    a.Hkv = kv->Hkv;
+    a.D = kv->D;
+    a.cap = (int)((int64_t)kv->max_pages * kv->page_size);
+    a.page_shift = (kv->page_size & (kv->page_size - 1)) == 0 ? __builtin_ctz((unsigned)kv->page_size) : -1;
+    return a;
+}
+
+// Rows of `heads` heads of D elements: aligned, and apart where there are several.
+static bool bad_rows(const void* p, int64_t stride, int64_t rows, int64_t heads, int D) {
+    return !p || misaligned(p, 16) || (rows > 1 && (bad_stride(stride) || stride < heads * D));
+}
+
+static dt_status check_attention_shape(const dt_kv_cache* kv, const dt_chunk* c, int32_t Hq) {
+    dt_status st = check_cache(kv, false);
+    if (st != DT_OK) return st;
+    if ((st = check_chunk(c, false)) != DT_OK) return st;
+    if (Hq < 1 || Hq % kv->Hkv != 0) return DT_ERR_INVALID_ARG;
+    if (Hq > kMaxPassHeads) return DT_ERR_UNSUPPORTED;
+    if ((int64_t)c->B * (c->lead + c->n_max) * Hq > INT32_MAX) return DT_ERR_UNSUPPORTED;
+    return DT_OK;
+}
+
+}  // namespace dt
+
+extern "C" dt_status dt_rope_frequencies(int32_t kind, int32_t rot_dim, double base, double factor, double low,
+                                         double high, double original, double* freqs, float* scale) {
+    if (!freqs || !scale || rot_dim < 2 || rot_dim % 2 != 0) return DT_ERR_INVALID_ARG;
+    if (kind < DT_ROPE_NONE || kind > DT_ROPE_YARN) return DT_ERR_INVALID_ARG;
+    if (!isfinite(base) || !(base > 1.0) || !isfinite(factor) || !(factor > 0.0)) return DT_ERR_INVALID_ARG;
+    const bool blend = kind == DT_ROPE_WAVELENGTH || kind == DT_ROPE_YARN;
+    if (blend && (!(low > 0.0) || !(high > low) || !isfinite(high) || !(original > 0.0) || !isfinite(original)))
+        return DT_ERR_INVALID_ARG;
+    const double pi2 = 6.283185307179586476925;
+    double i_low = 0, i_high = 0;
+    if (kind == DT_ROPE_YARN) {
+        const auto pair_of = [&](double turns) { return rot_dim * log(original / (pi2 * turns)) / (2 * log(base)); };
+        const auto clamp = [&](double x) { return x < 0 ? 0 : (x > rot_dim - 1 ? rot_dim - 1 : x); };
+        i_low = clamp(floor(pair_of(high)));
+        i_high = clamp(ceil(pair_of(low)));
+        if (i_high == i_low) i_high += 0.001;
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = pow(base, -2.0 * i / rot_dim);
+        double s = 1;                              // weight of the unscaled frequency
+        if (kind == DT_ROPE_LINEAR) s = 0;
+        if (kind == DT_ROPE_WAVELENGTH) {
+            const double turns = original * f / pi2;   // within the original context
+            s = turns < low ? 0 : (turns > high ? 1 : (turns - low) / (high - low));
+        }
+        if (kind == DT_ROPE_YARN) {
+            const double t = (i - i_low) / (i_high - i_low);
+            s = 1 - (t < 0 ? 0 : (t > 1 ? 1 : t));
+        }
+        freqs[i] = (1 - s) * f / factor + s * f;
+    }
+    *scale = kind == DT_ROPE_YARN && factor > 1 ? (float)(0.1 * log(factor) + 1) : 1.0f;
+    return DT_OK;
+}
+
+extern "C" dt_status dt_kv_append(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_append_params* p) {
+    if (!p) return DT_ERR_INVALID_ARG;
+    dt_status st = check_cache(kv, true);
+    if (st != DT_OK) return st;
+    if ((st = check_chunk(chunk, true)) != DT_OK) return st;
+    if (p->layer < 0 || p->layer >= kv->layers || !isfinite(p->eps) || p->eps < 0 || !isfinite(p->rot_scale))
+        return DT_ERR_INVALID_ARG;
+    if (p->rot_dim < 0 || p->rot_dim > kv->D) return DT_ERR_INVALID_ARG;
+    if (p->rot_dim % 16 != 0) return DT_ERR_UNSUPPORTED;
+    if (p->rot_dim > 0 && (!p->freqs || misaligned(p->freqs, 8))) return DT_ERR_INVALID_ARG;
+    if ((p->q == nullptr) != (p->q_out == nullptr)) return DT_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)chunk->B * (chunk->lead + chunk->n_max);
+    if (p->q) {
+        if (p->Hq < 1) return DT_ERR_INVALID_ARG;
+        if (p->Hq > kMaxPassHeads) return DT_ERR_UNSUPPORTED;
+    }
+    if (misaligned(p->q_norm, 16) || misaligned(p->k_norm, 16)) return DT_ERR_INVALID_ARG;
+    if (chunk->B == 0) return DT_OK;
+    if (bad_rows(p->k, p->k_stride, rows, kv->Hkv, kv->D) || bad_rows(p->v, p->v_stride, rows, kv->Hkv, kv->D))
+        return DT_ERR_INVALID_ARG;
+    if (p->q && (bad_rows(p->q, p->q_stride, rows, p->Hq, kv->D) ||
+                 bad_rows(p->q_out, p->q_out_stride, rows, p->Hq, kv->D) ||
+                 (rows > 1 && p->q == p->q_out && p->q_stride != p->q_out_stride)))
+        return DT_ERR_INVALID_ARG;
+    AppendArgs a{};
+    a.c = chunk_args(chunk);
+    a.kv = cache_args(kv, p->layer);
+    a.q = (const uint16_t*)p->q;
+    a.k = (const uint16_t*)p->k;
+    a.v = (const uint16_t*)p->v;
+    a.q_out = (uint16_t*)p->q_out;
+    a.q_stride = p->q_stride;
+    a.k_stride = p->k_stride;
+    a.v_stride = p->v_stride;
+    a.q_out_stride = p->q_out_stride;
+    a.Hq = p->q ? p->Hq : 0;
+    a.q_norm = (const uint16_t*)p->q_norm;
+    a.k_norm = (const uint16_t*)p->k_norm;
+    a.eps = p->eps;
+    a.rot_scale = p->rot_scale;
+    a.freqs = p->freqs;
+    a.rot_dim = p->rot_dim;
+    a.interleaved = p->interleaved != 0;
+    const DeviceScope scope((hipStream_t)p->stream);
+    if (!scope.ok() || launch_append(a, kv->dtype, (hipStream_t)p->stream) != hipSuccess) return DT_ERR_HIP;
+    return DT_OK;
+}
+
+extern "C" size_t dt_attention_workspace(const dt_kv_cache* kv, const dt_chunk* chunk, int32_t Hq) {
+    if (check_attention_shape(kv, chunk, Hq) != DT_OK) return 0;
+    return attention_workspace(chunk_args(chunk), kv->Hkv, Hq, kv->D);
+}
+
+extern "C" dt_status dt_tree_attention(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_attention_params* p) {
+    if (!p) return DT_ERR_INVALID_ARG;
+    dt_status st = check_attention_shape(kv, chunk, p->Hq);
+    if (st != DT_OK) return st;
+    if ((st = check_cache(kv, true)) != DT_OK) return st;
+    if ((st = check_chunk(chunk, true)) != DT_OK) return st;
+    if (p->layer < 0 || p->layer >= kv->layers || !isfinite(p->scale) || !(p->scale > 0)) return DT_ERR_INVALID_ARG;
+    if (misaligned(p->lse, 4)) return DT_ERR_INVALID_ARG;
+    if (chunk->B == 0) return DT_OK;
+    const int64_t rows = (int64_t)chunk->B * (chunk->lead + chunk->n_max);
+    if (bad_rows(p->q, p->q_stride, rows, p->Hq, kv->D) || bad_rows(p->out, p->out_stride, rows, p->Hq, kv->D) ||
+        p->q == p->out)
+        return DT_ERR_INVALID_ARG;
+    AttentionArgs a{};
+    a.c = chunk_args(chunk);
+    a.kv = cache_args(kv, p->layer);
+    const size_t need = attention_workspace(a.c, kv->Hkv, p->Hq, kv->D);
+    if (need > 0 && (!p->workspace || misaligned(p->workspace, 16) || p->workspace_bytes < need))
+        return DT_ERR_WORKSPACE;
+    a.q = (const uint16_t*)p->q;
+    a.out = (uint16_t*)p->out;
+    a.q_stride = p->q_stride;
+    a.out_stride = p->out_stride;
+    a.Hq = p->Hq;
+    a.G = p->Hq / kv->Hkv;
+    a.scale_log2 = (float)(p->scale * 1.4426950408889634074);
+    a.lse = p->lse;
+    const DeviceScope scope((hipStream_t)p->stream);
+    if (!scope.ok() || launch_attention(a, kv->dtype, p->workspace, (hipStream_t)p->stream) != hipSuccess)
+        return DT_ERR_HIP;
+    return DT_OK;
+}
+
+extern "C" dt_status dt_process_logits(const dt_logits_params* p) {
+    if (!p || p->B < 0 || p->lead < 0 || p->n_max < 0 || p->V < 1) return DT_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)p->lead + p->n_max;
+    if (rows < 1 || p->history_max < 0 || p->n_bias < 0) return DT_ERR_INVALID_ARG;
+    if (p->dtype != DT_DTYPE_F32 && p->dtype != DT_DTYPE_BF16) return DT_ERR_INVALID_ARG;
+    if (p->B > 65535 || rows > kMaxChunkRows || p->V >= kMaxV || p->n_bias > 65534) return DT_ERR_UNSUPPORTED;
+    if (p->history && !p->history_len) return DT_ERR_INVALID_ARG;
+    if (p->node_tokens && !p->node_mask) return DT_ERR_INVALID_ARG;
+    if (p->bias_ids && !p->bias) return DT_ERR_INVALID_ARG;
+    if (p->allow && p->allow_rows < 1) return DT_ERR_INVALID_ARG;
+    if (p->allow && !p->allow_index && p->allow_rows < p->B * rows) return DT_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)p->n_nodes, (const void*)p->history, (const void*)p->history_len,
+                          (const void*)p->prompt_len, (const void*)p->node_tokens, (const void*)p->node_mask,
+                          (const void*)p->repetition, (const void*)p->frequency, (const void*)p->presence,
+                          (const void*)p->bias_ids, (const void*)p->bias, (const void*)p->allow,
+                          (const void*)p->allow_index})
+        if (misaligned(q, 4)) return DT_ERR_INVALID_ARG;
+    if (p->B == 0) return DT_OK;
+    if (!p->logits || !p->out || misaligned(p->logits, 16) || misaligned(p->out, 16)) return DT_ERR_INVALID_ARG;
+    LogitsArgs a{};
+    a.logits = p->logits;
+    a.out = p->out;
+    a.B = p->B;
+    a.lead = p->lead;
+    a.n_max = p->n_max;
+    a.rows = (int)rows;
+    a.V = p->V;
+    a.mask_words = (p->n_max + 31) / 32;
+    a.n_nodes = p->n_nodes;
+    a.history = p->history_max > 0 ? p->history : nullptr;
+    a.history_max = p->history_max;
+    a.history_len = p->history_len;
+    a.prompt_len = p->prompt_len;
+    a.node_tokens = p->n_max > 0 ? p->node_tokens : nullptr;
+    a.node_mask = p->node_mask;
+    a.repetition = p->repetition;
+    a.frequency = p->frequency;
+    a.presence = p->presence;
+    a.bias_ids = p->bias_ids;
+    a.bias = p->bias;
+    a.n_bias = p->bias_ids ? p->n_bias : 0;
+    a.allow = p->allow;
+    a.allow_index = p->allow_index;
+    a.allow_rows = p->allow_rows;
+    const DeviceScope scope((hipStream_t)p->stream);
+    if (!scope.ok() || launch_logits(a, p->dtype, (hipStream_t)p->stream) != hipSuccess) return DT_ERR_HIP;
+    return DT_OK;
+}
+
+extern "C" dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_commit_params* p) {
+    if (!p) return DT_ERR_INVALID_ARG;
+    dt_status st;
+    if (kv && (st = check_cache(kv, true)) != DT_OK) return st;
+    if ((st = check_chunk(chunk, true)) != DT_OK) return st;
+    if (chunk->lead < 1 || p->L < 1) return DT_ERR_INVALID_ARG;
+    if (chunk->n_max > kMaxCommitNodes) return DT_ERR_UNSUPPORTED;
+    if (chunk->B == 0) return DT_OK;
+    if (!p->target || !p->accepted || !p->lengths || (chunk->n_max > 0 && (!p->tokens || !p->parents)))
+        return DT_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)p->tokens, (const void*)p->parents, (const void*)p->target,
+                          (const void*)p->accepted, (const void*)p->lengths, (const void*)p->nodes})
+        if (misaligned(q, 4)) return DT_ERR_INVALID_ARG;
+    CommitArgs a{};
+    a.c = chunk_args(chunk);
+    if (kv) {
+        a.kv = cache_args(kv, 0);
+        a.layer_stride = kv->layers > 1 ? kv->layer_stride : 0;
+        a.layers = kv->layers;
+    }
+    a.tokens = p->tokens;
+    a.parents = p->parents;
+    a.target = p->target;
+    a.L = p->L;
+    a.accepted = p->accepted;
+    a.lengths = p->lengths;
+    a.nodes = p->nodes;
+    const DeviceScope scope((hipStream_t)p->stream);
+    if (!scope.ok() || launch_commit(a, (hipStream_t)p->stream) != hipSuccess) return DT_ERR_HIP;
     return DT_OK;
 }

@@ -110,7 +110,8 @@ typedef enum dt_status {
     DT_ERR_HIP = 4            /* the HIP runtime refused a launch */
 } dt_status;
 
-typedef enum dt_dtype { DT_DTYPE_F32 = 0, DT_DTYPE_BF16 = 1 } dt_dtype;
+/* F16 is a type of the verification pass's heads (dt_kv_cache) only. */
+typedef enum dt_dtype { DT_DTYPE_F32 = 0, DT_DTYPE_BF16 = 1, DT_DTYPE_F16 = 2 } dt_dtype;
 
 typedef enum dt_mode {
     DT_MODE_DART = 0,      /* score = cumulative draft log-probability */
@@ -288,6 +289,230 @@ dt_status dt_ngram_update(const dt_ngram_table* table, const int32_t* ctx, const
  *   DT_ERR_UNSUPPORTED for budget > 1024; DT_ERR_HIP if the launch fails. */
 dt_status dt_verify_length(const dt_tree_out* tree, int32_t B, int32_t budget, double cost_fixed,
                            double cost_per_token, int32_t* n_verify, int32_t* rank, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The target's verification pass over the built trees: the operators between
+ * a tree and the accepted tokens.  With the model's own products between
+ * them, one layer is dt_kv_append, then dt_tree_attention; after the last
+ * layer dt_process_logits, dt_position_topk with k = 1 (the target's choice
+ * for every row) and dt_commit_path, whose outputs dt_ngram_update takes.
+ *
+ * A batch's new tokens are a CHUNK of `lead + n_max` rows a request: `lead`
+ * committed tokens whose keys and values are not in the cache yet (the last
+ * of them is the tree's root), then up to n_max tree nodes in the order of
+ * dt_build_tree, of which the first n_nodes[b] count.  lead = 1, n_max = 0
+ * is a step of plain decoding; lead = 0 with mask = NULL is a (ragged) piece
+ * of a prompt.  Row r of request b is position and cache slot
+ * ctx_len[b] + r; a node's POSITION is that of the root plus its depth.
+ * Rows at or behind lead + n_nodes[b] are neither read nor written, in any
+ * buffer.
+ *
+ * These entry points launch on the device of `stream` (the current device
+ * for the null stream), whichever device is current.
+ * ------------------------------------------------------------------------ */
+
+/* A paged cache of keys and values.  Element d of head h of the token in
+ * slot s of request b in layer l lies at
+ *   k + l * layer_stride + page * page_stride + (s % page_size) * slot_stride
+ *     + h * head_stride + d,      page = page_table[b * max_pages + s / page_size]
+ * and likewise for v.  Strides count elements and are multiples of 8 and not
+ * negative (the stride of an axis of length one is not read); k and v are
+ * 16-byte aligned.  Tokens whose page lies outside [0, num_pages), or whose
+ * slot lies behind the table (max_pages * page_size), are dropped on writing
+ * and unseen on reading.  Two tokens written in one call must not share a
+ * slot; pages that are only read may be shared by requests. */
+typedef struct dt_kv_cache {
+    void* k;
+    void* v;
+    const int32_t* page_table; /* device [B][max_pages] */
+    int64_t layer_stride;
+    int64_t page_stride;
+    int64_t slot_stride;
+    int64_t head_stride;
+    int32_t layers;            /* >= 1 */
+    int32_t num_pages;         /* >= 1 */
+    int32_t page_size;         /* >= 1; max_pages * page_size <= 2^30 */
+    int32_t max_pages;         /* >= 1 */
+    int32_t Hkv;               /* key heads, 1 <= Hkv <= 4096 */
+    int32_t D;                 /* elements of a head: 64, 128 or 256 */
+    int32_t dtype;             /* DT_DTYPE_BF16 or DT_DTYPE_F16 */
+} dt_kv_cache;
+
+/* The new tokens of a batch (see above); every array is on the device. */
+typedef struct dt_chunk {
+    int32_t B;                 /* requests, 0 <= B <= 65535 */
+    int32_t lead;              /* >= 0 */
+    int32_t n_max;             /* >= 0; 1 <= lead + n_max <= 65536 */
+    const int32_t* ctx_len;    /* [B] tokens in the cache; < 0: the request has no rows */
+    const int32_t* n_nodes;    /* [B], clamped to 0..n_max; NULL = n_max for all */
+    const uint32_t* mask;      /* [B][n_max][ceil(n_max/32)] as dt_tree_out; NULL = every row sees
+                                  all slots up to its own */
+    const int32_t* depths;     /* [B][n_max] as dt_tree_out; NULL = a row's position is its slot */
+} dt_chunk;
+
+/* Frequencies of the rotary positions, on the HOST: freqs[i], 0 <= i <
+ * rot_dim / 2, is the angle in radians by which pair i turns from one
+ * position to the next, and *scale the factor of dt_append_params.rot_scale.
+ *   NONE        f_i = base^(-2i / rot_dim), scale 1;
+ *   LINEAR      f_i / factor, scale 1;
+ *   WAVELENGTH  with l = 2 pi / f_i: f_i / factor where l > original / low,
+ *               f_i where l < original / high, else (1 - s) f_i / factor +
+ *               s f_i, s = (original / l - low) / (high - low); scale 1;
+ *   YARN        i_low = floor(c(high)), i_high = ceil(c(low)), both clamped
+ *               to 0..rot_dim - 1, with c(n) = rot_dim
+ *               ln(original / (2 pi n)) / (2 ln base); s = 1 - clamp((i -
+ *               i_low) / (i_high - i_low), 0, 1) (a difference of zero counts
+ *               as 0.001) in the blend above; scale 0.1 ln(factor) + 1 (1 for
+ *               factor <= 1).
+ * Errors: DT_ERR_INVALID_ARG for null pointers, rot_dim odd or < 2, base not
+ *   finite or <= 1, factor not finite or <= 0, an unknown kind; for WAVELENGTH
+ *   and YARN also unless 0 < low < high and original > 0, all finite. */
+typedef enum dt_rope_kind {
+    DT_ROPE_NONE = 0,
+    DT_ROPE_LINEAR = 1,
+    DT_ROPE_WAVELENGTH = 2,
+    DT_ROPE_YARN = 3
+} dt_rope_kind;
+dt_status dt_rope_frequencies(int32_t kind, int32_t rot_dim, double base, double factor, double low,
+                              double high, double original, double* freqs, float* scale);
+
+typedef struct dt_append_params {
+    const void* q;             /* [B][lead + n_max] rows of Hq heads of D, or NULL (keys and values only) */
+    const void* k;             /* ... rows of Hkv heads */
+    const void* v;
+    void* q_out;               /* as q; may be q itself with the same row stride; NULL iff q is */
+    int64_t q_stride;          /* elements from row to row; the heads of a row are contiguous */
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t q_out_stride;
+    int32_t Hq;                /* query heads, 1..4096 (not read when q is NULL) */
+    const void* q_norm;        /* [D] weights of dtype, or NULL = no norm */
+    const void* k_norm;
+    float eps;                 /* >= 0 */
+    const double* freqs;       /* device [rot_dim / 2] radians a position */
+    int32_t rot_dim;           /* the first rot_dim elements of a head turn: 0..D, a multiple of 16 */
+    int32_t interleaved;       /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+    float rot_scale;           /* factor of the turned elements (1 without scaling) */
+    int32_t layer;             /* layer of the cache, 0 <= layer < layers */
+    void* stream;
+} dt_append_params;
+
+/* The new tokens' queries, keys and values on their way from the projection:
+ * for every row, y = x * rsqrt(mean(x^2) + eps) * w over each head of q (k)
+ * if q_norm (k_norm) is given, then pair i of the first rot_dim elements
+ * turned by position * freqs[i]: (a, b) -> rot_scale * (a cos - b sin,
+ * a sin + b cos); q goes to q_out, k and v (as it is) to their cache slots.
+ * All in fp32 (the angle in fp64, reduced before the sine), rounded once.
+ * Pointers 16-byte aligned, strides multiples of 8 and, in buffers of more
+ * than one row, at least a row's heads; eps finite.
+ * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above), DT_ERR_HIP. */
+dt_status dt_kv_append(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_append_params* p);
+
+typedef struct dt_attention_params {
+    const void* q;             /* [B][lead + n_max] rows of Hq heads of D */
+    void* out;                 /* as q, of the cache's dtype */
+    int64_t q_stride;          /* elements from row to row; the heads of a row are contiguous */
+    int64_t out_stride;
+    int32_t Hq;                /* query heads, a multiple of Hkv, 1..4096; head h reads key head h / (Hq / Hkv) */
+    float scale;               /* > 0, finite */
+    float* lse;                /* [B][lead + n_max][Hq] or NULL: log of the sum of exp(scale * q . k) */
+    int32_t layer;
+    void* workspace;           /* 16-byte aligned device scratch of dt_attention_workspace() bytes */
+    size_t workspace_bytes;
+    void* stream;
+} dt_attention_params;
+
+/* Attention of the chunk's rows over the paged cache, which already holds the
+ * chunk's own keys and values (dt_kv_append):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j   over the slots j a row sees:
+ *   - row r < lead, or any row when mask is NULL: j <= ctx_len + r;
+ *   - node i otherwise: j < ctx_len + lead, and ctx_len + lead + i' for every
+ *     i' < n_nodes whose bit is set in mask row i.
+ * Scores, the softmax and the sums are fp32; the weights are rounded to the
+ * cache's type for the second product, the result once.  A row that sees
+ * nothing gives zeros (lse -inf).  Whatever lies in slots that a row does not
+ * see, infinities and NaN included, does not reach it.
+ * q may not overlap out.  Pointers 16-byte aligned (lse 4), strides multiples
+ * of 8 and at least Hq * D.
+ * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above, or
+ *   B * (lead + n_max) * Hq >= 2^31), DT_ERR_WORKSPACE, DT_ERR_HIP. */
+dt_status dt_tree_attention(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_attention_params* p);
+
+/* Bytes of workspace dt_tree_attention needs (depends on kv's Hkv and D, on
+ * the chunk's B, lead and n_max and on Hq only); 0 if a call would be
+ * refused for these.  Its contents are meaningless between calls. */
+size_t dt_attention_workspace(const dt_kv_cache* kv, const dt_chunk* chunk, int32_t Hq);
+
+typedef struct dt_logits_params {
+    const void* logits;        /* device [B][lead + n_max][V] of dtype, 16-byte aligned */
+    void* out;                 /* as logits; may be logits itself */
+    int32_t B;                 /* 0 <= B <= 65535 */
+    int32_t lead;              /* >= 0 */
+    int32_t n_max;             /* >= 0; 1 <= lead + n_max <= 65536 */
+    int32_t V;                 /* 1 <= V < 2^26 */
+    int32_t dtype;             /* DT_DTYPE_F32 or DT_DTYPE_BF16 */
+    const int32_t* n_nodes;    /* [B], clamped to 0..n_max; NULL = n_max */
+    const int32_t* history;    /* [B][history_max] token ids, oldest first; NULL = none */
+    int32_t history_max;       /* >= 0 */
+    const int32_t* history_len;/* [B], clamped to 0..history_max; needed with history */
+    const int32_t* prompt_len; /* [B], clamped to 0..history_len; NULL = 0: the first of a
+                                  request's history are its prompt, the rest were generated */
+    const int32_t* node_tokens;/* [B][n_max] tokens of the tree's nodes, or NULL */
+    const uint32_t* node_mask; /* [B][n_max][ceil(n_max/32)] as dt_tree_out; needed with node_tokens */
+    const float* repetition;   /* [B] > 0, or NULL = 1 */
+    const float* frequency;    /* [B] or NULL = 0 */
+    const float* presence;     /* [B] or NULL = 0 */
+    const int32_t* bias_ids;   /* [B][n_bias] or NULL */
+    const float* bias;         /* [B][n_bias]; needed with bias_ids */
+    int32_t n_bias;            /* 0..65534 */
+    const uint32_t* allow;     /* [allow_rows][ceil(V/32)] bits of allowed tokens, LSB first, or NULL */
+    const int32_t* allow_index;/* [B][lead + n_max] row of allow; outside 0..allow_rows-1: unmasked.
+                                  NULL = row number b * (lead + n_max) + r */
+    int32_t allow_rows;        /* >= 1 with allow */
+    void* stream;
+} dt_logits_params;
+
+/* Logits as the sampler should see them; rows are those of a chunk (draft
+ * positions: lead = d, n_max = 0).  Token v of row r of request b, with
+ *   c    = how often v occurs among the generated tokens of the history and,
+ *          for the row of node i, among the nodes whose bit is set in
+ *          node_mask row i (its path; nodes at or behind n_nodes do not
+ *          count),
+ *   seen = c > 0, or v occurs in the prompt:
+ *   x = seen ? (x > 0 ? x / repetition : x * repetition) : x
+ *   x = x - (frequency * c + presence * [c > 0])
+ *   x = x + bias of v (an id listed more than once takes its last entry)
+ *   x = -inf where allow's bit of v is 0, whatever x was.
+ * In fp32, rounded once; values that no step touches are copied bit by bit.
+ * Ids outside [0, V) are skipped, rows behind the last node left as they
+ * were.  logits and out must be the same buffer or not overlap.
+ * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above), DT_ERR_HIP. */
+dt_status dt_process_logits(const dt_logits_params* p);
+
+typedef struct dt_commit_params {
+    const int32_t* tokens;     /* [B][n_max] as dt_tree_out */
+    const int32_t* parents;    /* [B][n_max] as dt_tree_out */
+    const int32_t* target;     /* [B][lead + n_max] the token the target chose after each row */
+    int32_t L;                 /* row length of the outputs, >= 1; at most L - 1 nodes are accepted */
+    int32_t* accepted;         /* [B][L] the accepted nodes' tokens, the target's next token, then -1 */
+    int32_t* lengths;          /* [B] accepted nodes + 1 */
+    int32_t* nodes;            /* [B][L] the accepted nodes' indexes, then -1; or NULL */
+    void* stream;
+} dt_commit_params;
+
+/* After verification: from the root down, the child (lowest index) whose
+ * token the target chose after its parent is accepted, until there is none.
+ * The accepted nodes' keys and values move, in every layer of the cache, from
+ * slot ctx_len + lead + node to slots ctx_len + lead + 0, 1, ..., so the
+ * cache holds ctx_len + lead + lengths - 1 committed tokens (the next call's
+ * ctx_len).  accepted and lengths are dt_ngram_update's tokens and lengths.
+ * The chunk's mask and depths are not used; a node whose parent's index is
+ * not below its own is never accepted.  A request with ctx_len < 0 gets
+ * lengths 0 and -1 everywhere, and nothing moves.  kv may be NULL (tokens
+ * only).  A request's own slots must lie in pages of its own.
+ * Errors: DT_ERR_INVALID_ARG (also lead < 1, L < 1), DT_ERR_UNSUPPORTED
+ *   (n_max > 1024, or a limit above), DT_ERR_HIP. */
+dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_commit_params* p);
 
 #ifdef __cplusplus
 }
