@@ -1,6 +1,31 @@
-// dt_tree_attention: softmax(scale * q k^T) v over a paged cache, one pass
-// over the keys with a running maximum m and sum l:
+// dt_tree_attention: softmax(scale * q k^T) v over a paged cache in one pass
+// over the keys, with a running maximum m, sum l and output o per query:
 //   m' = max(m, x);  l' = l e^(m - m') + e^(x - m');  o' = o e^(m - m') + e^(x - m') v
+//
+// Rows.  The G query heads of a key head share its keys, so the matrix rows
+// of a request and key head are (chunk row, head in group), G * rows of them;
+// a wave takes 32.  A workgroup is WM x WK waves: WM x 32 rows, and WK
+// groups of waves that take the tiles of KT keys in turn (few rows: the
+// waves share the keys out; many rows: they share the tiles).
+//
+// Products.  Scores are computed transposed, K q^T on 32x32x16 matrix
+// instructions, so that a lane holds one query and the tile's keys lie in its
+// registers: the softmax needs one exchange (the wave's two halves) a tile.
+// The weights then are, as they lie, the right operand of V^T p^T: the sum
+// over keys may run in any order, so the left operand is read in the order in
+// which the first product left the keys (k = 16 s + 8 j + 4 half + i).
+//
+// Staging.  K and V tiles go from memory to LDS without passing registers,
+// one tile ahead.  16-byte pieces of a row are permuted by the row's number
+// on the way (the copy's LDS side is fixed, so the memory side is permuted):
+// K by single pieces (a wave reads one piece of 32 rows at once), V by 64-byte
+// groups (the transposing read takes 64 bytes of 4 rows at once), which
+// spreads both over the 64 banks.
+//
+// Work.  Each workgroup derives the whole split from the lengths: segments
+// (request, key head, row tile) times tiles, cut into chunks of equal size so
+// that about `slots` workgroups share the work however ragged the batch is.
+// A segment in one chunk is written at once, others by combine_kernel.
 #include <math.h>
 
 #include "pass.h"
@@ -8,68 +33,630 @@
 namespace dt {
 namespace {
 
-// One wave per row and query head; a lane holds D / 64 elements of it.
-template <class T, int D>
-__global__ void __launch_bounds__(64) attention_simple(AttentionArgs a) {
-    constexpr int E = D / 64;
-    const int lane = threadIdx.x;
-    const int h = blockIdx.x % a.Hq;
-    const int64_t row = blockIdx.x / a.Hq;
-    const int b = (int)(row / a.c.rows), r = (int)(row - (int64_t)b * a.c.rows);
-    const int nn = chunk_nodes(a.c, b);
-    if (nn < 0 || r >= a.c.lead + nn) return;
-    const int64_t ctx = a.c.ctx_len[b];
-    const bool node = a.c.mask && r >= a.c.lead;
-    const uint32_t* mask = node ? a.c.mask + ((int64_t)b * a.c.n_max + r - a.c.lead) * a.c.mask_words : nullptr;
-    int64_t keys = ctx + (node ? a.c.lead + nn : r + 1);
-    keys = keys < a.kv.cap ? keys : a.kv.cap;
-    float q[E], o[E] = {}, m = -INFINITY, l = 0;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+typedef uint64_t u64;
+
+constexpr int kUnit = 64;          // keys of the split's unit of work
+constexpr int kMinUnits = 4;       // a chunk has at least 256 keys
+constexpr int kRowsPerWave = 32;
+constexpr float kLazy = 8.0f;      // log2 of the largest weight before the sums are rescaled
+
+__device__ inline f32x16 mfma(Bf16, s16x8 a, s16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
+}
+__device__ inline f32x16 mfma(F16, s16x8 a, s16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h16x8, a), __builtin_bit_cast(h16x8, b), c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// the split
+// ---------------------------------------------------------------------------
+
+struct Request {
+    int rows, mtiles, units;       // live chunk rows, row tiles, key units
+    int keys;
+};
+
+__device__ inline Request request_of(const AttentionArgs& a, int b, int mt_rows) {
+    Request q{};
+    const int nn = b < a.c.B ? chunk_nodes(a.c, b) : -1;
+    if (nn < 0) return q;
+    q.rows = a.c.lead + nn;
+    const int64_t keys = (int64_t)a.c.ctx_len[b] + q.rows;
+    q.keys = (int)(keys < a.kv.cap ? keys : a.kv.cap);
+    q.mtiles = (q.rows * a.G + mt_rows - 1) / mt_rows;
+    q.units = (q.keys + kUnit - 1) / kUnit;
+    return q;
+}
+
+template <class V>
+__device__ inline V wave_sum(V x) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = T::get(a.q[row * a.q_stride + (int64_t)h * D + lane + 64 * e]);
-    for (int64_t j = 0; j < keys; ++j) {
-        const int64_t i = j - ctx - a.c.lead;
-        if (node && i >= 0 && !(mask[i >> 5] >> (i & 31) & 1)) continue;
-        const int64_t at = slot_offset(a.kv, b, j);
-        if (at < 0) continue;
-        const uint16_t* k = a.kv.k + at + (h / a.G) * a.kv.head_stride;
-        const uint16_t* v = a.kv.v + at + (h / a.G) * a.kv.head_stride;
-        float x = 0;
+    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+    return x;
+}
+
+__device__ inline int wave_prefix(int x, int lane) {      // inclusive
 #pragma unroll
-        for (int e = 0; e < E; ++e) x += q[e] * T::get(k[lane + 64 * e]);
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) x += __shfl_xor(x, s);
-        x *= a.scale_log2;
-        const float top = fmaxf(m, x);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float w = exp2f(m - base), p = exp2f(x - base);
-        m = top;
-        l = l * w + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * w + p * T::get(v[lane + 64 * e]);
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(x, o);
+        if (lane >= o) x += y;
     }
+    return x;
+}
+
+__device__ inline int64_t uniform(int64_t x) {
+    return (int64_t)((u64)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) |
+                     (u64)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32);
+}
+
+// Units of a chunk: the same on every wave of every workgroup of a call.
+__device__ inline int chunk_units(const AttentionArgs& a, int mt_rows, int slots, int lane, int* jobs) {
+    int64_t work = 0;
+    int segs = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += 64) {
+        const Request q = request_of(a, b0 + lane, mt_rows);
+        segs += q.mtiles * a.kv.Hkv;
+        work += (int64_t)q.mtiles * a.kv.Hkv * q.units;
+    }
+    segs = wave_sum(segs);
+    work = wave_sum(work);
+    // rounding adds at most one chunk a segment
+    const int64_t room = slots - segs > slots / 4 ? slots - segs : slots / 4;
+    int64_t c = (work + room - 1) / room;
+    if (c < kMinUnits) c = kMinUnits;
+    if (c > kMaxSlots) c = kMaxSlots;
+    int n = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += 64) {
+        const Request q = request_of(a, b0 + lane, mt_rows);
+        n += q.mtiles * a.kv.Hkv * (int)((q.units + c - 1) / c);
+    }
+    *jobs = wave_sum(n);
+    return (int)c;
+}
+
+// Chunks of a request in all, and of one whose segments are split (those have
+// partial results: a segment of more than c units has at most 2 units / c
+// chunks, so there are at most 2 work / c <= 2 room <= 2 slots of them).
+__device__ inline int chunks_of(const AttentionArgs& a, const Request& q, int c, int* split) {
+    const int per = (q.units + c - 1) / c, n = q.mtiles * a.kv.Hkv * per;
+    *split = per > 1 ? n : 0;
+    return n;
+}
+
+struct Job {
+    int b, head, mt, split, splits, slot;   // slot: of its partial result
+    Request q;
+};
+
+// Job `idx` of the call; the row tiles of a segment's chunk are neighbours.
+__device__ inline Job job_of(const AttentionArgs& a, int mt_rows, int c, int idx, int lane) {
+    Job j{};
+    int before = 0, slots_before = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += 64) {
+        const Request q = request_of(a, b0 + lane, mt_rows);
+        int ns;
+        const int n = chunks_of(a, q, c, &ns);
+        const int upto = wave_prefix(n, lane);
+        const u64 hit = __ballot(before + upto > idx);
+        if (hit) {
+            const int at = __builtin_ctzll(hit);
+            const int local = idx - before - (__shfl(upto, at) - __shfl(n, at));
+            j.b = __builtin_amdgcn_readfirstlane(b0 + at);
+            j.q.rows = __builtin_amdgcn_readfirstlane(__shfl(q.rows, at));
+            j.q.keys = __builtin_amdgcn_readfirstlane(__shfl(q.keys, at));
+            j.q.mtiles = __builtin_amdgcn_readfirstlane(__shfl(q.mtiles, at));
+            j.q.units = __builtin_amdgcn_readfirstlane(__shfl(q.units, at));
+            j.splits = (j.q.units + c - 1) / c;
+            j.mt = __builtin_amdgcn_readfirstlane(local) % j.q.mtiles;
+            const int rest = __builtin_amdgcn_readfirstlane(local) / j.q.mtiles;
+            j.split = rest % j.splits;
+            j.head = rest / j.splits;
+            j.slot = slots_before + __builtin_amdgcn_readfirstlane(wave_sum(lane < at ? ns : 0)) +
+                     __builtin_amdgcn_readfirstlane(local);
+            return j;
+        }
+        before += __shfl(upto, 63);
+        slots_before += wave_sum(ns);
+    }
+    j.b = -1;
+    return j;
+}
+
+// ---------------------------------------------------------------------------
+// the tile loop
+// ---------------------------------------------------------------------------
+
+template <class T>
+__device__ inline bool odd_value(uint32_t pair) {          // an infinity or NaN in either half
+    constexpr uint32_t e = T::kExponent;
+    return (pair & e) == e || (pair & (e << 16)) == (e << 16);
+}
+
+// 16 bytes a lane from memory to LDS at `to` + 16 * lane; the wait is the
+// caller's: wait_copies() ends when every copy of the wave has arrived and
+// every LDS read it issued before has its data, so that the next copies may
+// overwrite what was read.
+__device__ inline void copy_to_lds(const uint16_t* from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "m0");
+}
+__device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+template <int D>
+__device__ inline int swizzle_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
+template <int D>
+__device__ inline int swizzle_v(int row) { return D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2; }
+
+template <class T, int D, int WM, int WK, int KT>
+struct Shape {
+    static constexpr int kThreads = 64 * WM * WK;
+    static constexpr int kMt = WM * kRowsPerWave;
+    static constexpr int kTile = KT * D * 2;               // bytes of a K or V tile
+    static constexpr int kLds = 2 * 2 * kTile * WK;        // two buffers of K and V a key group
+    static constexpr int kPartial = kMt * (D + 2);         // floats of a split's partial result
+};
+
+template <class T, int D, int WM, int WK, int KT, int PER_CU>
+__global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
+    attention_kernel(AttentionArgs a, int slots, float* partial) {
+    using S = Shape<T, D, WM, WK, KT>;
+    constexpr int NB = KT / 32, KS = D / 16, ND = D / 32;
+    constexpr int kUnits16 = D / 8;                        // 16-byte pieces of a head
+    constexpr int kRpi = 64 / kUnits16;                    // rows of a wave's copy instruction
+    constexpr int kCopies = KT / kRpi / WM;                // copies of K (and of V) a wave and tile
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wk = wave / WM;
+    const int half = lane >> 5, col = lane & 31;
+
+    int jobs;
+    const int c = chunk_units(a, S::kMt, slots, lane, &jobs);
+    // neighbours in the job order share keys: give them to one XCD (workgroups go round over the 8)
+    const int per = (jobs + 7) >> 3;
+    const int idx = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || idx >= jobs) return;
+    const Job job = job_of(a, S::kMt, c, idx, lane);
+    const int b = job.b;
+    const int ctx = a.c.ctx_len[b], lead = a.c.lead, nn = job.q.rows - lead;
+    const int mrows = job.q.rows * a.G;
+
+    // this lane's query
+    const int m0 = job.mt * S::kMt + wm * kRowsPerWave;
+    const int mrow = m0 + col;
+    const bool live = mrow < mrows;
+    const int r = live ? mrow / a.G : 0, g = live ? mrow - r * a.G : 0;
+    const int64_t row = (int64_t)b * a.c.rows + r;
+    const int h = job.head * a.G + g;
+    const bool node = a.c.mask && r >= lead;
+    const uint32_t* mask = node ? a.c.mask + ((int64_t)b * a.c.n_max + r - lead) * a.c.mask_words : nullptr;
+    s16x8 qf[KS];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        a.out[row * a.out_stride + (int64_t)h * D + lane + 64 * e] = T::put(l == 0 ? 0.0f : o[e] / l);
-    if (a.lse && lane == 0) a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    for (int s = 0; s < KS; ++s)
+        qf[s] = *(const s16x8*)(a.q + row * a.q_stride + (int64_t)h * D + 16 * s + 8 * half);
+
+    // keys below `all` are seen by every query of the wave, keys at or behind
+    // `any` by none (64 bits: ctx_len may be anything an int32 holds)
+    int64_t all = live ? (int64_t)ctx + (node ? lead : r + 1) : INT64_MAX;
+    int64_t any = live ? (int64_t)ctx + (node ? lead + nn : r + 1) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_xor(all, o), y = __shfl_xor(any, o);
+        all = x < all ? x : all;
+        any = y > any ? y : any;
+    }
+    all = uniform(all);
+    any = uniform(any);
+    const bool work = m0 < mrows;
+    const int64_t limit = (int64_t)ctx + r + 1;            // causal rows: first unseen key
+    const int64_t first_node = (int64_t)ctx + lead;        // slot of node 0
+
+    // the chunk's tiles, shortened to what the workgroup's rows see
+    int last_row = ((job.mt + 1) * S::kMt - 1) / a.G;
+    if (last_row > job.q.rows - 1) last_row = job.q.rows - 1;
+    int64_t end = (int64_t)ctx + (a.c.mask && last_row >= lead ? job.q.rows : last_row + 1);
+    if (end > job.q.keys) end = job.q.keys;
+    const int64_t stop = (int64_t)(job.split + 1) * c * kUnit;
+    const int k_first = job.split * c * kUnit;
+    const int k_end = (int)(end < stop ? end : stop);
+    const int tiles = k_end > k_first ? (k_end - k_first + KT - 1) / KT : 0;
+
+    const uint16_t* kbase = a.kv.k + job.head * a.kv.head_stride;
+    const uint16_t* vbase = a.kv.v + job.head * a.kv.head_stride;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
+    const uint32_t group = lds0 + wk * 4 * S::kTile;       // K, V of buffer 0, K, V of buffer 1
+
+    // lane l looks up key l of a tile
+    const int32_t* table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
+    int next_page = -1, next_in = 0;
+    const auto look_up = [&](int t) {                      // of the group's tile t
+        const int key = k_first + t * KT + (lane & (KT - 1));
+        next_page = -1;
+        if (t < tiles && key < k_end) {
+            const int i = a.kv.page_shift >= 0 ? key >> a.kv.page_shift : key / a.kv.page_size;
+            next_page = table[i];
+            next_in = key - i * a.kv.page_size;
+        }
+    };
+    u64 valid_next = 0;
+    const auto issue = [&](int buf) {                      // the tile looked up last
+        const bool ok = next_page >= 0 && next_page < a.kv.num_pages;
+        // a key that is not there: some mapped address, its score and value are dropped below
+        const int64_t off = ok ? next_page * a.kv.page_stride + next_in * a.kv.slot_stride : 0;
+        valid_next = __ballot(ok);
+        const int lo = (int)off, hi = (int)(off >> 32);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int at = wm * kCopies + i;
+            const int trow = at * kRpi + lane / kUnits16, piece = lane % kUnits16;
+            const int64_t o = (int64_t)((u64)(uint32_t)__shfl(lo, trow) | (u64)(uint32_t)__shfl(hi, trow) << 32);
+            const uint32_t to = group + buf * 2 * S::kTile + at * 1024;
+            copy_to_lds(kbase + o + (piece ^ swizzle_k<D>(trow)) * 8, to);
+            copy_to_lds(vbase + o + (piece ^ swizzle_v<D>(trow)) * 8, to + S::kTile);
+        }
+    };
+
+    // LDS addresses of this lane's pieces
+    int kaddr[KS], vaddr[ND];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) kaddr[s] = col * D * 2 + ((2 * s + half) ^ swizzle_k<D>(col)) * 16;
+    const int vrow = 4 * half + ((lane >> 2) & 3);
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+        vaddr[d] = vrow * D * 2 + (((d * 4) ^ swizzle_v<D>(vrow)) * 16) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    char* const my = lds + wk * 4 * S::kTile;
+
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = f32x16{};
+    float m = -INFINITY, l = 0;                            // m in units of log2; l of this lane's keys
+
+    look_up(wk);
+    if (wk < tiles) issue(0);
+    u64 valid = valid_next;
+    look_up(wk + WK);
+    const int rounds = (tiles + WK - 1) / WK;
+    for (int i = 0; i < rounds; ++i) {
+        const int t = wk + i * WK;
+        wait_copies();
+        if constexpr (WM > 1) __syncthreads();
+        u64 now = valid;
+        if (t + WK < tiles) {
+            issue((i + 1) & 1);
+            valid = valid_next;
+            look_up(t + 2 * WK);
+        }
+        const int k0 = k_first + t * KT;
+        if (!work || t >= tiles || k0 >= any) continue;
+        char* const kt = my + (i & 1) * 2 * S::kTile;
+        char* const vt = kt + S::kTile;
+
+        f32x16 s[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            s[n] = f32x16{};
+#pragma unroll
+            for (int x = 0; x < KS; ++x)
+                s[n] = mfma(T(), *(const s16x8*)(kt + kaddr[x] + n * 32 * D * 2), qf[x], s[n]);
+        }
+        uint32_t see[NB];
+        const u64 full = KT == 64 ? ~0ull : 0xFFFFFFFFull;
+        const bool masked = k0 + KT > all || (now & full) != full;
+        if (masked) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const int64_t kk = k0 + 32 * n;
+                uint32_t w;
+                if (!node) {
+                    const int64_t left = limit - kk;
+                    w = left <= 0 ? 0u : (left >= 32 ? ~0u : (1u << left) - 1);
+                } else {
+                    const int64_t off = kk - first_node;
+                    if (off <= -32) {
+                        w = ~0u;
+                    } else {
+                        const int64_t from = off < 0 ? 0 : off;
+                        const int at = (int)(from >> 5), sh = (int)(from & 31);
+                        const uint32_t w0 = at < a.c.mask_words ? mask[at] : 0u;
+                        const uint32_t w1 = at + 1 < a.c.mask_words ? mask[at + 1] : 0u;
+                        w = (uint32_t)(((u64)w1 << 32 | w0) >> sh);
+                        const int64_t left = nn - from;
+                        w = left <= 0 ? 0u : (left >= 32 ? w : w & ((1u << left) - 1));
+                        if (off < 0) w = w << -off | ((1u << -off) - 1);
+                    }
+                }
+                w &= (uint32_t)(now >> (32 * n));
+                see[n] = w >> (4 * half);
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    if (!(see[n] >> (8 * (x >> 2) + (x & 3)) & 1)) s[n][x] = -INFINITY;
+            }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) top = fmaxf(top, s[n][x]);
+        top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
+        // The sums are kept relative to an m that may lag the maximum by
+        // kLazy: weights stay below 2^8, exact in relative terms for both
+        // types, and most tiles leave o alone.
+        if (__any(top > m + kLazy)) {
+            const float mm = fmaxf(m, top);
+            const float w = mm == -INFINITY ? 1.0f : exp2f(m - mm);
+            m = mm;
+            l *= w;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[d][x] *= w;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        s16x8 p[NB * 2];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][x], a.scale_log2, -base));
+                l += e;
+                p[2 * n + (x >> 3)][x & 7] = (short)T::put(e);
+            }
+        const auto value = [&](int d, int x) {
+            typedef __attribute__((address_space(3))) s16x4 lds4;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x) * D * 2));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x + 8) * D * 2));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+        bool odd = false;
+        if (masked) {
+            // An unseen key's weight is 0, but 0 times an infinity or NaN is
+            // not: tiles with such values take the careful way.
+#pragma unroll 1
+            for (int x = 0; x < S::kTile; x += 1024) {
+                const u32x4 v = *(const u32x4*)(vt + x + lane * 16);
+                odd |= odd_value<T>(v[0]) || odd_value<T>(v[1]) || odd_value<T>(v[2]) || odd_value<T>(v[3]);
+            }
+            odd = __any(odd);
+        }
+        if (!odd) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int x = 0; x < NB * 2; ++x) o[d] = mfma(T(), value(d, x), p[x], o[d]);
+        } else {
+            // The finite values are summed as always; whether a query sees
+            // an infinity (NaN: of both signs) is counted by two more
+            // products of truth values.
+            s16x8 seen[NB * 2];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    seen[2 * n + (x >> 3)][x & 7] = (see[n] >> (8 * (x >> 2) + (x & 3)) & 1) ? (short)T::kOne : (short)0;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                f32x16 up = {}, down = {};
+#pragma unroll
+                for (int x = 0; x < NB * 2; ++x) {
+                    s16x8 v = value(d, x), pos, neg;
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const uint32_t bits = (uint16_t)v[y];
+                        const bool special = (bits & T::kExponent) == T::kExponent;
+                        const bool nan = special && (bits & T::kFraction) != 0;
+                        pos[y] = special && (nan || !(bits >> 15)) ? (short)T::kOne : (short)0;
+                        neg[y] = special && (nan || (bits >> 15)) ? (short)T::kOne : (short)0;
+                        if (special) v[y] = 0;
+                    }
+                    o[d] = mfma(T(), v, p[x], o[d]);
+                    up = mfma(T(), pos, seen[x], up);
+                    down = mfma(T(), neg, seen[x], down);
+                    __builtin_amdgcn_sched_barrier(0);     // a rare path: registers before speed
+                }
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    if (up[x] > 0) o[d][x] += INFINITY;
+                    if (down[x] > 0) o[d][x] -= INFINITY;
+                }
+            }
+        }
+    }
+    l += __shfl_xor(l, 32);
+
+    if constexpr (WK > 1) {
+        // the key groups' results meet in LDS; group 0 goes on with the sum
+        __syncthreads();
+        float* const box = (float*)lds;                    // [WK][WM][64 lanes][16 ND + 2], a lane's own slots
+        constexpr int kSlot = 64;
+        const auto at = [&](int k, int x) -> float& { return box[((k * WM + wm) * (16 * ND + 2) + x) * kSlot + lane]; };
+        if (wk > 0) {
+            at(wk - 1, 0) = m;
+            at(wk - 1, 1) = l;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) at(wk - 1, 2 + d * 16 + x) = o[d][x];
+        }
+        __syncthreads();
+        if (wk > 0) return;
+        float mm = m;
+#pragma unroll
+        for (int k = 0; k < WK - 1; ++k) mm = fmaxf(mm, at(k, 0));
+        const float base = mm == -INFINITY ? 0.0f : mm;
+        float w = exp2f(m - base);
+        l *= w;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[d][x] *= w;
+#pragma unroll
+        for (int k = 0; k < WK - 1; ++k) {
+            const float mk = at(k, 0);
+            if (mk == -INFINITY && at(k, 1) == 0) continue;
+            w = exp2f(mk - base);
+            l += w * at(k, 1);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[d][x] += w * at(k, 2 + d * 16 + x);
+        }
+        m = mm;
+    }
+    if (!live) return;
+    if (job.splits == 1) {
+        const float inv = l == 0 ? 0.0f : 1.0f / l;
+        uint16_t* const out = a.out + row * a.out_stride + (int64_t)h * D + 4 * half;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                s16x4 y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = (short)T::put(l == 0 ? 0.0f : o[d][4 * x + e] * inv);
+                *(s16x4*)(out + d * 32 + 8 * x) = y;
+            }
+        if (a.lse && half == 0) a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    } else {
+        float* const part = partial + (int64_t)job.slot * S::kPartial;
+        const int at = wm * kRowsPerWave + col;
+        if (half == 0) {
+            part[at] = m;
+            part[S::kMt + at] = l;
+        }
+        float* const po = part + 2 * S::kMt + (int64_t)at * D + 4 * half;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *(f32x4*)(po + d * 32 + 8 * x) = f32x4{o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]};
+    }
+}
+
+// Joins the chunks of split segments; a wave per row and query head.
+template <class T, int D, int MT>
+__global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, int slots, const float* partial) {
+    constexpr int E = D / 64;
+    const int lane = threadIdx.x & 63;
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int h = (int)(id % a.Hq);
+    const int64_t row = id / a.Hq;
+    if (row >= (int64_t)a.c.B * a.c.rows) return;
+    const int b = (int)(row / a.c.rows), r = (int)(row - (int64_t)b * a.c.rows);
+    int jobs;
+    const int c = chunk_units(a, MT, slots, lane, &jobs);
+    const Request q = request_of(a, b, MT);
+    const int splits = q.rows ? (q.units + c - 1) / c : 0;
+    if (r >= q.rows || splits < 2) return;
+    int before = 0;
+    for (int b0 = 0; b0 < b; b0 += 64) {
+        const Request x = request_of(a, b0 + lane, MT);
+        int ns;
+        (void)chunks_of(a, x, c, &ns);
+        if (b0 + lane < b) before += ns;
+    }
+    before = wave_sum(before);
+    const int hk = h / a.G, mrow = r * a.G + (h - hk * a.G), mt = mrow / MT, at = mrow - mt * MT;
+    const int64_t first = before + (int64_t)hk * splits * q.mtiles + mt;
+    const float* part = partial + first * (MT * (D + 2));
+    const int64_t step = (int64_t)q.mtiles * (MT * (D + 2));
+    float top = -INFINITY;
+    for (int s = lane; s < splits; s += 64) top = fmaxf(top, part[s * step + at]);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float l = 0, o[E] = {};
+    for (int s = 0; s < splits; ++s) {
+        const float* p = part + s * step;
+        const float ms = p[at], ls = p[MT + at];
+        if (ls == 0) continue;                             // nothing seen: its sums are zeros
+        const float w = exp2f(ms - base);
+        l += w * ls;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += w * p[2 * MT + (int64_t)at * D + lane * E + e];
+    }
+    const float inv = l == 0 ? 0.0f : 1.0f / l;
+    uint16_t* const out = a.out + row * a.out_stride + (int64_t)h * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = T::put(l == 0 ? 0.0f : o[e] * inv);
+    if (a.lse && lane == 0) a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+constexpr int kCus = 256;
+
+// Row tile by the rows of a key head: up to 32 rows the waves share out the
+// keys, up to 64 both, beyond that the rows.
+int tile_rows(const ChunkArgs& c, int G) {
+    const int64_t m = (int64_t)c.rows * G;
+    return m <= 32 ? 32 : (m <= 64 ? 64 : 128);
+}
+
+int slots_for(int mt, int D) {
+    if (mt == 32) return kCus * (D == 64 ? 2 : 1);
+    return kCus * (D == 256 ? 1 : 2);
+}
+
+// Upper bound of a call's workgroups: chunk_units() makes at most
+// work / c + segments <= room + segments of them, room <= slots.
+int64_t max_jobs(const ChunkArgs& c, int Hkv, int G, int mt, int slots) {
+    return (int64_t)c.B * Hkv * (((int64_t)c.rows * G + mt - 1) / mt) + slots;
+}
+
+template <class T, int D, int WM, int WK, int KT, int PER_CU>
+hipError_t run(const AttentionArgs& a, float* partial, hipStream_t stream) {
+    using S = Shape<T, D, WM, WK, KT>;
+    const int slots = slots_for(S::kMt, D);
+    const int64_t jobs = (max_jobs(a.c, a.kv.Hkv, a.G, S::kMt, slots) + 7) / 8 * 8;
+    const auto kernel = attention_kernel<T, D, WM, WK, KT, PER_CU>;
+    kernel<<<(unsigned)jobs, S::kThreads, S::kLds, stream>>>(a, slots, partial);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t waves = (int64_t)a.c.B * a.c.rows * a.Hq;
+    combine_kernel<T, D, S::kMt><<<(unsigned)((waves + 3) / 4), 256, 0, stream>>>(a, slots, partial);
+    return hipGetLastError();
+}
+
+template <class T, int D>
+hipError_t run_rows(const AttentionArgs& a, float* partial, hipStream_t stream) {
+    const int mt = tile_rows(a.c, a.G);
+    if constexpr (D == 256) {
+        if (mt == 32) return run<T, D, 1, 2, 32, 1>(a, partial, stream);
+        if (mt == 64) return run<T, D, 2, 1, 32, 1>(a, partial, stream);
+        return run<T, D, 4, 1, 64, 1>(a, partial, stream);
+    } else {
+        if (mt == 32) return run<T, D, 1, 4, 32, D == 64 ? 2 : 1>(a, partial, stream);
+        if (mt == 64) return run<T, D, 2, 2, 32, 2>(a, partial, stream);
+        return run<T, D, 4, 1, 64, 2>(a, partial, stream);
+    }
 }
 
 template <class T>
-hipError_t launch_for(const AttentionArgs& a, hipStream_t stream) {
-    const unsigned grid = (unsigned)((int64_t)a.c.B * a.c.rows * a.Hq);
+hipError_t run_type(const AttentionArgs& a, float* partial, hipStream_t stream) {
     switch (a.kv.D) {
-    case 64: attention_simple<T, 64><<<grid, 64, 0, stream>>>(a); break;
-    case 128: attention_simple<T, 128><<<grid, 64, 0, stream>>>(a); break;
-    default: attention_simple<T, 256><<<grid, 64, 0, stream>>>(a); break;
+    case 64: return run_rows<T, 64>(a, partial, stream);
+    case 128: return run_rows<T, 128>(a, partial, stream);
+    default: return run_rows<T, 256>(a, partial, stream);
     }
-    return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attention_workspace(const ChunkArgs&, int, int, int) { return 256; }
+size_t attention_workspace(const ChunkArgs& c, int Hkv, int Hq, int D) {
+    const int G = Hq / Hkv, mt = tile_rows(c, G);
+    return (size_t)(2 * slots_for(mt, D)) * mt * (D + 2) * sizeof(float);
+}
 
-hipError_t launch_attention(const AttentionArgs& a, int dtype, void*, hipStream_t stream) {
-    return dtype == DT_DTYPE_BF16 ? launch_for<Bf16>(a, stream) : launch_for<F16>(a, stream);
+hipError_t launch_attention(const AttentionArgs& a, int dtype, void* workspace, hipStream_t stream) {
+    return dtype == DT_DTYPE_BF16 ? run_type<Bf16>(a, (float*)workspace, stream)
+                                  : run_type<F16>(a, (float*)workspace, stream);
 }
 
 }  // namespace dt
