@@ -104,19 +104,21 @@ __device__ inline int chunk_units(const AttentionArgs& a, int mt_rows, int slots
         segs += q.mtiles * a.kv.Hkv;
         work += (int64_t)q.mtiles * a.kv.Hkv * q.units;
     }
-    segs = wave_sum(segs);
-    work = wave_sum(work);
+    segs = __builtin_amdgcn_readfirstlane(wave_sum(segs));
+    work = uniform(wave_sum(work));
     // rounding adds at most one chunk a segment
-    const int64_t room = slots - segs > slots / 4 ? slots - segs : slots / 4;
-    int64_t c = (work + room - 1) / room;
+    const int room = slots - segs > slots / 4 ? slots - segs : slots / 4;
+    // the quotient from a division in doubles, put right by its remainder
+    int64_t c = (int64_t)((double)work / (double)room);
+    c += (c * room < work) + (c * room + room < work);
     if (c < kMinUnits) c = kMinUnits;
     if (c > kMaxSlots) c = kMaxSlots;
     int n = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
         const Request q = request_of(a, b0 + lane, mt_rows);
-        n += q.mtiles * a.kv.Hkv * (int)((q.units + c - 1) / c);
+        n += q.mtiles * a.kv.Hkv * ((q.units + (int)c - 1) / (int)c);
     }
-    *jobs = wave_sum(n);
+    *jobs = __builtin_amdgcn_readfirstlane(wave_sum(n));
     return (int)c;
 }
 
@@ -183,7 +185,8 @@ __device__ inline bool odd_value(uint32_t pair) {          // an infinity or NaN
 // every LDS read it issued before has its data, so that the next copies may
 // overwrite what was read.
 __device__ inline void copy_to_lds(const uint16_t* from, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
+                 "s"(__builtin_amdgcn_readfirstlane(to)) : "m0");
 }
 __device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
@@ -191,6 +194,13 @@ template <int D>
 __device__ inline int swizzle_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
 template <int D>
 __device__ inline int swizzle_v(int row) { return D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2; }
+
+struct True {
+    static constexpr bool value = true;
+};
+struct False {
+    static constexpr bool value = false;
+};
 
 template <class T, int D, int WM, int WK, int KT>
 struct Shape {
@@ -321,18 +331,23 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     u64 valid = valid_next;
     look_up(wk + WK);
     const int rounds = (tiles + WK - 1) / WK;
-    for (int i = 0; i < rounds; ++i) {
+    constexpr u64 kFull = KT == 64 ? ~0ull : 0xFFFFFFFFull;
+    // Round i of the loop; `masked` is a type: a chunk's first tiles are seen
+    // in full, and their loop has no code for anything else.
+    const auto round = [&](int i, auto is_masked) {
+        constexpr bool masked = decltype(is_masked)::value;
         const int t = wk + i * WK;
         wait_copies();
         if constexpr (WM > 1) __syncthreads();
-        u64 now = valid;
+        const u64 now = valid;
         if (t + WK < tiles) {
             issue((i + 1) & 1);
             valid = valid_next;
             look_up(t + 2 * WK);
         }
         const int k0 = k_first + t * KT;
-        if (!work || t >= tiles || k0 >= any) continue;
+        if constexpr (masked)
+            if (!work || t >= tiles || k0 >= any) return;
         char* const kt = my + (i & 1) * 2 * S::kTile;
         char* const vt = kt + S::kTile;
 
@@ -345,9 +360,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
                 s[n] = mfma(T(), *(const s16x8*)(kt + kaddr[x] + n * 32 * D * 2), qf[x], s[n]);
         }
         uint32_t see[NB];
-        const u64 full = KT == 64 ? ~0ull : 0xFFFFFFFFull;
-        const bool masked = k0 + KT > all || (now & full) != full;
-        if (masked) {
+        if constexpr (masked) {
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 const int64_t kk = k0 + 32 * n;
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         };
         bool odd = false;
-        if (masked) {
+        if constexpr (masked) {
             // An unseen key's weight is 0, but 0 times an infinity or NaN is
             // not: tiles with such values take the careful way.
 #pragma unroll 1
@@ -428,7 +441,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
             for (int d = 0; d < ND; ++d)
 #pragma unroll
                 for (int x = 0; x < NB * 2; ++x) o[d] = mfma(T(), value(d, x), p[x], o[d]);
-        } else {
+        } else if constexpr (masked) {
             // The finite values are summed as always; whether a query sees
             // an infinity (NaN: of both signs) is counted by two more
             // products of truth values.
@@ -465,7 +478,14 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
                 }
             }
         }
-    }
+    };
+    // rounds whose tile every query of the wave sees in full
+    const int64_t plain = work ? (all < k_end ? all : k_end) - k_first : 0;
+    const int whole = plain > 0 ? (int)(plain / KT) : 0;
+    const int fast = whole > wk ? (whole - wk + WK - 1) / WK : 0;
+    int i = 0;
+    for (; i < fast && (valid & kFull) == kFull; ++i) round(i, False());
+    for (; i < rounds; ++i) round(i, True());
     l += __shfl_xor(l, 32);
 
     if constexpr (WK > 1) {
