@@ -23,8 +23,8 @@
 // spreads both over the 64 banks.
 //
 // Work.  Each workgroup derives the whole split from the lengths: segments
-// (request, key head, row tile) times tiles, cut into chunks of equal size so
-// that about `slots` workgroups share the work however ragged the batch is.
+// (request, key head, row tile) times key units, cut into chunks of equal size
+// so that the resident workgroups share the work however ragged the batch is.
 // A segment in one chunk is written at once, others by combine_kernel.
 #include <math.h>
 
@@ -43,6 +43,9 @@ typedef uint64_t u64;
 
 constexpr int kUnit = 64;          // keys of the split's unit of work
 constexpr int kMinUnits = 4;       // a chunk has at least 256 keys
+constexpr float kOneRound = 16;    // units a slot up to which the work is cut into one round
+constexpr float kSplitCost = 4;    // a partial result's way through memory, in units
+constexpr int kMaxSearch = 512;    // requests up to which the chunk's size is searched for
 constexpr int kRowsPerWave = 32;
 constexpr float kLazy = 8.0f;      // log2 of the largest weight before the sums are rescaled
 
@@ -96,39 +99,71 @@ __device__ inline int64_t uniform(int64_t x) {
 }
 
 // Units of a chunk: the same on every wave of every workgroup of a call.
-__device__ inline int chunk_units(const AttentionArgs& a, int mt_rows, int slots, int lane, int* jobs) {
+// `slots` workgroups are resident at a time, so J chunks of c units take
+// ceil(J / slots) * (c + kSplitCost) units of time.  Work of a few units a slot is cut
+// into one round; more into the best of 64 sizes, a lane each, around one to
+// four rounds.
+__device__ inline int chunk_units(const AttentionArgs& a, int mt_rows, int slots, int lane) {
     int64_t work = 0;
-    int segs = 0;
+    int segs = 0, longest = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
         const Request q = request_of(a, b0 + lane, mt_rows);
         segs += q.mtiles * a.kv.Hkv;
         work += (int64_t)q.mtiles * a.kv.Hkv * q.units;
+        longest = q.units > longest ? q.units : longest;
     }
     segs = __builtin_amdgcn_readfirstlane(wave_sum(segs));
     work = uniform(wave_sum(work));
-    // rounding adds at most one chunk a segment
-    const int room = slots - segs > slots / 4 ? slots - segs : slots / 4;
-    // the quotient from a division in doubles, put right by its remainder
-    int64_t c = (int64_t)((double)work / (double)room);
-    c += (c * room < work) + (c * room + room < work);
-    if (c < kMinUnits) c = kMinUnits;
-    if (c > kMaxSlots) c = kMaxSlots;
-    int n = 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_xor(longest, o);
+        longest = y > longest ? y : longest;
+    }
+    longest = __builtin_amdgcn_readfirstlane(longest);
+    const float each = (float)work / (float)slots;         // units a slot
+    if (each < kOneRound || a.c.B > kMaxSearch) {
+        // rounding adds at most one chunk a segment
+        const int room = 2 * segs < slots ? slots - segs : slots;
+        const int c = (int)((float)work / (float)room) + 1;
+        return c < kMinUnits ? kMinUnits : c;
+    }
+    // sizes each * (1 .. 1.94) / (1 .. 4); the longest segment whole is one, too
+    const float want = each * (1.0f + 0.0625f * (lane & 15)) / (float)(1 + (lane >> 4));
+    int c = lane == 0 ? longest : (int)want + 1;
+    c = c < kMinUnits ? kMinUnits : c;
+    const float inv = 1.0f / (float)c;
+    int jobs = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
         const Request q = request_of(a, b0 + lane, mt_rows);
-        n += q.mtiles * a.kv.Hkv * ((q.units + (int)c - 1) / (int)c);
+        const int n = a.c.B - b0 < 64 ? a.c.B - b0 : 64;
+        for (int i = 0; i < n; ++i) {
+            const int u = __builtin_amdgcn_readlane(q.units, i), m = __builtin_amdgcn_readlane(q.mtiles, i);
+            jobs += m * a.kv.Hkv * (int)((float)(u + c - 1) * inv);
+        }
     }
-    *jobs = __builtin_amdgcn_readfirstlane(wave_sum(n));
-    return (int)c;
+    const int rounds = (jobs + slots - 1) / slots;
+    const int most = longest < c ? longest : c;
+    const float cost = (float)rounds * ((float)most + (longest > c ? kSplitCost : 0.0f));
+    // the cheapest; of equals the largest size (fewest partial results)
+    float best = cost;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) best = fminf(best, __shfl_xor(best, o));
+    int pick = cost == best ? c : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_xor(pick, o);
+        pick = y > pick ? y : pick;
+    }
+    return __builtin_amdgcn_readfirstlane(pick);
 }
 
-// Chunks of a request in all, and of one whose segments are split (those have
-// partial results: a segment of more than c units has at most 2 units / c
-// chunks, so there are at most 2 work / c <= 2 room <= 2 slots of them).
-__device__ inline int chunks_of(const AttentionArgs& a, const Request& q, int c, int* split) {
-    const int per = (q.units + c - 1) / c, n = q.mtiles * a.kv.Hkv * per;
-    *split = per > 1 ? n : 0;
-    return n;
+__device__ inline int splits_of(const Request& q, int c) { return (q.units + c - 1) / c; }
+
+// Partial results of a request: those of its chunks, if its segments are
+// split.  A segment of more than c units has at most 2 units / c chunks, so a
+// call has at most 2 work / c of them; c is at least work / (4 slots).
+__device__ inline int partials_of(const AttentionArgs& a, const Request& q, int splits) {
+    return splits > 1 ? q.mtiles * a.kv.Hkv * splits : 0;
 }
 
 struct Job {
@@ -136,35 +171,41 @@ struct Job {
     Request q;
 };
 
-// Job `idx` of the call; the row tiles of a segment's chunk are neighbours.
-__device__ inline Job job_of(const AttentionArgs& a, int mt_rows, int c, int idx, int lane) {
+// The job of workgroup `y` of XCD `x`.  The row tiles of one chunk of keys
+// read the same keys: they stay on one XCD, next to each other; the chunks go
+// round over the XCDs (workgroups do so by themselves, by their number).
+__device__ inline Job job_of(const AttentionArgs& a, int mt_rows, int c, int x, int y, int lane) {
     Job j{};
-    int before = 0, slots_before = 0;
+    int before = 0, groups_before = 0, partials_before = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
         const Request q = request_of(a, b0 + lane, mt_rows);
-        int ns;
-        const int n = chunks_of(a, q, c, &ns);
+        const int splits = splits_of(q, c), groups = q.rows ? a.kv.Hkv * splits : 0;
+        const int groups_upto = wave_prefix(groups, lane);
+        const int first = (x - (groups_before + groups_upto - groups)) & 7;
+        const int n = first < groups ? ((groups - first + 7) >> 3) * q.mtiles : 0;
         const int upto = wave_prefix(n, lane);
-        const u64 hit = __ballot(before + upto > idx);
+        const u64 hit = __ballot(before + upto > y);
+        const int partials = partials_of(a, q, splits);
         if (hit) {
             const int at = __builtin_ctzll(hit);
-            const int local = idx - before - (__shfl(upto, at) - __shfl(n, at));
-            j.b = __builtin_amdgcn_readfirstlane(b0 + at);
-            j.q.rows = __builtin_amdgcn_readfirstlane(__shfl(q.rows, at));
-            j.q.keys = __builtin_amdgcn_readfirstlane(__shfl(q.keys, at));
-            j.q.mtiles = __builtin_amdgcn_readfirstlane(__shfl(q.mtiles, at));
-            j.q.units = __builtin_amdgcn_readfirstlane(__shfl(q.units, at));
-            j.splits = (j.q.units + c - 1) / c;
-            j.mt = __builtin_amdgcn_readfirstlane(local) % j.q.mtiles;
-            const int rest = __builtin_amdgcn_readfirstlane(local) / j.q.mtiles;
-            j.split = rest % j.splits;
-            j.head = rest / j.splits;
-            j.slot = slots_before + __builtin_amdgcn_readfirstlane(wave_sum(lane < at ? ns : 0)) +
-                     __builtin_amdgcn_readfirstlane(local);
+            const int local = y - before - __builtin_amdgcn_readlane(upto, at) + __builtin_amdgcn_readlane(n, at);
+            j.b = b0 + at;
+            j.q.rows = __builtin_amdgcn_readlane(q.rows, at);
+            j.q.keys = __builtin_amdgcn_readlane(q.keys, at);
+            j.q.mtiles = __builtin_amdgcn_readlane(q.mtiles, at);
+            j.q.units = __builtin_amdgcn_readlane(q.units, at);
+            j.splits = splits_of(j.q, c);
+            j.mt = local % j.q.mtiles;
+            const int g = __builtin_amdgcn_readlane(first, at) + 8 * (local / j.q.mtiles);
+            j.split = g % j.splits;
+            j.head = g / j.splits;
+            j.slot = partials_before + __builtin_amdgcn_readfirstlane(wave_sum(lane < at ? partials : 0)) +
+                     g * j.q.mtiles + j.mt;
             return j;
         }
-        before += __shfl(upto, 63);
-        slots_before += wave_sum(ns);
+        before += __builtin_amdgcn_readlane(upto, 63);
+        groups_before += __builtin_amdgcn_readlane(groups_upto, 63);
+        partials_before += __builtin_amdgcn_readfirstlane(wave_sum(partials));
     }
     j.b = -1;
     return j;
@@ -225,13 +266,9 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     const int wm = wave % WM, wk = wave / WM;
     const int half = lane >> 5, col = lane & 31;
 
-    int jobs;
-    const int c = chunk_units(a, S::kMt, slots, lane, &jobs);
-    // neighbours in the job order share keys: give them to one XCD (workgroups go round over the 8)
-    const int per = (jobs + 7) >> 3;
-    const int idx = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || idx >= jobs) return;
-    const Job job = job_of(a, S::kMt, c, idx, lane);
+    const int c = chunk_units(a, S::kMt, slots, lane);
+    const Job job = job_of(a, S::kMt, c, blockIdx.x & 7, blockIdx.x >> 3, lane);
+    if (job.b < 0) return;
     const int b = job.b;
     const int ctx = a.c.ctx_len[b], lead = a.c.lead, nn = job.q.rows - lead;
     const int mrows = job.q.rows * a.G;
@@ -557,53 +594,60 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     }
 }
 
-// Joins the chunks of split segments; a wave per row and query head.
+// Joins the chunks of split segments; a wave per row and query head at a time.
 template <class T, int D, int MT>
 __global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, int slots, const float* partial) {
     constexpr int E = D / 64;
     const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int h = (int)(id % a.Hq);
-    const int64_t row = id / a.Hq;
-    if (row >= (int64_t)a.c.B * a.c.rows) return;
-    const int b = (int)(row / a.c.rows), r = (int)(row - (int64_t)b * a.c.rows);
-    int jobs;
-    const int c = chunk_units(a, MT, slots, lane, &jobs);
-    const Request q = request_of(a, b, MT);
-    const int splits = q.rows ? (q.units + c - 1) / c : 0;
-    if (r >= q.rows || splits < 2) return;
-    int before = 0;
-    for (int b0 = 0; b0 < b; b0 += 64) {
-        const Request x = request_of(a, b0 + lane, MT);
-        int ns;
-        (void)chunks_of(a, x, c, &ns);
-        if (b0 + lane < b) before += ns;
+    const int c = chunk_units(a, MT, slots, lane);
+    int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int64_t before = 0;                                    // rows of split requests, and partial results, so far
+    int partials_before = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += 64) {
+        const Request mine = request_of(a, b0 + lane, MT);
+        const int my_splits = splits_of(mine, c), partials = partials_of(a, mine, my_splits);
+        const int n = partials ? mine.rows * a.Hq : 0;     // below 2^31 over the call
+        const int upto = wave_prefix(n, lane), partials_upto = wave_prefix(partials, lane);
+        const int total = __builtin_amdgcn_readlane(upto, 63);
+        for (; id < before + total; id += (int64_t)gridDim.x * 4) {
+            const int local = (int)(id - before);
+            const int at = __builtin_ctzll(__ballot(upto > local));
+            const int b = b0 + at, splits = __builtin_amdgcn_readlane(my_splits, at);
+            const int mtiles = __builtin_amdgcn_readlane(mine.mtiles, at);
+            const int item = local - __builtin_amdgcn_readlane(upto, at) + __builtin_amdgcn_readlane(n, at);
+            const int r = item / a.Hq, h = item - r * a.Hq;
+            const int hk = h / a.G, mrow = r * a.G + (h - hk * a.G), mt = mrow / MT, in = mrow - mt * MT;
+            const int64_t first = (int64_t)partials_before + __builtin_amdgcn_readlane(partials_upto, at) -
+                                  __builtin_amdgcn_readlane(partials, at) + (int64_t)hk * splits * mtiles + mt;
+            const float* part = partial + first * (MT * (D + 2));
+            const int64_t step = (int64_t)mtiles * (MT * (D + 2));
+            float top = -INFINITY;
+            for (int s = lane; s < splits; s += 64) top = fmaxf(top, part[s * step + in]);
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+            const float base = top == -INFINITY ? 0.0f : top;
+            float l = 0, o[E] = {};
+#pragma unroll 4
+            for (int s = 0; s < splits; ++s) {
+                const float* p = part + s * step;
+                const float ms = p[in], ls = p[MT + in];
+                // l = 0: nothing seen, its sums are zeros (and m may be -inf)
+                const float w = ls == 0 ? 0.0f : exp2f(ms - base);
+                l += w * ls;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] += w * p[2 * MT + (int64_t)in * D + lane * E + e];
+            }
+            const float inv = l == 0 ? 0.0f : 1.0f / l;
+            const int64_t row = (int64_t)b * a.c.rows + r;
+            uint16_t* const out = a.out + row * a.out_stride + (int64_t)h * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) out[e] = T::put(l == 0 ? 0.0f : o[e] * inv);
+            if (a.lse && lane == 0)
+                a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+        }
+        before += total;
+        partials_before += __builtin_amdgcn_readlane(partials_upto, 63);
     }
-    before = wave_sum(before);
-    const int hk = h / a.G, mrow = r * a.G + (h - hk * a.G), mt = mrow / MT, at = mrow - mt * MT;
-    const int64_t first = before + (int64_t)hk * splits * q.mtiles + mt;
-    const float* part = partial + first * (MT * (D + 2));
-    const int64_t step = (int64_t)q.mtiles * (MT * (D + 2));
-    float top = -INFINITY;
-    for (int s = lane; s < splits; s += 64) top = fmaxf(top, part[s * step + at]);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float l = 0, o[E] = {};
-    for (int s = 0; s < splits; ++s) {
-        const float* p = part + s * step;
-        const float ms = p[at], ls = p[MT + at];
-        if (ls == 0) continue;                             // nothing seen: its sums are zeros
-        const float w = exp2f(ms - base);
-        l += w * ls;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += w * p[2 * MT + (int64_t)at * D + lane * E + e];
-    }
-    const float inv = l == 0 ? 0.0f : 1.0f / l;
-    uint16_t* const out = a.out + row * a.out_stride + (int64_t)h * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = T::put(l == 0 ? 0.0f : o[e] * inv);
-    if (a.lse && lane == 0) a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------------------
@@ -624,23 +668,26 @@ int slots_for(int mt, int D) {
     return kCus * (D == 256 ? 1 : 2);
 }
 
-// Upper bound of a call's workgroups: chunk_units() makes at most
-// work / c + segments <= room + segments of them, room <= slots.
+// Upper bound of a call's workgroups on one XCD.  chunk_units() makes at most
+// segments + 4 slots chunks; a request's groups go round over the XCDs, so
+// one XCD has at most an eighth of its chunks and one group of mtiles more.
 int64_t max_jobs(const ChunkArgs& c, int Hkv, int G, int mt, int slots) {
-    return (int64_t)c.B * Hkv * (((int64_t)c.rows * G + mt - 1) / mt) + slots;
+    const int64_t mtiles = ((int64_t)c.rows * G + mt - 1) / mt;
+    return ((int64_t)c.B * Hkv * mtiles + 4 * slots + 7) / 8 + c.B * mtiles;
 }
 
 template <class T, int D, int WM, int WK, int KT, int PER_CU>
 hipError_t run(const AttentionArgs& a, float* partial, hipStream_t stream) {
     using S = Shape<T, D, WM, WK, KT>;
     const int slots = slots_for(S::kMt, D);
-    const int64_t jobs = (max_jobs(a.c, a.kv.Hkv, a.G, S::kMt, slots) + 7) / 8 * 8;
+    const int64_t jobs = 8 * max_jobs(a.c, a.kv.Hkv, a.G, S::kMt, slots);
     const auto kernel = attention_kernel<T, D, WM, WK, KT, PER_CU>;
     kernel<<<(unsigned)jobs, S::kThreads, S::kLds, stream>>>(a, slots, partial);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t waves = (int64_t)a.c.B * a.c.rows * a.Hq;
-    combine_kernel<T, D, S::kMt><<<(unsigned)((waves + 3) / 4), 256, 0, stream>>>(a, slots, partial);
+    const unsigned grid = waves < 4 * 4 * kCus ? (unsigned)((waves + 3) / 4) : 4 * kCus;
+    combine_kernel<T, D, S::kMt><<<grid, 256, 0, stream>>>(a, slots, partial);
     return hipGetLastError();
 }
 
@@ -671,7 +718,7 @@ hipError_t run_type(const AttentionArgs& a, float* partial, hipStream_t stream) 
 
 size_t attention_workspace(const ChunkArgs& c, int Hkv, int Hq, int D) {
     const int G = Hq / Hkv, mt = tile_rows(c, G);
-    return (size_t)(2 * slots_for(mt, D)) * mt * (D + 2) * sizeof(float);
+    return (size_t)(8 * slots_for(mt, D)) * mt * (D + 2) * sizeof(float);
 }
 
 hipError_t launch_attention(const AttentionArgs& a, int dtype, void* workspace, hipStream_t stream) {
