@@ -814,6 +814,7 @@ extern "C" dt_status dt_tree_attention(const dt_kv_cache* kv, const dt_chunk* ch
     a.out_stride = p->out_stride;
     a.Hq = p->Hq;
     a.G = p->Hq / kv->Hkv;
+    a.by16 = kv->page_size % 16 == 0 && a.kv.slot_stride < (1 << 25);
     a.scale_log2 = (float)(p->scale * 1.4426950408889634074);
     a.lse = p->lse;
     const DeviceScope scope((hipStream_t)p->stream);
@@ -828,6 +829,7 @@ extern "C" dt_status dt_process_logits(const dt_logits_params* p) {
     if (rows < 1 || p->history_max < 0 || p->n_bias < 0) return DT_ERR_INVALID_ARG;
     if (p->dtype != DT_DTYPE_F32 && p->dtype != DT_DTYPE_BF16) return DT_ERR_INVALID_ARG;
     if (p->B > 65535 || rows > kMaxChunkRows || p->V >= kMaxV || p->n_bias > 65534) return DT_ERR_UNSUPPORTED;
+    if (p->node_tokens && p->n_max > kMaxCommitNodes) return DT_ERR_UNSUPPORTED;
     if (p->history && !p->history_len) return DT_ERR_INVALID_ARG;
     if (p->node_tokens && !p->node_mask) return DT_ERR_INVALID_ARG;
     if (p->bias_ids && !p->bias) return DT_ERR_INVALID_ARG;

@@ -29,6 +29,7 @@
 #include <math.h>
 
 #include "pass.h"
+#include "wave.h"
 
 namespace dt {
 namespace {
@@ -77,20 +78,14 @@ __device__ inline Request request_of(const AttentionArgs& a, int b, int mt_rows)
     return q;
 }
 
-template <class V>
-__device__ inline V wave_sum(V x) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
-    return x;
-}
-
 __device__ inline int wave_prefix(int x, int lane) {      // inclusive
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_up(x, o);
-        if (lane >= o) x += y;
-    }
-    return x;
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);      // row_shr:1 ... within rows of 16
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    const int a = __builtin_amdgcn_readlane(x, 15), b = __builtin_amdgcn_readlane(x, 31),
+              c = __builtin_amdgcn_readlane(x, 47);
+    return x + (lane >= 16 ? a : 0) + (lane >= 32 ? b : 0) + (lane >= 48 ? c : 0);
 }
 
 __device__ inline int64_t uniform(int64_t x) {
@@ -100,26 +95,21 @@ __device__ inline int64_t uniform(int64_t x) {
 
 // Units of a chunk: the same on every wave of every workgroup of a call.
 // `slots` workgroups are resident at a time, so J chunks of c units take
-// ceil(J / slots) * (c + kSplitCost) units of time.  Work of a few units a slot is cut
-// into one round; more into the best of 64 sizes, a lane each, around one to
-// four rounds.
-__device__ inline int chunk_units(const AttentionArgs& a, int mt_rows, int slots, int lane) {
-    int64_t work = 0;
+// about ceil(J / slots) * (c + kSplitCost) units of time.  Work of a few units
+// a slot is cut into one round; more into the best of 64 sizes, a lane each,
+// around one to four rounds.  `q0`: the first 64 requests.
+__device__ inline int chunk_units(const AttentionArgs& a, const Request& q0, int mt_rows, int slots, int lane) {
+    double work = 0;
     int segs = 0, longest = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
-        const Request q = request_of(a, b0 + lane, mt_rows);
+        const Request q = b0 ? request_of(a, b0 + lane, mt_rows) : q0;
         segs += q.mtiles * a.kv.Hkv;
-        work += (int64_t)q.mtiles * a.kv.Hkv * q.units;
+        work += (double)(q.mtiles * a.kv.Hkv) * q.units;
         longest = q.units > longest ? q.units : longest;
     }
-    segs = __builtin_amdgcn_readfirstlane(wave_sum(segs));
-    work = uniform(wave_sum(work));
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_xor(longest, o);
-        longest = y > longest ? y : longest;
-    }
-    longest = __builtin_amdgcn_readfirstlane(longest);
+    segs = wave_add_i32(segs);
+    work = wave_add_f64(work);
+    longest = -wave_min_i32(-longest);
     const float each = (float)work / (float)slots;         // units a slot
     if (each < kOneRound || a.c.B > kMaxSearch) {
         // rounding adds at most one chunk a segment
@@ -134,7 +124,7 @@ __device__ inline int chunk_units(const AttentionArgs& a, int mt_rows, int slots
     const float inv = 1.0f / (float)c;
     int jobs = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
-        const Request q = request_of(a, b0 + lane, mt_rows);
+        const Request q = b0 ? request_of(a, b0 + lane, mt_rows) : q0;
         const int n = a.c.B - b0 < 64 ? a.c.B - b0 : 64;
         for (int i = 0; i < n; ++i) {
             const int u = __builtin_amdgcn_readlane(q.units, i), m = __builtin_amdgcn_readlane(q.mtiles, i);
@@ -145,23 +135,16 @@ __device__ inline int chunk_units(const AttentionArgs& a, int mt_rows, int slots
     const int most = longest < c ? longest : c;
     const float cost = (float)rounds * ((float)most + (longest > c ? kSplitCost : 0.0f));
     // the cheapest; of equals the largest size (fewest partial results)
-    float best = cost;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) best = fminf(best, __shfl_xor(best, o));
-    int pick = cost == best ? c : 0;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_xor(pick, o);
-        pick = y > pick ? y : pick;
-    }
-    return __builtin_amdgcn_readfirstlane(pick);
+    const float best = wave_min_f32(cost);
+    return -wave_min_i32(cost == best ? -c : 0);
 }
 
 __device__ inline int splits_of(const Request& q, int c) { return (q.units + c - 1) / c; }
 
 // Partial results of a request: those of its chunks, if its segments are
-// split.  A segment of more than c units has at most 2 units / c chunks, so a
-// call has at most 2 work / c of them; c is at least work / (4 slots).
+// split.  A segment of u > c units has fewer than u / c + 1 < 2 u / c chunks, a
+// call thus fewer than work / c + (split segments) of them, and fewer split
+// segments than work / c; c is more than work / (4 slots).
 __device__ inline int partials_of(const AttentionArgs& a, const Request& q, int splits) {
     return splits > 1 ? q.mtiles * a.kv.Hkv * splits : 0;
 }
@@ -174,11 +157,11 @@ struct Job {
 // The job of workgroup `y` of XCD `x`.  The row tiles of one chunk of keys
 // read the same keys: they stay on one XCD, next to each other; the chunks go
 // round over the XCDs (workgroups do so by themselves, by their number).
-__device__ inline Job job_of(const AttentionArgs& a, int mt_rows, int c, int x, int y, int lane) {
+__device__ inline Job job_of(const AttentionArgs& a, const Request& q0, int mt_rows, int c, int x, int y, int lane) {
     Job j{};
     int before = 0, groups_before = 0, partials_before = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
-        const Request q = request_of(a, b0 + lane, mt_rows);
+        const Request q = b0 ? request_of(a, b0 + lane, mt_rows) : q0;
         const int splits = splits_of(q, c), groups = q.rows ? a.kv.Hkv * splits : 0;
         const int groups_upto = wave_prefix(groups, lane);
         const int first = (x - (groups_before + groups_upto - groups)) & 7;
@@ -199,13 +182,13 @@ __device__ inline Job job_of(const AttentionArgs& a, int mt_rows, int c, int x, 
             const int g = __builtin_amdgcn_readlane(first, at) + 8 * (local / j.q.mtiles);
             j.split = g % j.splits;
             j.head = g / j.splits;
-            j.slot = partials_before + __builtin_amdgcn_readfirstlane(wave_sum(lane < at ? partials : 0)) +
+            j.slot = partials_before + wave_add_i32(lane < at ? partials : 0) +
                      g * j.q.mtiles + j.mt;
             return j;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
         groups_before += __builtin_amdgcn_readlane(groups_upto, 63);
-        partials_before += __builtin_amdgcn_readfirstlane(wave_sum(partials));
+        partials_before += wave_add_i32(partials);
     }
     j.b = -1;
     return j;
@@ -229,6 +212,11 @@ __device__ inline void copy_to_lds(const uint16_t* from, uint32_t to) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
                  "s"(__builtin_amdgcn_readfirstlane(to)) : "m0");
 }
+// The same from `base` + `offset` bytes, with a base common to the wave.
+__device__ inline void copy_to_lds(const char* base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset),
+                 "s"((const char*)uniform((int64_t)base)), "s"(__builtin_amdgcn_readfirstlane(to)) : "m0");
+}
 __device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
 template <int D>
@@ -248,26 +236,30 @@ struct Shape {
     static constexpr int kThreads = 64 * WM * WK;
     static constexpr int kMt = WM * kRowsPerWave;
     static constexpr int kTile = KT * D * 2;               // bytes of a K or V tile
-    static constexpr int kLds = 2 * 2 * kTile * WK;        // two buffers of K and V a key group
+    static constexpr int kGroup = 4 * kTile;               // K's two buffers, V's two
+    static constexpr int kLds = kGroup * WK;
     static constexpr int kPartial = kMt * (D + 2);         // floats of a split's partial result
 };
 
 template <class T, int D, int WM, int WK, int KT, int PER_CU>
 __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
-    attention_kernel(AttentionArgs a, int slots, float* partial) {
+    attention_kernel(AttentionArgs a, int slots, int* plan, float* partial) {
     using S = Shape<T, D, WM, WK, KT>;
     constexpr int NB = KT / 32, KS = D / 16, ND = D / 32;
     constexpr int kUnits16 = D / 8;                        // 16-byte pieces of a head
     constexpr int kRpi = 64 / kUnits16;                    // rows of a wave's copy instruction
     constexpr int kCopies = KT / kRpi / WM;                // copies of K (and of V) a wave and tile
+    constexpr int kPer16 = 16 / kRpi;                      // copies of 16 rows
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wk = wave / WM;
     const int half = lane >> 5, col = lane & 31;
 
-    const int c = chunk_units(a, S::kMt, slots, lane);
-    const Job job = job_of(a, S::kMt, c, blockIdx.x & 7, blockIdx.x >> 3, lane);
+    const Request q0 = request_of(a, lane, S::kMt);
+    const int c = chunk_units(a, q0, S::kMt, slots, lane);
+    if (blockIdx.x == 0 && tid == 0) *plan = c;            // for combine_kernel
+    const Job job = job_of(a, q0, S::kMt, c, blockIdx.x & 7, blockIdx.x >> 3, lane);
     if (job.b < 0) return;
     const int b = job.b;
     const int ctx = a.c.ctx_len[b], lead = a.c.lead, nn = job.q.rows - lead;
@@ -316,35 +308,62 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     const uint16_t* kbase = a.kv.k + job.head * a.kv.head_stride;
     const uint16_t* vbase = a.kv.v + job.head * a.kv.head_stride;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
-    const uint32_t group = lds0 + wk * 4 * S::kTile;       // K, V of buffer 0, K, V of buffer 1
+    const uint32_t group = lds0 + wk * S::kGroup;
 
-    // lane l looks up key l of a tile
+    // Lane l looks up key l of a tile, one tile before its copies are issued.
+    struct Place {
+        int page, in;                                      // page id (-1: no such key) and slot in the page
+    };
     const int32_t* table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
-    int next_page = -1, next_in = 0;
-    const auto look_up = [&](int t) {                      // of the group's tile t
+    const auto look_up = [&](int t) {
         const int key = k_first + t * KT + (lane & (KT - 1));
-        next_page = -1;
+        Place p = {-1, 0};
         if (t < tiles && key < k_end) {
             const int i = a.kv.page_shift >= 0 ? key >> a.kv.page_shift : key / a.kv.page_size;
-            next_page = table[i];
-            next_in = key - i * a.kv.page_size;
+            p.page = table[i];
+            p.in = key - i * a.kv.page_size;
         }
+        return p;
     };
-    u64 valid_next = 0;
-    const auto issue = [&](int buf) {                      // the tile looked up last
-        const bool ok = next_page >= 0 && next_page < a.kv.num_pages;
-        // a key that is not there: some mapped address, its score and value are dropped below
-        const int64_t off = ok ? next_page * a.kv.page_stride + next_in * a.kv.slot_stride : 0;
-        valid_next = __ballot(ok);
-        const int lo = (int)off, hi = (int)(off >> 32);
+    const auto is_valid = [&](const Place& p) { return p.page >= 0 && p.page < a.kv.num_pages; };
+    // Byte offsets of a lane's copies within the 16 rows they belong to.
+    constexpr int kOwn = kCopies < kPer16 ? kCopies : kPer16;
+    static_assert(kCopies % kOwn == 0 && kPer16 % kOwn == 0, "a wave's copies lie in whole parts of 16 rows");
+    uint32_t koff[kOwn], voff[kOwn];
+    const int piece = lane % kUnits16, prow = lane / kUnits16;
+    const uint32_t slot_bytes = (uint32_t)(a.kv.slot_stride * 2);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int at = wm * kCopies + i;
-            const int trow = at * kRpi + lane / kUnits16, piece = lane % kUnits16;
-            const int64_t o = (int64_t)((u64)(uint32_t)__shfl(lo, trow) | (u64)(uint32_t)__shfl(hi, trow) << 32);
-            const uint32_t to = group + buf * 2 * S::kTile + at * 1024;
-            copy_to_lds(kbase + o + (piece ^ swizzle_k<D>(trow)) * 8, to);
-            copy_to_lds(vbase + o + (piece ^ swizzle_v<D>(trow)) * 8, to + S::kTile);
+    for (int i = 0; i < kOwn; ++i) {
+        const int rg = (wm * kCopies + i) % kPer16 * kRpi + prow;
+        koff[i] = rg * slot_bytes + (piece ^ swizzle_k<D>(rg)) * 16;
+        voff[i] = rg * slot_bytes + (piece ^ swizzle_v<D>(rg)) * 16;
+    }
+    // Copies of a tile into K's (V's) buffer; a key that is not there comes
+    // from some mapped address, its score and value are dropped below.
+    const auto issue = [&](const Place& p, bool is_v, int buf) {
+        const uint16_t* const from = is_v ? vbase : kbase;
+        const uint32_t to = group + (2 * is_v + buf) * S::kTile;
+        const bool ok = is_valid(p);
+        if (a.by16) {
+            // 16 rows that begin at a multiple of 16 lie in one page
+#pragma unroll
+            for (int g = 0; g < kCopies / kOwn; ++g) {
+                const int at = wm * kCopies + g * kOwn, row = at / kPer16 * 16;
+                const int page = __builtin_amdgcn_readlane(ok ? p.page : 0, row);
+                const int in = __builtin_amdgcn_readlane(ok ? p.in : 0, row);
+                const char* base = (const char*)(from + page * a.kv.page_stride) + (int64_t)in * slot_bytes;
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) copy_to_lds(base, is_v ? voff[i] : koff[i], to + (at + i) * 1024);
+            }
+        } else {
+            const int64_t off = ok ? p.page * a.kv.page_stride + p.in * a.kv.slot_stride : 0;
+            const int lo = (int)off, hi = (int)(off >> 32);
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int at = wm * kCopies + i, trow = at * kRpi + prow;
+                const int64_t o = (int64_t)((u64)(uint32_t)__shfl(lo, trow) | (u64)(uint32_t)__shfl(hi, trow) << 32);
+                copy_to_lds(from + o + (piece ^ (is_v ? swizzle_v<D>(trow) : swizzle_k<D>(trow))) * 8, to + at * 1024);
+            }
         }
     };
 
@@ -356,46 +375,44 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
 #pragma unroll
     for (int d = 0; d < ND; ++d)
         vaddr[d] = vrow * D * 2 + (((d * 4) ^ swizzle_v<D>(vrow)) * 16) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-    char* const my = lds + wk * 4 * S::kTile;
+    char* const my = lds + wk * S::kGroup;
 
     f32x16 o[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d] = f32x16{};
     float m = -INFINITY, l = 0;                            // m in units of log2; l of this lane's keys
 
-    look_up(wk);
-    if (wk < tiles) issue(0);
-    u64 valid = valid_next;
-    look_up(wk + WK);
-    const int rounds = (tiles + WK - 1) / WK;
     constexpr u64 kFull = KT == 64 ? ~0ull : 0xFFFFFFFFull;
-    // Round i of the loop; `masked` is a type: a chunk's first tiles are seen
-    // in full, and their loop has no code for anything else.
-    const auto round = [&](int i, auto is_masked) {
+    const auto rescale = [&](float top) {
+        const float mm = fmaxf(m, top);
+        const float w = mm == -INFINITY ? 1.0f : exp2f(m - mm);
+        m = mm;
+        l *= w;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[d][x] *= w;
+    };
+    const auto value = [&](const char* vt, int d, int x) {  // V^T of 32 elements and 16 keys
+        typedef __attribute__((address_space(3))) s16x4 lds4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x) * D * 2));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x + 8) * D * 2));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    // A wave's products go before the other's vector work on the same SIMD
+    // (a prompt's chunk 795 -> 769 us).
+    const auto scores = [&](const char* kt, int n) {
+        f32x16 s = {};
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int x = 0; x < KS; ++x) s = mfma(T(), *(const s16x8*)(kt + kaddr[x] + n * 32 * D * 2), qf[x], s);
+        __builtin_amdgcn_s_setprio(0);
+        return s;
+    };
+    // A tile's scores into the sums; `masked` is a type: the tiles that every
+    // row sees in full have no code for anything else.
+    const auto tile = [&](int k0, f32x16 (&s)[NB], const char* vt, u64 now, auto is_masked) {
         constexpr bool masked = decltype(is_masked)::value;
-        const int t = wk + i * WK;
-        wait_copies();
-        if constexpr (WM > 1) __syncthreads();
-        const u64 now = valid;
-        if (t + WK < tiles) {
-            issue((i + 1) & 1);
-            valid = valid_next;
-            look_up(t + 2 * WK);
-        }
-        const int k0 = k_first + t * KT;
-        if constexpr (masked)
-            if (!work || t >= tiles || k0 >= any) return;
-        char* const kt = my + (i & 1) * 2 * S::kTile;
-        char* const vt = kt + S::kTile;
-
-        f32x16 s[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            s[n] = f32x16{};
-#pragma unroll
-            for (int x = 0; x < KS; ++x)
-                s[n] = mfma(T(), *(const s16x8*)(kt + kaddr[x] + n * 32 * D * 2), qf[x], s[n]);
-        }
         uint32_t see[NB];
         if constexpr (masked) {
 #pragma unroll
@@ -436,16 +453,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
         // The sums are kept relative to an m that may lag the maximum by
         // kLazy: weights stay below 2^8, exact in relative terms for both
         // types, and most tiles leave o alone.
-        if (__any(top > m + kLazy)) {
-            const float mm = fmaxf(m, top);
-            const float w = mm == -INFINITY ? 1.0f : exp2f(m - mm);
-            m = mm;
-            l *= w;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int x = 0; x < 16; ++x) o[d][x] *= w;
-        }
+        if (__any(top > m + kLazy)) rescale(top);
         const float base = m == -INFINITY ? 0.0f : m;
         s16x8 p[NB * 2];
 #pragma unroll
@@ -456,12 +464,6 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
                 l += e;
                 p[2 * n + (x >> 3)][x & 7] = (short)T::put(e);
             }
-        const auto value = [&](int d, int x) {
-            typedef __attribute__((address_space(3))) s16x4 lds4;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x) * D * 2));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x + 8) * D * 2));
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        };
         bool odd = false;
         if constexpr (masked) {
             // An unseen key's weight is 0, but 0 times an infinity or NaN is
@@ -474,10 +476,12 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
             odd = __any(odd);
         }
         if (!odd) {
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int x = 0; x < NB * 2; ++x) o[d] = mfma(T(), value(d, x), p[x], o[d]);
+                for (int x = 0; x < NB * 2; ++x) o[d] = mfma(T(), value(vt, d, x), p[x], o[d]);
+            __builtin_amdgcn_s_setprio(0);
         } else if constexpr (masked) {
             // The finite values are summed as always; whether a query sees
             // an infinity (NaN: of both signs) is counted by two more
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
                 f32x16 up = {}, down = {};
 #pragma unroll
                 for (int x = 0; x < NB * 2; ++x) {
-                    s16x8 v = value(d, x), pos, neg;
+                    s16x8 v = value(vt, d, x), pos, neg;
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
                         const uint32_t bits = (uint16_t)v[y];
@@ -516,10 +520,38 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
             }
         }
     };
-    // rounds whose tile every query of the wave sees in full
+    // tiles that every query of the wave sees in full
     const int64_t plain = work ? (all < k_end ? all : k_end) - k_first : 0;
     const int whole = plain > 0 ? (int)(plain / KT) : 0;
+
+    Place place = look_up(wk);
+    u64 valid = __ballot(is_valid(place));
+    if (wk < tiles) {
+        issue(place, false, 0);
+        issue(place, true, 0);
+    }
+    place = look_up(wk + WK);
+    const int rounds = (tiles + WK - 1) / WK;
     const int fast = whole > wk ? (whole - wk + WK - 1) / WK : 0;
+    const auto round = [&](int i, auto is_masked) {
+        const int t = wk + i * WK;
+        wait_copies();
+        if constexpr (WM > 1) __syncthreads();
+        const u64 now = valid;
+        if (t + WK < tiles) {
+            valid = __ballot(is_valid(place));
+            issue(place, false, (i + 1) & 1);
+            issue(place, true, (i + 1) & 1);
+            place = look_up(t + 2 * WK);
+        }
+        const int k0 = k_first + t * KT;
+        if constexpr (decltype(is_masked)::value)
+            if (!work || t >= tiles || k0 >= any) return;
+        f32x16 s[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) s[n] = scores(my + (i & 1) * S::kTile, n);
+        tile(k0, s, my + (2 + (i & 1)) * S::kTile, now, is_masked);
+    };
     int i = 0;
     for (; i < fast && (valid & kFull) == kFull; ++i) round(i, False());
     for (; i < rounds; ++i) round(i, True());
@@ -594,14 +626,17 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     }
 }
 
-// Joins the chunks of split segments; a wave per row and query head at a time.
+// Joins the chunks of split segments: D / 4 lanes for a row and query head, a
+// running maximum over its chunks, four of which are read at a time.
 template <class T, int D, int MT>
-__global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, int slots, const float* partial) {
-    constexpr int E = D / 64;
+__global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, const int* plan, const float* partial) {
+    constexpr int kLanes = D / 4, kItems = 64 / kLanes;
     const int lane = threadIdx.x & 63;
-    const int c = chunk_units(a, MT, slots, lane);
+    const int c = *plan;
+    // a wave takes kItems neighbours; the items of a batch of requests are
+    // rounded up to whole waves
     int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t before = 0;                                    // rows of split requests, and partial results, so far
+    int64_t before = 0;
     int partials_before = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
         const Request mine = request_of(a, b0 + lane, MT);
@@ -609,43 +644,64 @@ __global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, int slots
         const int n = partials ? mine.rows * a.Hq : 0;     // below 2^31 over the call
         const int upto = wave_prefix(n, lane), partials_upto = wave_prefix(partials, lane);
         const int total = __builtin_amdgcn_readlane(upto, 63);
-        for (; id < before + total; id += (int64_t)gridDim.x * 4) {
-            const int local = (int)(id - before);
-            const int at = __builtin_ctzll(__ballot(upto > local));
-            const int b = b0 + at, splits = __builtin_amdgcn_readlane(my_splits, at);
-            const int mtiles = __builtin_amdgcn_readlane(mine.mtiles, at);
-            const int item = local - __builtin_amdgcn_readlane(upto, at) + __builtin_amdgcn_readlane(n, at);
+        const int waves = (total + kItems - 1) / kItems;
+        for (; id < before + waves; id += (int64_t)gridDim.x * 4) {
+            const int first_item = (int)(id - before) * kItems;
+            const bool live = first_item + lane / kLanes < total;
+            int local = 0, at = 0;                         // the item, and the lane of its request
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {             // with every lane: reads across lanes need them all
+                const int it = first_item + i < total ? first_item + i : total - 1;
+                const int from = __builtin_ctzll(__ballot(upto > it));
+                if (lane / kLanes == i) {
+                    local = it;
+                    at = from;
+                }
+            }
+            const int b = b0 + at, splits = __shfl(my_splits, at), mtiles = __shfl(mine.mtiles, at);
+            const int item = local - __shfl(upto, at) + __shfl(n, at);
             const int r = item / a.Hq, h = item - r * a.Hq;
             const int hk = h / a.G, mrow = r * a.G + (h - hk * a.G), mt = mrow / MT, in = mrow - mt * MT;
-            const int64_t first = (int64_t)partials_before + __builtin_amdgcn_readlane(partials_upto, at) -
-                                  __builtin_amdgcn_readlane(partials, at) + (int64_t)hk * splits * mtiles + mt;
+            const int64_t first = (int64_t)partials_before + __shfl(partials_upto, at) - __shfl(partials, at) +
+                                  (int64_t)hk * splits * mtiles + mt;
             const float* part = partial + first * (MT * (D + 2));
             const int64_t step = (int64_t)mtiles * (MT * (D + 2));
-            float top = -INFINITY;
-            for (int s = lane; s < splits; s += 64) top = fmaxf(top, part[s * step + in]);
+            const int d = lane % kLanes * 4;
+            float m = -INFINITY, l = 0;
+            f32x4 o = {};
+            for (int s0 = 0; s0 < splits; s0 += 4) {
+                float ms[4], ls[4];
+                f32x4 os[4];
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-            const float base = top == -INFINITY ? 0.0f : top;
-            float l = 0, o[E] = {};
-#pragma unroll 4
-            for (int s = 0; s < splits; ++s) {
-                const float* p = part + s * step;
-                const float ms = p[in], ls = p[MT + in];
-                // l = 0: nothing seen, its sums are zeros (and m may be -inf)
-                const float w = ls == 0 ? 0.0f : exp2f(ms - base);
-                l += w * ls;
+                for (int i = 0; i < 4; ++i) {
+                    const float* p = part + (s0 + i < splits ? s0 + i : s0) * step;
+                    ms[i] = p[in];
+                    ls[i] = s0 + i < splits ? p[MT + in] : 0.0f;
+                    os[i] = *(const f32x4*)(p + 2 * MT + (int64_t)in * D + d);
+                }
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] += w * p[2 * MT + (int64_t)in * D + lane * E + e];
+                for (int i = 0; i < 4; ++i) {
+                    if (ls[i] == 0) continue;              // nothing seen: its sums are zeros (and m may be -inf)
+                    const float mm = fmaxf(m, ms[i]);
+                    const float base = mm == -INFINITY ? 0.0f : mm;
+                    const float w = exp2f(m - base), v = exp2f(ms[i] - base);
+                    m = mm;
+                    l = l * w + ls[i] * v;
+                    // (m = -inf: o is 0, and so is w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = o[e] * w + os[i][e] * v;
+                }
             }
+            if (!live) continue;
             const float inv = l == 0 ? 0.0f : 1.0f / l;
             const int64_t row = (int64_t)b * a.c.rows + r;
-            uint16_t* const out = a.out + row * a.out_stride + (int64_t)h * D + lane * E;
+            s16x4 y;
 #pragma unroll
-            for (int e = 0; e < E; ++e) out[e] = T::put(l == 0 ? 0.0f : o[e] * inv);
-            if (a.lse && lane == 0)
-                a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+            for (int e = 0; e < 4; ++e) y[e] = (short)T::put(l == 0 ? 0.0f : o[e] * inv);
+            *(s16x4*)(a.out + row * a.out_stride + (int64_t)h * D + d) = y;
+            if (a.lse && d == 0) a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         }
-        before += total;
+        before += waves;
         partials_before += __builtin_amdgcn_readlane(partials_upto, 63);
     }
 }
@@ -655,6 +711,7 @@ __global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, int slots
 // ---------------------------------------------------------------------------
 
 constexpr int kCus = 256;
+constexpr int kPlanBytes = 256;    // of the workspace: the chunk's size
 
 // Row tile by the rows of a key head: up to 32 rows the waves share out the
 // keys, up to 64 both, beyond that the rows.
@@ -677,53 +734,59 @@ int64_t max_jobs(const ChunkArgs& c, int Hkv, int G, int mt, int slots) {
 }
 
 template <class T, int D, int WM, int WK, int KT, int PER_CU>
-hipError_t run(const AttentionArgs& a, float* partial, hipStream_t stream) {
+hipError_t run(const AttentionArgs& a, void* workspace, hipStream_t stream) {
     using S = Shape<T, D, WM, WK, KT>;
     const int slots = slots_for(S::kMt, D);
     const int64_t jobs = 8 * max_jobs(a.c, a.kv.Hkv, a.G, S::kMt, slots);
     const auto kernel = attention_kernel<T, D, WM, WK, KT, PER_CU>;
-    kernel<<<(unsigned)jobs, S::kThreads, S::kLds, stream>>>(a, slots, partial);
+    int* const plan = (int*)workspace;
+    float* const partial = (float*)((char*)workspace + kPlanBytes);
+    kernel<<<(unsigned)jobs, S::kThreads, S::kLds, stream>>>(a, slots, plan, partial);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t waves = (int64_t)a.c.B * a.c.rows * a.Hq;
-    const unsigned grid = waves < 4 * 4 * kCus ? (unsigned)((waves + 3) / 4) : 4 * kCus;
-    combine_kernel<T, D, S::kMt><<<grid, 256, 0, stream>>>(a, slots, partial);
+    const int64_t waves = ((int64_t)a.c.B * a.c.rows * a.Hq * (D / 4) + 63) / 64;
+    const unsigned grid = waves < 4 * 8 * kCus ? (unsigned)((waves + 3) / 4) : 8 * kCus;
+    combine_kernel<T, D, S::kMt><<<grid, 256, 0, stream>>>(a, plan, partial);
     return hipGetLastError();
 }
 
 template <class T, int D>
-hipError_t run_rows(const AttentionArgs& a, float* partial, hipStream_t stream) {
+hipError_t run_rows(const AttentionArgs& a, void* workspace, hipStream_t stream) {
     const int mt = tile_rows(a.c, a.G);
     if constexpr (D == 256) {
-        if (mt == 32) return run<T, D, 1, 2, 32, 1>(a, partial, stream);
-        if (mt == 64) return run<T, D, 2, 1, 32, 1>(a, partial, stream);
-        return run<T, D, 4, 1, 64, 1>(a, partial, stream);
+        if (mt == 32) return run<T, D, 1, 2, 32, 1>(a, workspace, stream);
+        if (mt == 64) return run<T, D, 2, 1, 64, 1>(a, workspace, stream);
+        return run<T, D, 4, 1, 64, 1>(a, workspace, stream);
     } else {
-        if (mt == 32) return run<T, D, 1, 4, 32, D == 64 ? 2 : 1>(a, partial, stream);
-        if (mt == 64) return run<T, D, 2, 2, 32, 2>(a, partial, stream);
-        return run<T, D, 4, 1, 64, 2>(a, partial, stream);
+        if (mt == 32) return run<T, D, 1, 4, 32, D == 64 ? 2 : 1>(a, workspace, stream);
+        if (mt == 64) return run<T, D, 2, 2, 32, 2>(a, workspace, stream);
+        return run<T, D, 4, 1, 64, 2>(a, workspace, stream);
     }
 }
 
 template <class T>
-hipError_t run_type(const AttentionArgs& a, float* partial, hipStream_t stream) {
+hipError_t run_type(const AttentionArgs& a, void* workspace, hipStream_t stream) {
     switch (a.kv.D) {
-    case 64: return run_rows<T, 64>(a, partial, stream);
-    case 128: return run_rows<T, 128>(a, partial, stream);
-    default: return run_rows<T, 256>(a, partial, stream);
+    case 64: return run_rows<T, 64>(a, workspace, stream);
+    case 128: return run_rows<T, 128>(a, workspace, stream);
+    default: return run_rows<T, 256>(a, workspace, stream);
     }
 }
 
 }  // namespace
 
 size_t attention_workspace(const ChunkArgs& c, int Hkv, int Hq, int D) {
-    const int G = Hq / Hkv, mt = tile_rows(c, G);
-    return (size_t)(8 * slots_for(mt, D)) * mt * (D + 2) * sizeof(float);
+    const int G = Hq / Hkv, mt = tile_rows(c, G), slots = slots_for(mt, D);
+    const int64_t segments = (int64_t)c.B * Hkv * (((int64_t)c.rows * G + mt - 1) / mt);
+    // partials_of(): at most work / c <= 4 slots of them and one a split
+    // segment, of which there are at most work / c, too
+    const int64_t partials = 4 * slots + (segments < 4 * slots ? segments : 4 * slots);
+    return (size_t)partials * mt * (D + 2) * sizeof(float) + kPlanBytes;
 }
 
 hipError_t launch_attention(const AttentionArgs& a, int dtype, void* workspace, hipStream_t stream) {
-    return dtype == DT_DTYPE_BF16 ? run_type<Bf16>(a, (float*)workspace, stream)
-                                  : run_type<F16>(a, (float*)workspace, stream);
+    return dtype == DT_DTYPE_BF16 ? run_type<Bf16>(a, workspace, stream)
+                                  : run_type<F16>(a, workspace, stream);
 }
 
 }  // namespace dt

@@ -457,7 +457,7 @@ typedef struct dt_logits_params {
     const int32_t* history_len;/* [B], clamped to 0..history_max; needed with history */
     const int32_t* prompt_len; /* [B], clamped to 0..history_len; NULL = 0: the first of a
                                   request's history are its prompt, the rest were generated */
-    const int32_t* node_tokens;/* [B][n_max] tokens of the tree's nodes, or NULL */
+    const int32_t* node_tokens;/* [B][n_max] tokens of the tree's nodes (n_max <= 1024), or NULL */
     const uint32_t* node_mask; /* [B][n_max][ceil(n_max/32)] as dt_tree_out; needed with node_tokens */
     const float* repetition;   /* [B] > 0, or NULL = 1 */
     const float* frequency;    /* [B] or NULL = 0 */

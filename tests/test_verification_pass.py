@@ -198,7 +198,8 @@ def test_attention_limits_of_a_call():
     (dict(history=FAKE, history_max=8), BAD), (dict(history_max=-1), BAD), (dict(n_bias=-1), BAD),
     (dict(node_tokens=FAKE), BAD), (dict(bias_ids=FAKE, n_bias=2), BAD), (dict(allow=FAKE), BAD),
     (dict(allow=FAKE, allow_rows=13), BAD), (dict(n_nodes=FAKE + 2), BAD), (dict(presence=FAKE + 1), BAD),
-    (dict(B=65536), LIMIT), (dict(V=1 << 26), LIMIT), (dict(n_bias=65535), LIMIT), (dict(lead=65536), LIMIT),
+    (dict(B=65536), LIMIT), (dict(V=1 << 26), LIMIT), (dict(n_bias=65535), LIMIT),
+    (dict(node_tokens=FAKE, node_mask=FAKE, n_max=1025), LIMIT), (dict(lead=65536), LIMIT),
 ])
 def test_logits_refusals(kw, status):
     p = _logits(**kw)
