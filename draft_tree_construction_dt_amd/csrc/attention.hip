@@ -78,16 +78,6 @@ __device__ inline Request request_of(const AttentionArgs& a, int b, int mt_rows)
     return q;
 }
 
-__device__ inline int wave_prefix(int x, int lane) {      // inclusive
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);      // row_shr:1 ... within rows of 16
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
-    const int a = __builtin_amdgcn_readlane(x, 15), b = __builtin_amdgcn_readlane(x, 31),
-              c = __builtin_amdgcn_readlane(x, 47);
-    return x + (lane >= 16 ? a : 0) + (lane >= 32 ? b : 0) + (lane >= 48 ? c : 0);
-}
-
 __device__ inline int64_t uniform(int64_t x) {
     return (int64_t)((u64)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) |
                      (u64)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32);
@@ -163,10 +153,10 @@ __device__ inline Job job_of(const AttentionArgs& a, const Request& q0, int mt_r
     for (int b0 = 0; b0 < a.c.B; b0 += 64) {
         const Request q = b0 ? request_of(a, b0 + lane, mt_rows) : q0;
         const int splits = splits_of(q, c), groups = q.rows ? a.kv.Hkv * splits : 0;
-        const int groups_upto = wave_prefix(groups, lane);
+        const int groups_upto = wave_prefix_i32(groups, lane);
         const int first = (x - (groups_before + groups_upto - groups)) & 7;
         const int n = first < groups ? ((groups - first + 7) >> 3) * q.mtiles : 0;
-        const int upto = wave_prefix(n, lane);
+        const int upto = wave_prefix_i32(n, lane);
         const u64 hit = __ballot(before + upto > y);
         const int partials = partials_of(a, q, splits);
         if (hit) {
@@ -642,7 +632,7 @@ __global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, const int
         const Request mine = request_of(a, b0 + lane, MT);
         const int my_splits = splits_of(mine, c), partials = partials_of(a, mine, my_splits);
         const int n = partials ? mine.rows * a.Hq : 0;     // below 2^31 over the call
-        const int upto = wave_prefix(n, lane), partials_upto = wave_prefix(partials, lane);
+        const int upto = wave_prefix_i32(n, lane), partials_upto = wave_prefix_i32(partials, lane);
         const int total = __builtin_amdgcn_readlane(upto, 63);
         const int waves = (total + kItems - 1) / kItems;
         for (; id < before + waves; id += (int64_t)gridDim.x * 4) {

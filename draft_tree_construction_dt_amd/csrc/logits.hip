@@ -8,20 +8,24 @@
 // the table before its row and taken out behind it, by the few nodes whose
 // tokens lie in the chunk at all (most chunks have none).
 //
-// The kernel is bound by memory: every logit is read and written once, and the
-// table costs its LDS reads (8 words of 16 bytes read).  The table is kept as
+// The kernel is bound by memory: every logit is read and written once.  What
+// stands in the way is latency, so the tables are kept small (8 workgroups a
+// compute unit): counts in 16 bits where the history is short enough, biases
+// by their rank among the chunk's biased tokens.  The counts are kept as
 // [t % 8][t / 8], so that a wave's reads of a vector's j-th token are
 // consecutive words whatever the row's alignment.
 #include <math.h>
 
 #include "pass.h"
+#include "wave.h"
 
 namespace dt {
 namespace {
 
-constexpr uint32_t kPrompt = 0x80000000u;  // the token occurs in the prompt
-constexpr int kMaxNodes = kMaxCommitNodes;
+constexpr int kChunk = 4096;               // tokens of a workgroup
+constexpr int kWords = kChunk / 32;        // of a bit a token
 constexpr int64_t kWorkgroups = 2048;
+constexpr int kMaxShort = 32767;           // occurrences that 15 bits count
 
 template <class T>
 struct Io;
@@ -47,35 +51,75 @@ struct Io<uint16_t> {
     static __device__ inline uint16_t put(float x) { return Bf16::put(x); }
 };
 
-template <class T, int CHUNK, bool BIAS>
+// How often each token of the chunk was generated, and a flag (the highest
+// bit of its count) for one that occurs in the prompt: 32 bits a token, or 16
+// with tokens t and t + kChunk / 2 in one word.
+template <bool WIDE>
+struct Counts {
+    static constexpr int kSize = WIDE ? kChunk : kChunk / 2;
+    static constexpr uint32_t kPrompt = WIDE ? 0x80000000u : 0x8000u;
+    static __device__ inline int word(int t) {
+        const int u = WIDE ? t : t & (kChunk / 2 - 1);
+        return (u & 7) * (kSize / 8) + (u >> 3);
+    }
+    static __device__ inline int shift(int t) { return WIDE ? 0 : (t / (kChunk / 2)) * 16; }
+    static __device__ inline uint32_t get(const uint32_t* s, int t) {
+        const uint32_t w = s[word(t)] >> shift(t);
+        return WIDE ? w : w & 0xFFFFu;
+    }
+    static __device__ inline void add(uint32_t* s, int t, int by) { atomicAdd(&s[word(t)], (uint32_t)by << shift(t)); }
+    static __device__ inline void prompt(uint32_t* s, int t) { atomicOr(&s[word(t)], kPrompt << shift(t)); }
+};
+
+// Eight bits (of which the caller wants the first few) from bit `at` of a
+// bitmap in LDS, `last` the last bit that is wanted.
+__device__ inline uint32_t bits_at(const uint32_t* bitmap, int at, int last) {
+    const uint8_t* const p = (const uint8_t*)bitmap;
+    return (p[at >> 3] | (uint32_t)p[last >> 3] << 8) >> (at & 7);
+}
+
+template <class T, bool WIDE, bool BIAS>
 __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
-    constexpr int kVec = Io<T>::kVec, kPer = CHUNK / kVec / 256;     // full vectors of a thread and row
-    __shared__ uint32_t s_cnt[CHUNK];
-    __shared__ uint32_t s_bias[BIAS ? CHUNK : 1];
-    __shared__ uint32_t s_node[kMaxNodes];                 // node << 16 | place in the chunk
+    using C = Counts<WIDE>;
+    constexpr int kVec = Io<T>::kVec, kPer = kChunk / kVec / 256;    // full vectors of a thread and row
+    extern __shared__ uint32_t lds[];
+    uint32_t* const s_cnt = lds;
+    uint32_t* const s_touched = s_cnt + C::kSize;          // tokens with a count, or on some node's path
+    uint32_t* const s_biased = s_touched + kWords;         // tokens with a bias
+    uint32_t* const s_rank = s_biased + (BIAS ? kWords : 0);         // biased tokens before each 32
+    uint32_t* const s_bias = s_rank + (BIAS ? kWords : 0);           // their biases, by rank
+    uint32_t* const s_node = s_bias + (BIAS ? (a.n_bias < kChunk ? a.n_bias : kChunk) : 0);  // node << 16 | token
     __shared__ int s_nodes;
-    const int b = blockIdx.y, v0 = blockIdx.x * CHUNK, tid = threadIdx.x;
-    const int len = a.V - v0 < CHUNK ? a.V - v0 : CHUNK;
+    const int b = blockIdx.y, v0 = blockIdx.x * kChunk, tid = threadIdx.x, lane = tid & 63;
+    const int len = a.V - v0 < kChunk ? a.V - v0 : kChunk;
     int nn = a.n_nodes ? a.n_nodes[b] : a.n_max;
     nn = nn < 0 ? 0 : (nn > a.n_max ? a.n_max : nn);
     const int rows = a.lead + nn;
     const int step = gridDim.z;
     if ((int)blockIdx.z >= rows) return;
-    const auto place = [](int t) { return (t & 7) * (CHUNK / 8) + (t >> 3); };
 
     // A row's vectors begin at its 16-byte boundaries: vector k holds the
     // chunk's tokens k * kVec - miss + 0 .. kVec - 1.  Vectors that reach out
     // of the chunk are done token by token.
     const auto miss_of = [&](int r) { return (int)((((int64_t)b * a.rows + r) * a.V + v0) & (kVec - 1)); };
-    const auto allow_of = [&](int r) -> const uint8_t* {
-        if (!a.allow || r >= rows) return nullptr;
-        const int64_t row = (int64_t)b * a.rows + r;
-        const int64_t i = a.allow_index ? a.allow_index[row] : row;
-        return i >= 0 && i < a.allow_rows ? (const uint8_t*)(a.allow + i * ((a.V + 31) >> 5)) : nullptr;
+    // The mask row of this workgroup's i-th row; 64 indexes are read at once, a
+    // lane each, so that no row waits for its own.
+    int index = -1;
+    const auto allow_of = [&](int i) -> const uint8_t* {
+        if (!a.allow || (int)blockIdx.z + i * step >= rows) return nullptr;
+        const int64_t row0 = (int64_t)b * a.rows + blockIdx.z;
+        int64_t at = row0 + (int64_t)i * step;
+        if (a.allow_index) {
+            const int mine = i + lane;
+            if ((i & 63) == 0)
+                index = (int)blockIdx.z + mine * step < rows ? a.allow_index[row0 + (int64_t)mine * step] : -1;
+            at = __builtin_amdgcn_readlane(index, i & 63);
+        }
+        return at >= 0 && at < a.allow_rows ? (const uint8_t*)(a.allow + at * ((a.V + 31) >> 5)) : nullptr;
     };
     struct Row {
         u32x4 x[kPer];
-        uint32_t ok[kPer];
+        uint8_t lo[kPer], hi[kPer];                        // the mask bytes of a vector's first and last token
     };
     const auto load = [&](int r, const uint8_t* allow, Row& row) {
         const int miss = miss_of(r);
@@ -83,85 +127,106 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             const int lo = (tid + 256 * u) * kVec - miss;
-            row.ok[u] = ~0u;
             if (lo < 0 || lo + kVec > len) continue;
             row.x[u] = *(const u32x4*)(in + lo);
             if (allow) {
-                const int bit = v0 + lo, last = (bit + kVec - 1) >> 3;
-                row.ok[u] = (allow[bit >> 3] | (uint32_t)allow[last] << 8) >> (bit & 7);
-                if (last == bit >> 3) row.ok[u] = (uint32_t)allow[last] >> (bit & 7);
+                row.lo[u] = allow[(v0 + lo) >> 3];
+                row.hi[u] = miss ? allow[(v0 + lo + kVec - 1) >> 3] : 0;
             }
         }
     };
     Row cur;
     int r = blockIdx.z;
-    const uint8_t* allow = allow_of(r);
+    const uint8_t* allow = allow_of(0);
     load(r, allow, cur);
 
-    for (int i = tid; i < CHUNK; i += 256) {
-        s_cnt[i] = 0;
-        if (BIAS) s_bias[i] = 0;
-    }
+    // the tables
+    const int cleared = (int)(s_node - lds);
+    for (int i = tid; i < cleared; i += 256) lds[i] = 0;
     if (tid == 0) s_nodes = 0;
     __syncthreads();
+    const auto touch = [&](uint32_t t) { atomicOr(&s_touched[t >> 5], 1u << (t & 31)); };
     if (a.history) {
         int n = a.history_len[b];
         n = n < 0 ? 0 : (n > a.history_max ? a.history_max : n);
         const int np = a.prompt_len ? a.prompt_len[b] : 0;
         const int32_t* const h = a.history + (int64_t)b * a.history_max;
-        for (int i0 = tid; i0 < n; i0 += 4 * 256) {
-            uint32_t t[4];
+        constexpr int kDeep = 16;                          // ids of a thread in flight
+        for (int i0 = tid; i0 < n; i0 += kDeep * 256) {
+            uint32_t t[kDeep];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) t[j] = i0 + 256 * j < n ? (uint32_t)(h[i0 + 256 * j] - v0) : ~0u;
+            for (int j = 0; j < kDeep; ++j) t[j] = i0 + 256 * j < n ? (uint32_t)(h[i0 + 256 * j] - v0) : ~0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kDeep; ++j) {
                 if (t[j] >= (uint32_t)len) continue;
-                uint32_t* const c = &s_cnt[place((int)t[j])];
-                if (i0 + 256 * j < np) atomicOr(c, kPrompt);
-                else atomicAdd(c, 1u);
+                if (i0 + 256 * j < np) C::prompt(s_cnt, (int)t[j]);
+                else C::add(s_cnt, (int)t[j], 1);
+                touch(t[j]);
             }
         }
     }
+    const int32_t* const bias_ids = a.bias_ids + (int64_t)b * a.n_bias;
     if (BIAS) {
         for (int i = tid; i < a.n_bias; i += 256) {
-            const uint32_t t = (uint32_t)(a.bias_ids[(int64_t)b * a.n_bias + i] - v0);
-            if (t < (uint32_t)len) atomicMax(&s_bias[place((int)t)], (uint32_t)i + 1);
+            const uint32_t t = (uint32_t)(bias_ids[i] - v0);
+            if (t < (uint32_t)len) atomicOr(&s_biased[t >> 5], 1u << (t & 31));
         }
     }
     if (a.node_tokens) {
         for (int i = tid; i < nn; i += 256) {
             const uint32_t t = (uint32_t)(a.node_tokens[(int64_t)b * a.n_max + i] - v0);
-            if (t < (uint32_t)len) s_node[atomicAdd(&s_nodes, 1)] = (uint32_t)i << 16 | t;
+            if (t >= (uint32_t)len) continue;
+            s_node[atomicAdd(&s_nodes, 1)] = (uint32_t)i << 16 | t;
+            touch(t);
         }
     }
     __syncthreads();
     const int nodes = s_nodes;
+    const auto rank_of = [&](int t) {                      // biased tokens before t
+        return (int)s_rank[t >> 5] + __popc(s_biased[t >> 5] & ((1u << (t & 31)) - 1));
+    };
+    if (BIAS) {
+        if (tid < 64) {                                    // two words a lane
+            static_assert(kWords == 128, "two words a lane");
+            const int x = __popc(s_biased[2 * lane]), y = __popc(s_biased[2 * lane + 1]);
+            const int upto = wave_prefix_i32(x + y, lane);
+            s_rank[2 * lane] = upto - x - y;
+            s_rank[2 * lane + 1] = upto - y;
+        }
+        __syncthreads();
+        for (int i = tid; i < a.n_bias; i += 256) {
+            const uint32_t t = (uint32_t)(bias_ids[i] - v0);
+            if (t < (uint32_t)len) atomicMax(&s_bias[rank_of((int)t)], (uint32_t)i + 1);
+        }
+        __syncthreads();
+        for (int i = tid; i < (int)(s_node - s_bias); i += 256)      // from the last entry's number to its value
+            if (s_bias[i]) s_bias[i] = __float_as_uint(a.bias[(int64_t)b * a.n_bias + s_bias[i] - 1]);
+        __syncthreads();
+    }
     const float rep = a.repetition ? a.repetition[b] : 1.0f, freq = a.frequency ? a.frequency[b] : 0.0f,
                 pres = a.presence ? a.presence[b] : 0.0f, inv = 1.0f / rep;
-    // token t of the chunk; false where nothing touches it
-    const auto apply = [&](int t, float& x) {
-        const uint32_t c = s_cnt[place(t)], bi = BIAS ? s_bias[place(t)] : 0;
-        const float n = (float)(c & ~kPrompt);
+    // the penalties of token t; false where there are none
+    const auto penalise = [&](int t, float& x) {
+        const uint32_t c = C::get(s_cnt, t), n = c & ~C::kPrompt;
         const float y = c ? x * (x > 0 ? inv : rep) : x;
-        x = (c & ~kPrompt) ? y - __builtin_fmaf(freq, n, pres) : y;
-        if (BIAS && bi) x += a.bias[(int64_t)b * a.n_bias + bi - 1];
-        return (c | bi) != 0;
+        x = n ? y - __builtin_fmaf(freq, (float)n, pres) : y;
+        return c != 0;
     };
 
-    for (; r < rows; r += step) {
+    for (int i = 1; r < rows; r += step, ++i) {
         Row next;
-        const uint8_t* const allow_next = allow_of(r + step);
+        const uint8_t* const allow_next = allow_of(i);
         if (r + step < rows) load(r + step, allow_next, next);
         const bool path = nodes > 0 && r >= a.lead;
-        const auto walk = [&](uint32_t by) {
+        const auto walk = [&](int by) {
             const uint32_t* const m = a.node_mask + ((int64_t)b * a.n_max + r - a.lead) * a.mask_words;
-            for (int i = tid; i < nodes; i += 256) {
-                const uint32_t e = s_node[i], node = e >> 16;
-                if (m[node >> 5] >> (node & 31) & 1) atomicAdd(&s_cnt[place((int)(e & 0xFFFF))], by);
+            for (int k = tid; k < nodes; k += 256) {
+                const uint32_t e = s_node[k], node = e >> 16;
+                if (m[node >> 5] >> (node & 31) & 1) C::add(s_cnt, (int)(e & 0xFFFF), by);
             }
         };
         if (path) {
-            walk(1u);
+            walk(1);
             __syncthreads();
         }
         const int miss = miss_of(r);
@@ -170,7 +235,12 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
         const auto single = [&](int t) {
             T y = in[t];
             float x = Io<T>::get(y);
-            if (apply(t, x)) y = Io<T>::put(x);
+            bool changed = penalise(t, x);
+            if (BIAS && s_biased[t >> 5] >> (t & 31) & 1) {
+                x += __uint_as_float(s_bias[rank_of(t)]);
+                changed = true;
+            }
+            if (changed) y = Io<T>::put(x);
             if (allow && !(allow[(v0 + t) >> 3] >> ((v0 + t) & 7) & 1)) y = Io<T>::put(-INFINITY);
             out[t] = y;
         };
@@ -182,18 +252,35 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
                 continue;
             }
             u32x4 y = cur.x[u];
+            constexpr uint32_t kAll = (1u << kVec) - 1;
+            const uint32_t counted = bits_at(s_touched, lo, lo + kVec - 1) & kAll;
+            const uint32_t biased = BIAS ? bits_at(s_biased, lo, lo + kVec - 1) & kAll : 0;
+            if (__any((counted | biased) != 0)) {
+                int rank = 0;
+                if (BIAS && biased) rank = rank_of(lo);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                float x = Io<T>::get(cur.x[u], j);
-                if (apply(lo + j, x)) Io<T>::put(y, j, x);
-                if (!(cur.ok[u] >> j & 1)) Io<T>::put(y, j, -INFINITY);
+                for (int j = 0; j < kVec; ++j) {
+                    float x = Io<T>::get(cur.x[u], j);
+                    bool changed = penalise(lo + j, x);
+                    if (BIAS && biased >> j & 1) {
+                        x += __uint_as_float(s_bias[rank++]);
+                        changed = true;
+                    }
+                    if (changed) Io<T>::put(y, j, x);
+                }
+            }
+            if (allow) {
+                const uint32_t ok = (cur.lo[u] | (uint32_t)cur.hi[u] << 8) >> ((v0 + lo) & 7);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (!(ok >> j & 1)) Io<T>::put(y, j, -INFINITY);
             }
             *(u32x4*)(out + lo) = y;
         }
-        if (miss > 0 && tid < miss && CHUNK - miss + tid < len) single(CHUNK - miss + tid);
+        if (miss > 0 && tid < miss && kChunk - miss + tid < len) single(kChunk - miss + tid);
         if (path) {
             __syncthreads();
-            walk(~0u);
+            walk(-1);
             __syncthreads();
         }
         cur = next;
@@ -201,23 +288,27 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
     }
 }
 
-template <class T, int CHUNK>
+template <class T, bool WIDE>
 hipError_t run(const LogitsArgs& a, hipStream_t stream) {
-    const int64_t chunks = (a.V + CHUNK - 1) / CHUNK;
+    const int64_t chunks = (a.V + kChunk - 1) / kChunk;
     // a table serves several rows once there are some workgroups a compute unit
     int64_t z = (kWorkgroups + chunks * a.B - 1) / (chunks * a.B);
     z = z < a.rows ? z : a.rows;
     const dim3 grid((unsigned)chunks, (unsigned)a.B, (unsigned)z);
-    if (a.n_bias > 0) logits_kernel<T, CHUNK, true><<<grid, 256, 0, stream>>>(a);
-    else logits_kernel<T, CHUNK, false><<<grid, 256, 0, stream>>>(a);
+    const int biases = a.n_bias < kChunk ? a.n_bias : kChunk;
+    const size_t words = Counts<WIDE>::kSize + kWords + (a.n_bias > 0 ? 2 * kWords + biases : 0) +
+                         (a.node_tokens ? a.n_max : 0);
+    if (a.n_bias > 0) logits_kernel<T, WIDE, true><<<grid, 256, words * 4, stream>>>(a);
+    else logits_kernel<T, WIDE, false><<<grid, 256, words * 4, stream>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_logits(const LogitsArgs& a, int dtype, hipStream_t stream) {
-    if (dtype == DT_DTYPE_F32) return run<float, 4096>(a, stream);
-    return run<uint16_t, 4096>(a, stream);
+    const bool wide = (int64_t)a.history_max + (a.node_tokens ? a.n_max : 0) > kMaxShort;
+    if (dtype == DT_DTYPE_F32) return wide ? run<float, true>(a, stream) : run<float, false>(a, stream);
+    return wide ? run<uint16_t, true>(a, stream) : run<uint16_t, false>(a, stream);
 }
 
 }  // namespace dt

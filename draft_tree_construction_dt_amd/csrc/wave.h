@@ -229,6 +229,18 @@ __device__ __forceinline__ int wave_add_i32(int v) {
            (__builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48));
 }
 
+// inclusive prefix sums over the lanes: shifts within the rows of 16, then
+// the sums of the rows before
+__device__ __forceinline__ int wave_prefix_i32(int v, int lane) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);      // row_shr:1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    const int a = __builtin_amdgcn_readlane(v, 15), b = __builtin_amdgcn_readlane(v, 31),
+              c = __builtin_amdgcn_readlane(v, 47);
+    return v + (lane >= 16 ? a : 0) + (lane >= 32 ? b : 0) + (lane >= 48 ? c : 0);
+}
+
 __device__ __forceinline__ int wave_min_i32(int v) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) v = min(v, dpp_step(v, s));
