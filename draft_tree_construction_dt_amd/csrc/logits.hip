@@ -26,6 +26,13 @@ constexpr int kChunk = 4096;               // tokens of a workgroup
 constexpr int kWords = kChunk / 32;        // of a bit a token
 constexpr int64_t kWorkgroups = 2048;
 constexpr int kMaxShort = 32767;           // occurrences that 15 bits count
+// A lane goes through its vector's few entries one by one; a wave in which a
+// lane has more does all tokens of its vectors at once (the benchmark's draft
+// logits behind 4096 tokens: all at once 91 us, one by one 78, chosen 70).
+constexpr int kFew = 3;
+// Outputs that no cache would keep are written past the caches (91 -> 100 us
+// without, at 156 MB).
+constexpr int64_t kStreamOut = 64 << 20;
 
 template <class T>
 struct Io;
@@ -34,6 +41,14 @@ struct Io<float> {
     static constexpr int kVec = 4;
     static __device__ inline float get(const u32x4& v, int j) { return __uint_as_float(v[j]); }
     static __device__ inline void put(u32x4& v, int j, float x) { v[j] = __float_as_uint(x); }
+    // ... for a j that is not known when compiled
+    static __device__ inline float pick(const u32x4& v, int j) {
+        return __uint_as_float(j & 2 ? (j & 1 ? v[3] : v[2]) : (j & 1 ? v[1] : v[0]));
+    }
+    static __device__ inline void set(u32x4& v, int j, float x) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[w] = w == j ? __float_as_uint(x) : v[w];
+    }
     static __device__ inline float get(float x) { return x; }
     static __device__ inline float put(float x) { return x; }
 };
@@ -46,6 +61,17 @@ struct Io<uint16_t> {
     static __device__ inline void put(u32x4& v, int j, float x) {
         const uint32_t h = Bf16::put(x);
         v[j >> 1] = j & 1 ? (v[j >> 1] & 0xFFFFu) | h << 16 : (v[j >> 1] & 0xFFFF0000u) | h;
+    }
+    static __device__ inline uint32_t word(const u32x4& v, int j) {
+        return j & 4 ? (j & 2 ? v[3] : v[2]) : (j & 2 ? v[1] : v[0]);
+    }
+    static __device__ inline float pick(const u32x4& v, int j) {
+        return __uint_as_float(j & 1 ? word(v, j) & 0xFFFF0000u : word(v, j) << 16);
+    }
+    static __device__ inline void set(u32x4& v, int j, float x) {
+        const uint32_t h = Bf16::put(x), old = word(v, j), y = j & 1 ? (old & 0xFFFFu) | h << 16 : (old & 0xFFFF0000u) | h;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[w] = w == j >> 1 ? y : v[w];
     }
     static __device__ inline float get(uint16_t x) { return Bf16::get(x); }
     static __device__ inline uint16_t put(float x) { return Bf16::put(x); }
@@ -255,7 +281,8 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
             constexpr uint32_t kAll = (1u << kVec) - 1;
             const uint32_t counted = bits_at(s_touched, lo, lo + kVec - 1) & kAll;
             const uint32_t biased = BIAS ? bits_at(s_biased, lo, lo + kVec - 1) & kAll : 0;
-            if (__any((counted | biased) != 0)) {
+            uint32_t todo = counted | biased;
+            if (__any(__popc(todo) > kFew)) {
                 int rank = 0;
                 if (BIAS && biased) rank = rank_of(lo);
 #pragma unroll
@@ -268,6 +295,18 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
                     }
                     if (changed) Io<T>::put(y, j, x);
                 }
+            } else {
+                while (todo) {
+                    const int j = __builtin_ctz(todo);
+                    todo &= todo - 1;
+                    float x = Io<T>::pick(y, j);
+                    bool changed = penalise(lo + j, x);
+                    if (BIAS && biased >> j & 1) {
+                        x += __uint_as_float(s_bias[rank_of(lo + j)]);
+                        changed = true;
+                    }
+                    if (changed) Io<T>::set(y, j, x);
+                }
             }
             if (allow) {
                 const uint32_t ok = (cur.lo[u] | (uint32_t)cur.hi[u] << 8) >> ((v0 + lo) & 7);
@@ -275,7 +314,8 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
                 for (int j = 0; j < kVec; ++j)
                     if (!(ok >> j & 1)) Io<T>::put(y, j, -INFINITY);
             }
-            *(u32x4*)(out + lo) = y;
+            if (a.stream_out) __builtin_nontemporal_store(y, (u32x4*)(out + lo));
+            else *(u32x4*)(out + lo) = y;
         }
         if (miss > 0 && tid < miss && kChunk - miss + tid < len) single(kChunk - miss + tid);
         if (path) {
@@ -294,12 +334,14 @@ hipError_t run(const LogitsArgs& a, hipStream_t stream) {
     // a table serves several rows once there are some workgroups a compute unit
     int64_t z = (kWorkgroups + chunks * a.B - 1) / (chunks * a.B);
     z = z < a.rows ? z : a.rows;
+    LogitsArgs args = a;
+    args.stream_out = (int64_t)a.B * a.rows * a.V * (int64_t)sizeof(T) > kStreamOut;
     const dim3 grid((unsigned)chunks, (unsigned)a.B, (unsigned)z);
     const int biases = a.n_bias < kChunk ? a.n_bias : kChunk;
     const size_t words = Counts<WIDE>::kSize + kWords + (a.n_bias > 0 ? 2 * kWords + biases : 0) +
                          (a.node_tokens ? a.n_max : 0);
-    if (a.n_bias > 0) logits_kernel<T, WIDE, true><<<grid, 256, words * 4, stream>>>(a);
-    else logits_kernel<T, WIDE, false><<<grid, 256, words * 4, stream>>>(a);
+    if (a.n_bias > 0) logits_kernel<T, WIDE, true><<<grid, 256, words * 4, stream>>>(args);
+    else logits_kernel<T, WIDE, false><<<grid, 256, words * 4, stream>>>(args);
     return hipGetLastError();
 }
 
