@@ -28,11 +28,9 @@ constexpr int64_t kWorkgroups = 2048;
 constexpr int kMaxShort = 32767;           // occurrences that 15 bits count
 // A lane goes through its vector's few entries one by one; a wave in which a
 // lane has more does all tokens of its vectors at once (the benchmark's draft
-// logits behind 4096 tokens: all at once 91 us, one by one 78, chosen 70).
+// logits behind 4096 tokens, inputs in the last-level cache: all at once
+// 91 us, one by one 78, chosen 70).
 constexpr int kFew = 3;
-// Outputs that no cache would keep are written past the caches (91 -> 100 us
-// without, at 156 MB).
-constexpr int64_t kStreamOut = 64 << 20;
 
 template <class T>
 struct Io;
@@ -116,7 +114,7 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
     uint32_t* const s_bias = s_rank + (BIAS ? kWords : 0);           // their biases, by rank
     uint32_t* const s_node = s_bias + (BIAS ? (a.n_bias < kChunk ? a.n_bias : kChunk) : 0);  // node << 16 | token
     __shared__ int s_nodes;
-    const int b = blockIdx.y, v0 = blockIdx.x * kChunk, tid = threadIdx.x, lane = tid & 63;
+    const int b = blockIdx.x, v0 = blockIdx.y * kChunk, tid = threadIdx.x, lane = tid & 63;
     const int len = a.V - v0 < kChunk ? a.V - v0 : kChunk;
     int nn = a.n_nodes ? a.n_nodes[b] : a.n_max;
     nn = nn < 0 ? 0 : (nn > a.n_max ? a.n_max : nn);
@@ -177,7 +175,7 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
         n = n < 0 ? 0 : (n > a.history_max ? a.history_max : n);
         const int np = a.prompt_len ? a.prompt_len[b] : 0;
         const int32_t* const h = a.history + (int64_t)b * a.history_max;
-        constexpr int kDeep = 16;                          // ids of a thread in flight
+        constexpr int kDeep = 8;                           // ids of a thread in flight
         for (int i0 = tid; i0 < n; i0 += kDeep * 256) {
             uint32_t t[kDeep];
 #pragma unroll
@@ -314,8 +312,7 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
                 for (int j = 0; j < kVec; ++j)
                     if (!(ok >> j & 1)) Io<T>::put(y, j, -INFINITY);
             }
-            if (a.stream_out) __builtin_nontemporal_store(y, (u32x4*)(out + lo));
-            else *(u32x4*)(out + lo) = y;
+            *(u32x4*)(out + lo) = y;
         }
         if (miss > 0 && tid < miss && kChunk - miss + tid < len) single(kChunk - miss + tid);
         if (path) {
@@ -334,14 +331,14 @@ hipError_t run(const LogitsArgs& a, hipStream_t stream) {
     // a table serves several rows once there are some workgroups a compute unit
     int64_t z = (kWorkgroups + chunks * a.B - 1) / (chunks * a.B);
     z = z < a.rows ? z : a.rows;
-    LogitsArgs args = a;
-    args.stream_out = (int64_t)a.B * a.rows * a.V * (int64_t)sizeof(T) > kStreamOut;
-    const dim3 grid((unsigned)chunks, (unsigned)a.B, (unsigned)z);
+    // the chunks of low ids first: they hold most entries and take longest
+    // (the draft logits of 64 requests 101 -> 93 us)
+    const dim3 grid((unsigned)a.B, (unsigned)chunks, (unsigned)z);
     const int biases = a.n_bias < kChunk ? a.n_bias : kChunk;
     const size_t words = Counts<WIDE>::kSize + kWords + (a.n_bias > 0 ? 2 * kWords + biases : 0) +
                          (a.node_tokens ? a.n_max : 0);
-    if (a.n_bias > 0) logits_kernel<T, WIDE, true><<<grid, 256, words * 4, stream>>>(args);
-    else logits_kernel<T, WIDE, false><<<grid, 256, words * 4, stream>>>(args);
+    if (a.n_bias > 0) logits_kernel<T, WIDE, true><<<grid, 256, words * 4, stream>>>(a);
+    else logits_kernel<T, WIDE, false><<<grid, 256, words * 4, stream>>>(a);
     return hipGetLastError();
 }
 

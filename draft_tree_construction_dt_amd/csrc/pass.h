@@ -77,7 +77,6 @@ struct LogitsArgs {
     const uint32_t* allow;
     const int32_t* allow_index;
     int allow_rows;
-    bool stream_out;               // set by the launcher: write past the caches
 };
 
 struct CommitArgs {
