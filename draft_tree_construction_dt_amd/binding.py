@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass, field
 from typing import Optional
 
@@ -68,6 +69,16 @@ def _fields(spec):
     return [(name, kinds[kind]) for kind, names in spec for name in names.split()]
 
 
+def _packer(struct_type):
+    """The same structure as bytes from its fields' values, in a third of the
+    time (a call of a few microseconds is made for every layer and token)."""
+    kinds = {ctypes.c_void_p: "P", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f",
+             ctypes.c_size_t: "N"}
+    packer = struct.Struct("@" + "".join(kinds[kind] for _, kind in struct_type._fields_) + "0q")
+    assert packer.size == ctypes.sizeof(struct_type)
+    return packer.pack
+
+
 class _KVCache(ctypes.Structure):
     _fields_ = _fields([("p", "k v page_table"), ("l", "layer_stride page_stride slot_stride head_stride"),
                         ("i", "layers num_pages page_size max_pages Hkv D dtype")])
@@ -97,6 +108,10 @@ class _LogitsParams(ctypes.Structure):
 
 class _CommitParams(ctypes.Structure):
     _fields_ = _fields([("p", "tokens parents target"), ("i", "L"), ("p", "accepted lengths nodes stream")])
+
+
+_pack_append, _pack_attention, _pack_logits, _pack_commit = (
+    _packer(c) for c in (_AppendParams, _AttentionParams, _LogitsParams, _CommitParams))
 
 
 class _TreeOut(ctypes.Structure):
@@ -146,18 +161,13 @@ def _load():
         lib.dt_rope_frequencies.restype = ctypes.c_int
         lib.dt_rope_frequencies.argtypes = [ctypes.c_int32, ctypes.c_int32] + [ctypes.c_double] * 5 + \
             [ctypes.c_void_p, ctypes.POINTER(ctypes.c_float)]
-        lib.dt_kv_append.restype = ctypes.c_int
-        lib.dt_kv_append.argtypes = [ctypes.POINTER(_KVCache), ctypes.POINTER(_Chunk), ctypes.POINTER(_AppendParams)]
-        lib.dt_tree_attention.restype = ctypes.c_int
-        lib.dt_tree_attention.argtypes = [ctypes.POINTER(_KVCache), ctypes.POINTER(_Chunk),
-                                          ctypes.POINTER(_AttentionParams)]
+        for fn in (lib.dt_kv_append, lib.dt_tree_attention, lib.dt_commit_path):
+            fn.restype = ctypes.c_int
+            fn.argtypes = [ctypes.c_void_p] * 3            # kv, chunk, params (a structure or its bytes)
         lib.dt_attention_workspace.restype = ctypes.c_size_t
-        lib.dt_attention_workspace.argtypes = [ctypes.POINTER(_KVCache), ctypes.POINTER(_Chunk), ctypes.c_int32]
+        lib.dt_attention_workspace.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32]
         lib.dt_process_logits.restype = ctypes.c_int
-        lib.dt_process_logits.argtypes = [ctypes.POINTER(_LogitsParams)]
-        lib.dt_commit_path.restype = ctypes.c_int
-        lib.dt_commit_path.argtypes = [ctypes.POINTER(_KVCache), ctypes.POINTER(_Chunk),
-                                       ctypes.POINTER(_CommitParams)]
+        lib.dt_process_logits.argtypes = [ctypes.c_void_p]
         _lib = lib
     return _lib
 
@@ -344,21 +354,27 @@ def _need(ok: bool, where: str, what: str) -> None:
         raise DtError(DT_ERR_INVALID_ARG, f"{where}: {what}")
 
 
-def _check(t: Optional[torch.Tensor], shape, dtype, device, where: str, name: str) -> Optional[int]:
-    """Address of a contiguous tensor of this shape and type (None: no tensor)."""
+def _at(t: Optional[torch.Tensor], shape, dtype, index: int, where: str, name: str) -> int:
+    """Address of a contiguous tensor of this shape, type and device (get_device()); 0 without one."""
     if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        return 0
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
         raise DtError(DT_ERR_INVALID_ARG,
-                      f"{where}: {name} must be contiguous {dtype} {tuple(shape)} on {device}, "
-                      f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+                      f"{where}: {name} must be contiguous {dtype} {tuple(shape)} on the call's device, "
+                      f"not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-def _stream_of(stream, device) -> int:
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream if device.type == "cuda" else 0
-    return stream if isinstance(stream, int) else stream.cuda_stream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, index: int) -> int:
+    """Raw handle of `stream`, or of the device's current one."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    if index < 0:
+        return 0
+    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
 
 
 class KVCache:
@@ -369,7 +385,7 @@ class KVCache:
     ``transpose(-3, -2)``); page_table int32 [B][max_pages].  Holds the
     tensors; make another for other tensors."""
 
-    __slots__ = ("k", "v", "page_table", "device", "dtype", "Hkv", "D", "layers", "_struct", "_ref")
+    __slots__ = ("k", "v", "page_table", "device", "index", "dtype", "Hkv", "D", "layers", "_struct", "_ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor):
         w = "KVCache"
@@ -382,11 +398,11 @@ class KVCache:
         _need(v.device == k.device and page_table.device == k.device, w, "k, v and page_table on one device")
         self.k, self.v, self.page_table = k, v, page_table
         self.device, self.dtype, self.Hkv, self.D = k.device, k.dtype, int(k.shape[-2]), int(k.shape[-1])
-        self.layers = int(k.shape[0]) if k.dim() == 5 else 1
+        self.layers, self.index = int(k.shape[0]) if k.dim() == 5 else 1, k.get_device()
         self._struct = _KVCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), k.stride(0) if k.dim() == 5 else 0,
                                 k.stride(-4), k.stride(-3), k.stride(-2), self.layers, k.shape[-4], k.shape[-3],
                                 page_table.shape[1], self.Hkv, self.D, _HEAD_TYPES[k.dtype])
-        self._ref = ctypes.byref(self._struct)
+        self._ref = ctypes.addressof(self._struct)
 
 
 class Chunk:
@@ -396,21 +412,23 @@ class Chunk:
     (``Chunk.of_tree``).  Holds the tensors, whose values may change between
     calls; make another for other tensors."""
 
-    __slots__ = ("ctx_len", "n_nodes", "mask", "depths", "B", "lead", "n_max", "rows", "device", "_struct", "_ref")
+    __slots__ = ("ctx_len", "n_nodes", "mask", "depths", "B", "lead", "n_max", "rows", "device", "index", "_struct",
+                 "_ref")
 
     def __init__(self, ctx_len: torch.Tensor, lead: int = 1, n_max: int = 0, n_nodes: Optional[torch.Tensor] = None,
                  mask: Optional[torch.Tensor] = None, depths: Optional[torch.Tensor] = None):
-        w, dev = "Chunk", ctx_len.device
+        w, dev = "Chunk", ctx_len.get_device()
         _need(ctx_len.dim() == 1, w, "ctx_len must be int32 [B]")
         B, n_max, lead = int(ctx_len.shape[0]), int(n_max), int(lead)
-        _check(ctx_len, (B,), torch.int32, dev, w, "ctx_len")
-        _check(n_nodes, (B,), torch.int32, dev, w, "n_nodes")
-        _check(mask, (B, n_max, (n_max + 31) // 32), torch.int32, dev, w, "mask")
-        _check(depths, (B, n_max), torch.int32, dev, w, "depths")
+        _at(ctx_len, (B,), torch.int32, dev, w, "ctx_len")
+        _at(n_nodes, (B,), torch.int32, dev, w, "n_nodes")
+        _at(mask, (B, n_max, (n_max + 31) // 32), torch.int32, dev, w, "mask")
+        _at(depths, (B, n_max), torch.int32, dev, w, "depths")
         self.ctx_len, self.n_nodes, self.mask, self.depths = ctx_len, n_nodes, mask, depths
-        self.B, self.lead, self.n_max, self.rows, self.device = B, lead, n_max, lead + n_max, dev
+        self.B, self.lead, self.n_max, self.rows = B, lead, n_max, lead + n_max
+        self.device, self.index = ctx_len.device, dev
         self._struct = _Chunk(B, lead, n_max, _ptr(ctx_len), _ptr(n_nodes), _ptr(mask), _ptr(depths))
-        self._ref = ctypes.byref(self._struct)
+        self._ref = ctypes.addressof(self._struct)
 
     @classmethod
     def of_tree(cls, ctx_len: torch.Tensor, tree: TreeOut, lead: int = 1) -> "Chunk":
@@ -418,23 +436,27 @@ class Chunk:
         return cls(ctx_len, lead, int(tree.tokens.shape[1]), tree.n_nodes, tree.mask, tree.depths)
 
 
-def _row_heads(t: torch.Tensor, chunk: Chunk, H: Optional[int], kv: KVCache, where: str, name: str) -> int:
+def _row_stride(t: Optional[torch.Tensor], shape, kv: KVCache, where: str, name: str) -> int:
     """Row stride of a [B][rows][H][D] tensor whose rows' heads are contiguous."""
-    sh, st = t.shape, t.stride()
-    _need(len(sh) == 4 and sh[0] == chunk.B and sh[1] == chunk.rows and (H is None or sh[2] == H) and sh[3] == kv.D,
-          where, f"{name} must be [B][lead + n_max][heads][D], not {tuple(sh)}")
-    _need(t.dtype == kv.dtype and t.device == kv.device, where, f"{name} must have the cache's type and device")
-    _need(st[3] == 1 and (sh[2] == 1 or st[2] == kv.D), where, f"the heads of a row of {name} must be contiguous")
-    if sh[0] == 1:
-        return st[1]
-    if sh[1] == 1:
-        return st[0]
-    _need(st[0] == sh[1] * st[1], where, f"the rows of {name} must be evenly spaced over the batch")
-    return st[1]
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype is not kv.dtype or t.get_device() != kv.index:
+        raise DtError(DT_ERR_INVALID_ARG, f"{where}: {name} must be {kv.dtype} [B][lead + n_max][heads][D] = "
+                                          f"{tuple(shape)} on the cache's device, not {t.dtype} {tuple(t.shape)}")
+    batch, row, head, one = t.stride()
+    if one != 1 or (head != kv.D and shape[2] != 1):
+        raise DtError(DT_ERR_INVALID_ARG, f"{where}: the heads of a row of {name} must be contiguous")
+    if shape[0] == 1:
+        return row
+    if shape[1] == 1:
+        return batch
+    if batch != shape[1] * row:
+        raise DtError(DT_ERR_INVALID_ARG, f"{where}: the rows of {name} must be evenly spaced over the batch")
+    return row
 
 
 def _pass_devices(kv: Optional[KVCache], chunk: Chunk, where: str) -> None:
-    _need(kv is None or (chunk.device == kv.device and kv.page_table.shape[0] >= chunk.B), where,
+    _need(kv is None or (chunk.index == kv.index and kv.page_table.shape[0] >= chunk.B), where,
           "the chunk and the cache must be on one device, with a row of page_table for every request")
 
 
@@ -459,19 +481,20 @@ def dt_kv_append(kv: KVCache, chunk: Chunk, k: torch.Tensor, v: torch.Tensor, q:
     the cache (see dt_kv_append in dt.h).  q, k, v, q_out [B][lead + n_max]
     [heads][D], evenly spaced rows (slices of one projection); q_norm and
     k_norm [D]; freqs float64 [rot_dim / 2] on the device."""
-    w = "dt_kv_append"
+    w, index, dtype = "dt_kv_append", kv.index, kv.dtype
     _pass_devices(kv, chunk, w)
-    Hq = int(q.shape[2]) if q is not None and q.dim() == 4 else None
-    p = _AppendParams(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out),
-                      0 if q is None else _row_heads(q, chunk, None, kv, w, "q"),
-                      _row_heads(k, chunk, kv.Hkv, kv, w, "k"), _row_heads(v, chunk, kv.Hkv, kv, w, "v"),
-                      0 if q_out is None else _row_heads(q_out, chunk, Hq, kv, w, "q_out"), Hq or 0,
-                      _check(q_norm, (kv.D,), kv.dtype, kv.device, w, "q_norm"),
-                      _check(k_norm, (kv.D,), kv.dtype, kv.device, w, "k_norm"), eps,
-                      None if freqs is None else _check(freqs, (freqs.numel(),), torch.float64, kv.device, w, "freqs"),
-                      0 if freqs is None else 2 * freqs.numel(), bool(interleaved), rot_scale, layer,
-                      _stream_of(stream, kv.device))
-    st = _load().dt_kv_append(kv._ref, chunk._ref, ctypes.byref(p))
+    B, rows, D, Hq = chunk.B, chunk.rows, kv.D, 0
+    if q is not None:
+        _need(q.dim() == 4, w, "q must be [B][lead + n_max][heads][D]")
+        Hq = int(q.shape[2])
+    heads, kv_heads = (B, rows, Hq, D), (B, rows, kv.Hkv, D)
+    st = _load().dt_kv_append(kv._ref, chunk._ref, _pack_append(
+        0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if q_out is None else q_out.data_ptr(),
+        _row_stride(q, heads, kv, w, "q"), _row_stride(k, kv_heads, kv, w, "k"), _row_stride(v, kv_heads, kv, w, "v"),
+        _row_stride(q_out, heads, kv, w, "q_out"), Hq, _at(q_norm, (D,), dtype, index, w, "q_norm"),
+        _at(k_norm, (D,), dtype, index, w, "k_norm"), eps,
+        0 if freqs is None else _at(freqs, (freqs.numel(),), torch.float64, index, w, "freqs"),
+        0 if freqs is None else 2 * freqs.numel(), bool(interleaved), rot_scale, layer, _stream_of(stream, index)))
     if st != DT_OK:
         raise DtError(st, w)
 
@@ -487,17 +510,18 @@ def dt_tree_attention(kv: KVCache, chunk: Chunk, q: torch.Tensor, out: torch.Ten
     dt.h).  q and out [B][lead + n_max][Hq][D]; scale defaults to D^-1/2; lse
     float32 [B][lead + n_max][Hq] or None; workspace of
     dt_attention_workspace() bytes."""
-    w = "dt_tree_attention"
+    w, index = "dt_tree_attention", kv.index
     _pass_devices(kv, chunk, w)
-    q_stride = _row_heads(q, chunk, None, kv, w, "q")
+    _need(q.dim() == 4, w, "q must be [B][lead + n_max][heads][D]")
     Hq = int(q.shape[2])
-    p = _AttentionParams(q.data_ptr(), out.data_ptr(), q_stride, _row_heads(out, chunk, Hq, kv, w, "out"), Hq,
-                         kv.D ** -0.5 if scale is None else scale,
-                         _check(lse, (chunk.B, chunk.rows, Hq), torch.float32, kv.device, w, "lse"), layer,
-                         _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                         _stream_of(stream, kv.device))
-    _need(workspace is None or workspace.device == kv.device, w, "workspace must be on the cache's device")
-    st = _load().dt_tree_attention(kv._ref, chunk._ref, ctypes.byref(p))
+    heads = (chunk.B, chunk.rows, Hq, kv.D)
+    _need(workspace is None or (workspace.get_device() == index and workspace.is_contiguous()), w,
+          "workspace must be contiguous, on the cache's device")
+    st = _load().dt_tree_attention(kv._ref, chunk._ref, _pack_attention(
+        q.data_ptr(), out.data_ptr(), _row_stride(q, heads, kv, w, "q"), _row_stride(out, heads, kv, w, "out"), Hq,
+        kv.D ** -0.5 if scale is None else scale, _at(lse, heads[:3], torch.float32, index, w, "lse"), layer,
+        0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _stream_of(stream, index)))
     if st != DT_OK:
         raise DtError(st, w)
 
@@ -515,30 +539,28 @@ def dt_process_logits(logits: torch.Tensor, out: torch.Tensor, history: Optional
     positions, no tree).  history int32 [B][history_max]; bias_ids int32 and
     bias float32 [B][n_bias]; allow int32 [allow_rows][ceil(V/32)];
     allow_index int32 [B][lead + n_max]; the rest [B]."""
-    w, dev = "dt_process_logits", logits.device
+    w, dev = "dt_process_logits", logits.get_device()
     _need(logits.dim() == 3 and logits.dtype in _LOGIT_TYPES, w, "logits must be float32 or bfloat16 [B][rows][V]")
-    B, rows, V = (int(x) for x in logits.shape)
+    B, rows, V = logits.shape
     lead = rows if lead is None else int(lead)
-    n_max, i32, f32 = rows - lead, torch.int32, torch.float32
+    n_max, i32, f32, each = rows - lead, torch.int32, torch.float32, (B,)
     _need(0 <= lead <= rows, w, "lead must be 0..rows")
     for t, name in ((history, "history"), (bias_ids, "bias_ids"), (allow, "allow")):
         _need(t is None or t.dim() == 2, w, f"{name} must have two axes")
-    hmax = 0 if history is None else int(history.shape[1])
-    nb = 0 if bias_ids is None else int(bias_ids.shape[1])
-    arows = 0 if allow is None else int(allow.shape[0])
-    p = _LogitsParams(
-        _check(logits, logits.shape, logits.dtype, dev, w, "logits"),
-        _check(out, logits.shape, logits.dtype, dev, w, "out"), B, lead, n_max, V, _LOGIT_TYPES[logits.dtype],
-        _check(n_nodes, (B,), i32, dev, w, "n_nodes"), _check(history, (B, hmax), i32, dev, w, "history"), hmax,
-        _check(history_len, (B,), i32, dev, w, "history_len"), _check(prompt_len, (B,), i32, dev, w, "prompt_len"),
-        _check(node_tokens, (B, n_max), i32, dev, w, "node_tokens"),
-        _check(node_mask, (B, n_max, (n_max + 31) // 32), i32, dev, w, "node_mask"),
-        _check(repetition, (B,), f32, dev, w, "repetition"), _check(frequency, (B,), f32, dev, w, "frequency"),
-        _check(presence, (B,), f32, dev, w, "presence"), _check(bias_ids, (B, nb), i32, dev, w, "bias_ids"),
-        _check(bias, (B, nb), f32, dev, w, "bias"), nb,
-        _check(allow, (arows, (V + 31) // 32), i32, dev, w, "allow"),
-        _check(allow_index, (B, rows), i32, dev, w, "allow_index"), arows, _stream_of(stream, dev))
-    st = _load().dt_process_logits(ctypes.byref(p))
+    hmax = 0 if history is None else history.shape[1]
+    nb = 0 if bias_ids is None else bias_ids.shape[1]
+    arows = 0 if allow is None else allow.shape[0]
+    st = _load().dt_process_logits(_pack_logits(
+        _at(logits, logits.shape, logits.dtype, dev, w, "logits"), _at(out, logits.shape, logits.dtype, dev, w, "out"),
+        B, lead, n_max, V, _LOGIT_TYPES[logits.dtype],
+        _at(n_nodes, each, i32, dev, w, "n_nodes"), _at(history, (B, hmax), i32, dev, w, "history"), hmax,
+        _at(history_len, each, i32, dev, w, "history_len"), _at(prompt_len, each, i32, dev, w, "prompt_len"),
+        _at(node_tokens, (B, n_max), i32, dev, w, "node_tokens"),
+        _at(node_mask, (B, n_max, (n_max + 31) // 32), i32, dev, w, "node_mask"),
+        _at(repetition, each, f32, dev, w, "repetition"), _at(frequency, each, f32, dev, w, "frequency"),
+        _at(presence, each, f32, dev, w, "presence"), _at(bias_ids, (B, nb), i32, dev, w, "bias_ids"),
+        _at(bias, (B, nb), f32, dev, w, "bias"), nb, _at(allow, (arows, (V + 31) // 32), i32, dev, w, "allow"),
+        _at(allow_index, (B, rows), i32, dev, w, "allow_index"), arows, _stream_of(stream, dev)))
     if st != DT_OK:
         raise DtError(st, w)
 
@@ -551,17 +573,14 @@ def dt_commit_path(kv: Optional[KVCache], chunk: Chunk, tokens: Optional[torch.T
     dt_commit_path in dt.h).  tokens and parents int32 [B][n_max] as
     dt_build_tree wrote them; target int32 [B][lead + n_max]; accepted and
     nodes int32 [B][L], lengths int32 [B] are written."""
-    w, dev, i32 = "dt_commit_path", chunk.device, torch.int32
+    w, dev, i32 = "dt_commit_path", chunk.index, torch.int32
     _pass_devices(kv, chunk, w)
     _need(accepted.dim() == 2, w, "accepted must be int32 [B][L]")
-    L = int(accepted.shape[1])
-    p = _CommitParams(_check(tokens, (chunk.B, chunk.n_max), i32, dev, w, "tokens"),
-                      _check(parents, (chunk.B, chunk.n_max), i32, dev, w, "parents"),
-                      _check(target, (chunk.B, chunk.rows), i32, dev, w, "target"), L,
-                      _check(accepted, (chunk.B, L), i32, dev, w, "accepted"),
-                      _check(lengths, (chunk.B,), i32, dev, w, "lengths"),
-                      _check(nodes, (chunk.B, L), i32, dev, w, "nodes"), _stream_of(stream, dev))
-    st = _load().dt_commit_path(None if kv is None else kv._ref, chunk._ref, ctypes.byref(p))
+    B, L = chunk.B, accepted.shape[1]
+    st = _load().dt_commit_path(0 if kv is None else kv._ref, chunk._ref, _pack_commit(
+        _at(tokens, (B, chunk.n_max), i32, dev, w, "tokens"), _at(parents, (B, chunk.n_max), i32, dev, w, "parents"),
+        _at(target, (B, chunk.rows), i32, dev, w, "target"), L, _at(accepted, (B, L), i32, dev, w, "accepted"),
+        _at(lengths, (B,), i32, dev, w, "lengths"), _at(nodes, (B, L), i32, dev, w, "nodes"), _stream_of(stream, dev)))
     if st != DT_OK:
         raise DtError(st, w)
 
