@@ -231,26 +231,19 @@ struct Shape {
     static constexpr int kPartial = kMt * (D + 2);         // floats of a split's partial result
 };
 
-template <class T, int D, int WM, int WK, int KT, int PER_CU>
-__global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
-    attention_kernel(AttentionArgs a, int slots, int* plan, float* partial) {
+// One job; every wave of the workgroup calls it.
+template <class T, int D, int WM, int WK, int KT>
+__device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, int c, char* lds, float* partial) {
     using S = Shape<T, D, WM, WK, KT>;
     constexpr int NB = KT / 32, KS = D / 16, ND = D / 32;
     constexpr int kUnits16 = D / 8;                        // 16-byte pieces of a head
     constexpr int kRpi = 64 / kUnits16;                    // rows of a wave's copy instruction
     constexpr int kCopies = KT / kRpi / WM;                // copies of K (and of V) a wave and tile
     constexpr int kPer16 = 16 / kRpi;                      // copies of 16 rows
-    extern __shared__ __attribute__((aligned(1024))) char lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wk = wave / WM;
     const int half = lane >> 5, col = lane & 31;
-
-    const Request q0 = request_of(a, lane, S::kMt);
-    const int c = chunk_units(a, q0, S::kMt, slots, lane);
-    if (blockIdx.x == 0 && tid == 0) *plan = c;            // for combine_kernel
-    const Job job = job_of(a, q0, S::kMt, c, blockIdx.x & 7, blockIdx.x >> 3, lane);
-    if (job.b < 0) return;
     const int b = job.b;
     const int ctx = a.c.ctx_len[b], lead = a.c.lead, nn = job.q.rows - lead;
     const int mrows = job.q.rows * a.G;
@@ -305,7 +298,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
         int page, in;                                      // page id (-1: no such key) and slot in the page
     };
     const int32_t* table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
-    const auto look_up = [&](int t) {
+    const auto look_up = [&](int t) __attribute__((always_inline)) {
         const int key = k_first + t * KT + (lane & (KT - 1));
         Place p = {-1, 0};
         if (t < tiles && key < k_end) {
@@ -315,7 +308,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
         }
         return p;
     };
-    const auto is_valid = [&](const Place& p) { return p.page >= 0 && p.page < a.kv.num_pages; };
+    const auto is_valid = [&](const Place& p) __attribute__((always_inline)) { return p.page >= 0 && p.page < a.kv.num_pages; };
     // Byte offsets of a lane's copies within the 16 rows they belong to.
     constexpr int kOwn = kCopies < kPer16 ? kCopies : kPer16;
     static_assert(kCopies % kOwn == 0 && kPer16 % kOwn == 0, "a wave's copies lie in whole parts of 16 rows");
@@ -330,7 +323,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     }
     // Copies of a tile into K's (V's) buffer; a key that is not there comes
     // from some mapped address, its score and value are dropped below.
-    const auto issue = [&](const Place& p, bool is_v, int buf) {
+    const auto issue = [&](const Place& p, bool is_v, int buf) __attribute__((always_inline)) {
         const uint16_t* const from = is_v ? vbase : kbase;
         const uint32_t to = group + (2 * is_v + buf) * S::kTile;
         const bool ok = is_valid(p);
@@ -373,7 +366,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     float m = -INFINITY, l = 0;                            // m in units of log2; l of this lane's keys
 
     constexpr u64 kFull = KT == 64 ? ~0ull : 0xFFFFFFFFull;
-    const auto rescale = [&](float top) {
+    const auto rescale = [&](float top) __attribute__((always_inline)) {
         const float mm = fmaxf(m, top);
         const float w = mm == -INFINITY ? 1.0f : exp2f(m - mm);
         m = mm;
@@ -383,7 +376,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
 #pragma unroll
             for (int x = 0; x < 16; ++x) o[d][x] *= w;
     };
-    const auto value = [&](const char* vt, int d, int x) {  // V^T of 32 elements and 16 keys
+    const auto value = [&](const char* vt, int d, int x) __attribute__((always_inline)) {  // V^T of 32 elements and 16 keys
         typedef __attribute__((address_space(3))) s16x4 lds4;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x) * D * 2));
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x + 8) * D * 2));
@@ -391,7 +384,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     };
     // A wave's products go before the other's vector work on the same SIMD
     // (a prompt's chunk 795 -> 769 us).
-    const auto scores = [&](const char* kt, int n) {
+    const auto scores = [&](const char* kt, int n) __attribute__((always_inline)) {
         f32x16 s = {};
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -401,7 +394,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     };
     // A tile's scores into the sums; `masked` is a type: the tiles that every
     // row sees in full have no code for anything else.
-    const auto tile = [&](int k0, f32x16 (&s)[NB], const char* vt, u64 now, auto is_masked) {
+    const auto tile = [&](int k0, f32x16 (&s)[NB], const char* vt, u64 now, auto is_masked) __attribute__((always_inline)) {
         constexpr bool masked = decltype(is_masked)::value;
         uint32_t see[NB];
         if constexpr (masked) {
@@ -523,7 +516,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
     place = look_up(wk + WK);
     const int rounds = (tiles + WK - 1) / WK;
     const int fast = whole > wk ? (whole - wk + WK - 1) / WK : 0;
-    const auto round = [&](int i, auto is_masked) {
+    const auto round = [&](int i, auto is_masked) __attribute__((always_inline)) {
         const int t = wk + i * WK;
         wait_copies();
         if constexpr (WM > 1) __syncthreads();
@@ -552,7 +545,7 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
         __syncthreads();
         float* const box = (float*)lds;                    // [WK][WM][64 lanes][16 ND + 2], a lane's own slots
         constexpr int kSlot = 64;
-        const auto at = [&](int k, int x) -> float& { return box[((k * WM + wm) * (16 * ND + 2) + x) * kSlot + lane]; };
+        const auto at = [&](int k, int x) __attribute__((always_inline)) -> float& { return box[((k * WM + wm) * (16 * ND + 2) + x) * kSlot + lane]; };
         if (wk > 0) {
             at(wk - 1, 0) = m;
             at(wk - 1, 1) = l;
@@ -613,6 +606,31 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 *(f32x4*)(po + d * 32 + 8 * x) = f32x4{o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]};
+    }
+}
+
+// A workgroup takes every (gridDim / 8)-th job of its XCD: its only one, where
+// the host could tell how many there may be, or one after the other in a grid
+// of as many workgroups as are resident.
+template <class T, int D, int WM, int WK, int KT, int PER_CU, bool LOOP>
+__global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
+    attention_kernel(AttentionArgs a, int slots, int* plan, float* partial) {
+    using S = Shape<T, D, WM, WK, KT>;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    const int lane = threadIdx.x & 63;
+    const Request q0 = request_of(a, lane, S::kMt);
+    const int c = chunk_units(a, q0, S::kMt, slots, lane);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *plan = c;    // for combine_kernel
+    if constexpr (LOOP) {
+        for (int y = blockIdx.x >> 3;; y += gridDim.x >> 3) {
+            const Job job = job_of(a, q0, S::kMt, c, blockIdx.x & 7, y, lane);
+            if (job.b < 0) return;
+            attend<T, D, WM, WK, KT>(a, job, c, lds, partial);
+            __syncthreads();                               // the next job's copies overwrite what this one reads
+        }
+    } else {
+        const Job job = job_of(a, q0, S::kMt, c, blockIdx.x & 7, blockIdx.x >> 3, lane);
+        if (job.b >= 0) attend<T, D, WM, WK, KT>(a, job, c, lds, partial);
     }
 }
 
@@ -715,28 +733,40 @@ int slots_for(int mt, int D) {
     return kCus * (D == 256 ? 1 : 2);
 }
 
-// Upper bound of a call's workgroups on one XCD.  chunk_units() makes at most
-// segments + 4 slots chunks; a request's groups go round over the XCDs, so
-// one XCD has at most an eighth of its chunks and one group of mtiles more.
-int64_t max_jobs(const ChunkArgs& c, int Hkv, int G, int mt, int slots) {
-    const int64_t mtiles = ((int64_t)c.rows * G + mt - 1) / mt;
-    return ((int64_t)c.B * Hkv * mtiles + 4 * slots + 7) / 8 + c.B * mtiles;
+// Upper bound of a call's jobs on one XCD.  chunk_units() makes at most
+// segments + 4 slots chunks, at most `slots` of few segments in one round, and
+// none but a segment's last below kMinUnits; a request's groups go round over
+// the XCDs, so one XCD has at most an eighth of its chunks and one group of
+// mtiles more.
+int64_t max_jobs(const AttentionArgs& a, int mt, int slots) {
+    const int64_t mtiles = ((int64_t)a.c.rows * a.G + mt - 1) / mt, segments = (int64_t)a.c.B * a.kv.Hkv * mtiles;
+    const int64_t units = ((int64_t)a.kv.cap + kUnit - 1) / kUnit;
+    int64_t jobs = segments + 4 * slots;
+    const int64_t finest = segments * ((units + kMinUnits - 1) / kMinUnits);
+    if (finest < jobs) jobs = finest;
+    return (jobs + 7) / 8 + a.c.B * mtiles;
 }
 
 template <class T, int D, int WM, int WK, int KT, int PER_CU>
 hipError_t run(const AttentionArgs& a, void* workspace, hipStream_t stream) {
     using S = Shape<T, D, WM, WK, KT>;
     const int slots = slots_for(S::kMt, D);
-    const int64_t jobs = 8 * max_jobs(a.c, a.kv.Hkv, a.G, S::kMt, slots);
-    const auto kernel = attention_kernel<T, D, WM, WK, KT, PER_CU>;
+    // Few segments, cut into chunks of one size: the resident workgroups take
+    // them in turn, and none is started for nothing.  Many segments of many
+    // sizes: a workgroup a job, handed out as others end.
+    const int64_t most = 8 * max_jobs(a, S::kMt, slots), mtiles = ((int64_t)a.c.rows * a.G + S::kMt - 1) / S::kMt;
+    const bool loop = most > slots && 2 * a.c.B * a.kv.Hkv * mtiles < slots;
+    const int64_t grid = loop ? slots : most;
+    const auto kernel = loop ? attention_kernel<T, D, WM, WK, KT, PER_CU, true>
+                             : attention_kernel<T, D, WM, WK, KT, PER_CU, false>;
     int* const plan = (int*)workspace;
     float* const partial = (float*)((char*)workspace + kPlanBytes);
-    kernel<<<(unsigned)jobs, S::kThreads, S::kLds, stream>>>(a, slots, plan, partial);
+    kernel<<<(unsigned)grid, S::kThreads, S::kLds, stream>>>(a, slots, plan, partial);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t waves = ((int64_t)a.c.B * a.c.rows * a.Hq * (D / 4) + 63) / 64;
-    const unsigned grid = waves < 4 * 8 * kCus ? (unsigned)((waves + 3) / 4) : 8 * kCus;
-    combine_kernel<T, D, S::kMt><<<grid, 256, 0, stream>>>(a, plan, partial);
+    const unsigned groups = waves < 4 * 8 * kCus ? (unsigned)((waves + 3) / 4) : 8 * kCus;
+    combine_kernel<T, D, S::kMt><<<groups, 256, 0, stream>>>(a, plan, partial);
     return hipGetLastError();
 }
 
