@@ -4,9 +4,11 @@
 //
 // Rows.  The G query heads of a key head share its keys, so the matrix rows
 // of a request and key head are (chunk row, head in group), G * rows of them;
-// a wave takes 32.  A workgroup is WM x WK waves: WM x 32 rows, and WK
+// a wave takes 32.  A workgroup is WM x WK (x WD) waves: WM x 32 rows, and WK
 // groups of waves that take the tiles of KT keys in turn (few rows: the
-// waves share the keys out; many rows: they share the tiles).
+// waves share the keys out; many rows: they share the tiles).  With heads of
+// 256 a wave's sums would not fit its registers: WD = 2 waves then make the
+// same scores and half of the outputs each.
 //
 // Products.  Scores are computed transposed, K q^T on 32x32x16 matrix
 // instructions, so that a lane holds one query and the tile's keys lie in its
@@ -221,9 +223,9 @@ struct False {
     static constexpr bool value = false;
 };
 
-template <class T, int D, int WM, int WK, int KT>
+template <class T, int D, int WM, int WK, int WD, int KT>
 struct Shape {
-    static constexpr int kThreads = 64 * WM * WK;
+    static constexpr int kThreads = 64 * WM * WK * WD;
     static constexpr int kMt = WM * kRowsPerWave;
     static constexpr int kTile = KT * D * 2;               // bytes of a K or V tile
     static constexpr int kGroup = 4 * kTile;               // K's two buffers, V's two
@@ -232,17 +234,17 @@ struct Shape {
 };
 
 // One job; every wave of the workgroup calls it.
-template <class T, int D, int WM, int WK, int KT>
+template <class T, int D, int WM, int WK, int WD, int KT>
 __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, int c, char* lds, float* partial) {
-    using S = Shape<T, D, WM, WK, KT>;
-    constexpr int NB = KT / 32, KS = D / 16, ND = D / 32;
+    using S = Shape<T, D, WM, WK, WD, KT>;
+    constexpr int NB = KT / 32, KS = D / 16, ND = D / 32 / WD;     // ND: the wave's own blocks of outputs
     constexpr int kUnits16 = D / 8;                        // 16-byte pieces of a head
     constexpr int kRpi = 64 / kUnits16;                    // rows of a wave's copy instruction
-    constexpr int kCopies = KT / kRpi / WM;                // copies of K (and of V) a wave and tile
+    constexpr int kCopies = KT / kRpi / (WM * WD);         // copies of K (and of V) a wave and tile
     constexpr int kPer16 = 16 / kRpi;                      // copies of 16 rows
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave % WM, wk = wave / WM;
+    const int wm = wave % WM, wd = wave / WM % WD, wk = wave / (WM * WD), wl = wave % (WM * WD);
     const int half = lane >> 5, col = lane & 31;
     const int b = job.b;
     const int ctx = a.c.ctx_len[b], lead = a.c.lead, nn = job.q.rows - lead;
@@ -317,7 +319,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     const uint32_t slot_bytes = (uint32_t)(a.kv.slot_stride * 2);
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-        const int rg = (wm * kCopies + i) % kPer16 * kRpi + prow;
+        const int rg = (wl * kCopies + i) % kPer16 * kRpi + prow;
         koff[i] = rg * slot_bytes + (piece ^ swizzle_k<D>(rg)) * 16;
         voff[i] = rg * slot_bytes + (piece ^ swizzle_v<D>(rg)) * 16;
     }
@@ -331,7 +333,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
             // 16 rows that begin at a multiple of 16 lie in one page
 #pragma unroll
             for (int g = 0; g < kCopies / kOwn; ++g) {
-                const int at = wm * kCopies + g * kOwn, row = at / kPer16 * 16;
+                const int at = wl * kCopies + g * kOwn, row = at / kPer16 * 16;
                 const int page = __builtin_amdgcn_readlane(ok ? p.page : 0, row);
                 const int in = __builtin_amdgcn_readlane(ok ? p.in : 0, row);
                 const char* base = (const char*)(from + page * a.kv.page_stride) + (int64_t)in * slot_bytes;
@@ -343,7 +345,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
             const int lo = (int)off, hi = (int)(off >> 32);
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
-                const int at = wm * kCopies + i, trow = at * kRpi + prow;
+                const int at = wl * kCopies + i, trow = at * kRpi + prow;
                 const int64_t o = (int64_t)((u64)(uint32_t)__shfl(lo, trow) | (u64)(uint32_t)__shfl(hi, trow) << 32);
                 copy_to_lds(from + o + (piece ^ (is_v ? swizzle_v<D>(trow) : swizzle_k<D>(trow))) * 8, to + at * 1024);
             }
@@ -357,7 +359,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     const int vrow = 4 * half + ((lane >> 2) & 3);
 #pragma unroll
     for (int d = 0; d < ND; ++d)
-        vaddr[d] = vrow * D * 2 + (((d * 4) ^ swizzle_v<D>(vrow)) * 16) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+        vaddr[d] = vrow * D * 2 + ((((wd * ND + d) * 4) ^ swizzle_v<D>(vrow)) * 16) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
     char* const my = lds + wk * S::kGroup;
 
     f32x16 o[ND];
@@ -519,7 +521,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     const auto round = [&](int i, auto is_masked) __attribute__((always_inline)) {
         const int t = wk + i * WK;
         wait_copies();
-        if constexpr (WM > 1) __syncthreads();
+        if constexpr (WM * WD > 1) __syncthreads();
         const u64 now = valid;
         if (t + WK < tiles) {
             valid = __ballot(is_valid(place));
@@ -543,9 +545,9 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     if constexpr (WK > 1) {
         // the key groups' results meet in LDS; group 0 goes on with the sum
         __syncthreads();
-        float* const box = (float*)lds;                    // [WK][WM][64 lanes][16 ND + 2], a lane's own slots
+        float* const box = (float*)lds;                    // [WK - 1][WM WD][16 ND + 2][64 lanes], a lane's own slots
         constexpr int kSlot = 64;
-        const auto at = [&](int k, int x) __attribute__((always_inline)) -> float& { return box[((k * WM + wm) * (16 * ND + 2) + x) * kSlot + lane]; };
+        const auto at = [&](int k, int x) __attribute__((always_inline)) -> float& { return box[((k * WM * WD + wl) * (16 * ND + 2) + x) * kSlot + lane]; };
         if (wk > 0) {
             at(wk - 1, 0) = m;
             at(wk - 1, 1) = l;
@@ -582,7 +584,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     if (!live) return;
     if (job.splits == 1) {
         const float inv = l == 0 ? 0.0f : 1.0f / l;
-        uint16_t* const out = a.out + row * a.out_stride + (int64_t)h * D + 4 * half;
+        uint16_t* const out = a.out + row * a.out_stride + (int64_t)h * D + wd * ND * 32 + 4 * half;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -592,15 +594,15 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
                 for (int e = 0; e < 4; ++e) y[e] = (short)T::put(l == 0 ? 0.0f : o[d][4 * x + e] * inv);
                 *(s16x4*)(out + d * 32 + 8 * x) = y;
             }
-        if (a.lse && half == 0) a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        if (a.lse && half == 0 && wd == 0) a.lse[row * a.Hq + h] = l == 0 ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     } else {
         float* const part = partial + (int64_t)job.slot * S::kPartial;
         const int at = wm * kRowsPerWave + col;
-        if (half == 0) {
+        if (half == 0 && wd == 0) {
             part[at] = m;
             part[S::kMt + at] = l;
         }
-        float* const po = part + 2 * S::kMt + (int64_t)at * D + 4 * half;
+        float* const po = part + 2 * S::kMt + (int64_t)at * D + wd * ND * 32 + 4 * half;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -612,10 +614,10 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
 // A workgroup takes every (gridDim / 8)-th job of its XCD: its only one, where
 // the host could tell how many there may be, or one after the other in a grid
 // of as many workgroups as are resident.
-template <class T, int D, int WM, int WK, int KT, int PER_CU, bool LOOP>
-__global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
+template <class T, int D, int WM, int WK, int WD, int KT, int PER_CU, bool LOOP>
+__global__ void __launch_bounds__(64 * WM * WK * WD, (PER_CU * WM * WK * WD + 3) / 4)
     attention_kernel(AttentionArgs a, int slots, int* plan, float* partial) {
-    using S = Shape<T, D, WM, WK, KT>;
+    using S = Shape<T, D, WM, WK, WD, KT>;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const int lane = threadIdx.x & 63;
     const Request q0 = request_of(a, lane, S::kMt);
@@ -625,12 +627,12 @@ __global__ void __launch_bounds__(64 * WM * WK, (PER_CU * WM * WK + 3) / 4)
         for (int y = blockIdx.x >> 3;; y += gridDim.x >> 3) {
             const Job job = job_of(a, q0, S::kMt, c, blockIdx.x & 7, y, lane);
             if (job.b < 0) return;
-            attend<T, D, WM, WK, KT>(a, job, c, lds, partial);
+            attend<T, D, WM, WK, WD, KT>(a, job, c, lds, partial);
             __syncthreads();                               // the next job's copies overwrite what this one reads
         }
     } else {
         const Job job = job_of(a, q0, S::kMt, c, blockIdx.x & 7, blockIdx.x >> 3, lane);
-        if (job.b >= 0) attend<T, D, WM, WK, KT>(a, job, c, lds, partial);
+        if (job.b >= 0) attend<T, D, WM, WK, WD, KT>(a, job, c, lds, partial);
     }
 }
 
@@ -747,9 +749,9 @@ int64_t max_jobs(const AttentionArgs& a, int mt, int slots) {
     return (jobs + 7) / 8 + a.c.B * mtiles;
 }
 
-template <class T, int D, int WM, int WK, int KT, int PER_CU>
+template <class T, int D, int WM, int WK, int WD, int KT, int PER_CU>
 hipError_t run(const AttentionArgs& a, void* workspace, hipStream_t stream) {
-    using S = Shape<T, D, WM, WK, KT>;
+    using S = Shape<T, D, WM, WK, WD, KT>;
     const int slots = slots_for(S::kMt, D);
     // Few segments, cut into chunks of one size: the resident workgroups take
     // them in turn, and none is started for nothing.  Many segments of many
@@ -757,8 +759,8 @@ hipError_t run(const AttentionArgs& a, void* workspace, hipStream_t stream) {
     const int64_t most = 8 * max_jobs(a, S::kMt, slots), mtiles = ((int64_t)a.c.rows * a.G + S::kMt - 1) / S::kMt;
     const bool loop = most > slots && 2 * a.c.B * a.kv.Hkv * mtiles < slots;
     const int64_t grid = loop ? slots : most;
-    const auto kernel = loop ? attention_kernel<T, D, WM, WK, KT, PER_CU, true>
-                             : attention_kernel<T, D, WM, WK, KT, PER_CU, false>;
+    const auto kernel = loop ? attention_kernel<T, D, WM, WK, WD, KT, PER_CU, true>
+                             : attention_kernel<T, D, WM, WK, WD, KT, PER_CU, false>;
     int* const plan = (int*)workspace;
     float* const partial = (float*)((char*)workspace + kPlanBytes);
     kernel<<<(unsigned)grid, S::kThreads, S::kLds, stream>>>(a, slots, plan, partial);
@@ -774,13 +776,13 @@ template <class T, int D>
 hipError_t run_rows(const AttentionArgs& a, void* workspace, hipStream_t stream) {
     const int mt = tile_rows(a.c, a.G);
     if constexpr (D == 256) {
-        if (mt == 32) return run<T, D, 1, 2, 32, 1>(a, workspace, stream);
-        if (mt == 64) return run<T, D, 2, 1, 64, 1>(a, workspace, stream);
-        return run<T, D, 4, 1, 64, 1>(a, workspace, stream);
+        if (mt == 32) return run<T, D, 1, 2, 2, 32, 1>(a, workspace, stream);
+        if (mt == 64) return run<T, D, 2, 1, 2, 64, 1>(a, workspace, stream);
+        return run<T, D, 4, 1, 2, 64, 1>(a, workspace, stream);
     } else {
-        if (mt == 32) return run<T, D, 1, 4, 32, D == 64 ? 2 : 1>(a, workspace, stream);
-        if (mt == 64) return run<T, D, 2, 2, 32, 2>(a, workspace, stream);
-        return run<T, D, 4, 1, 64, 2>(a, workspace, stream);
+        if (mt == 32) return run<T, D, 1, 4, 1, 32, D == 64 ? 2 : 1>(a, workspace, stream);
+        if (mt == 64) return run<T, D, 2, 2, 1, 32, 2>(a, workspace, stream);
+        return run<T, D, 4, 1, 1, 64, 2>(a, workspace, stream);
     }
 }
 
