@@ -196,10 +196,11 @@ __device__ inline bool odd_value(uint32_t pair) {          // an infinity or NaN
     return (pair & e) == e || (pair & (e << 16)) == (e << 16);
 }
 
-// 16 bytes a lane from memory to LDS at `to` + 16 * lane; the wait is the
-// caller's: wait_copies() ends when every copy of the wave has arrived and
-// every LDS read it issued before has its data, so that the next copies may
-// overwrite what was read.
+// 16 bytes a lane from memory to LDS at `to` + 16 * lane; the waits are the
+// caller's: wait_copies<LEFT>() ends when all but the wave's LEFT last copies
+// (and loads) have arrived and every LDS read it issued before has its data,
+// wait_reads() for the latter alone: then the next copies may overwrite what
+// was read.
 __device__ inline void copy_to_lds(const uint16_t* from, uint32_t to) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
                  "s"(__builtin_amdgcn_readfirstlane(to)) : "m0");
@@ -209,7 +210,12 @@ __device__ inline void copy_to_lds(const char* base, uint32_t offset, uint32_t t
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset),
                  "s"((const char*)uniform((int64_t)base)), "s"(__builtin_amdgcn_readfirstlane(to)) : "m0");
 }
-__device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+template <int LEFT>
+__device__ inline void wait_copies() {
+    // (loads and copies end in order: all but the LEFT last have)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
+}
+__device__ inline void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 template <int D>
 __device__ inline int swizzle_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
@@ -509,33 +515,64 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     const int64_t plain = work ? (all < k_end ? all : k_end) - k_first : 0;
     const int whole = plain > 0 ? (int)(plain / KT) : 0;
 
+    const int rounds = (tiles + WK - 1) / WK;
+    const int fast = whole > wk ? (whole - wk + WK - 1) / WK : 0;
+    // A wave that has its tiles for itself needs no barrier and fetches two
+    // tiles ahead, each into the buffer it has just read; waves that share a
+    // tile fetch one ahead, into the buffer that all have left.
+    constexpr bool kAlone = WM * WD == 1;
     Place place = look_up(wk);
-    u64 valid = __ballot(is_valid(place));
+    u64 valid = __ballot(is_valid(place)), valid1 = 0;     // of this round's tile and of the next
     if (wk < tiles) {
         issue(place, false, 0);
         issue(place, true, 0);
     }
     place = look_up(wk + WK);
-    const int rounds = (tiles + WK - 1) / WK;
-    const int fast = whole > wk ? (whole - wk + WK - 1) / WK : 0;
+    if constexpr (kAlone) {
+        valid1 = __ballot(is_valid(place));
+        if (wk + WK < tiles) {
+            issue(place, false, 1);
+            issue(place, true, 1);
+            place = look_up(wk + 2 * WK);
+        }
+    }
     const auto round = [&](int i, auto is_masked) __attribute__((always_inline)) {
         const int t = wk + i * WK;
-        wait_copies();
-        if constexpr (WM * WD > 1) __syncthreads();
+        if constexpr (kAlone) {
+            if (t + WK < tiles) wait_copies<2 * kCopies>();
+            else wait_copies<0>();
+        } else {
+            wait_copies<0>();
+            __syncthreads();
+        }
         const u64 now = valid;
-        if (t + WK < tiles) {
-            valid = __ballot(is_valid(place));
-            issue(place, false, (i + 1) & 1);
-            issue(place, true, (i + 1) & 1);
-            place = look_up(t + 2 * WK);
+        if constexpr (!kAlone) {
+            if (t + WK < tiles) {
+                valid = __ballot(is_valid(place));
+                issue(place, false, (i + 1) & 1);
+                issue(place, true, (i + 1) & 1);
+                place = look_up(t + 2 * WK);
+            }
         }
         const int k0 = k_first + t * KT;
-        if constexpr (decltype(is_masked)::value)
-            if (!work || t >= tiles || k0 >= any) return;
-        f32x16 s[NB];
+        bool mine = true;
+        if constexpr (decltype(is_masked)::value) mine = work && t < tiles && k0 < any;
+        if (mine) {
+            f32x16 s[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) s[n] = scores(my + (i & 1) * S::kTile, n);
-        tile(k0, s, my + (2 + (i & 1)) * S::kTile, now, is_masked);
+            for (int n = 0; n < NB; ++n) s[n] = scores(my + (i & 1) * S::kTile, n);
+            tile(k0, s, my + (2 + (i & 1)) * S::kTile, now, is_masked);
+        }
+        if constexpr (kAlone) {
+            valid = valid1;
+            if (t + 2 * WK < tiles) {
+                valid1 = __ballot(is_valid(place));
+                wait_reads();
+                issue(place, false, i & 1);
+                issue(place, true, i & 1);
+                place = look_up(t + 3 * WK);
+            }
+        }
     };
     int i = 0;
     for (; i < fast && (valid & kFull) == kFull; ++i) round(i, False());
