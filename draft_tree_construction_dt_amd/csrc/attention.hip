@@ -170,7 +170,7 @@ __device__ inline Job job_of(const AttentionArgs& a, const Request& q0, int mt_r
             j.q.mtiles = __builtin_amdgcn_readlane(q.mtiles, at);
             j.q.units = __builtin_amdgcn_readlane(q.units, at);
             j.splits = splits_of(j.q, c);
-            j.mt = local % j.q.mtiles;
+            j.mt = j.q.mtiles - 1 - local % j.q.mtiles;    // a causal chunk's last rows see most: they go first
             const int g = __builtin_amdgcn_readlane(first, at) + 8 * (local / j.q.mtiles);
             j.split = g % j.splits;
             j.head = g / j.splits;
@@ -815,7 +815,7 @@ hipError_t run_rows(const AttentionArgs& a, void* workspace, hipStream_t stream)
     if constexpr (D == 256) {
         if (mt == 32) return run<T, D, 1, 2, 2, 32, 1>(a, workspace, stream);
         if (mt == 64) return run<T, D, 2, 1, 2, 64, 1>(a, workspace, stream);
-        return run<T, D, 4, 1, 2, 64, 1>(a, workspace, stream);
+        return run<T, D, 4, 1, 2, 32, 1>(a, workspace, stream);
     } else {
         if (mt == 32) return run<T, D, 1, 4, 1, 32, D == 64 ? 2 : 1>(a, workspace, stream);
         if (mt == 64) return run<T, D, 2, 2, 1, 32, 2>(a, workspace, stream);
