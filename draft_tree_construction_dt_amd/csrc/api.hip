@@ -814,7 +814,7 @@ extern "C" dt_status dt_tree_attention(const dt_kv_cache* kv, const dt_chunk* ch
     a.out_stride = p->out_stride;
     a.Hq = p->Hq;
     a.G = p->Hq / kv->Hkv;
-    a.by16 = kv->page_size % 16 == 0 && a.kv.slot_stride < (1 << 25);
+    a.by8 = kv->page_size % 8 == 0 && a.kv.slot_stride < (1 << 26);
     a.scale_log2 = (float)(p->scale * 1.4426950408889634074);
     a.lse = p->lse;
     const DeviceScope scope((hipStream_t)p->stream);

@@ -317,34 +317,40 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
         return p;
     };
     const auto is_valid = [&](const Place& p) __attribute__((always_inline)) { return p.page >= 0 && p.page < a.kv.num_pages; };
-    // Byte offsets of a lane's copies within the 16 rows they belong to.
+    // Byte offsets of a lane's copies within the 8 rows they belong to (the
+    // permutation of K's pieces repeats after 16).
     constexpr int kOwn = kCopies < kPer16 ? kCopies : kPer16;
-    static_assert(kCopies % kOwn == 0 && kPer16 % kOwn == 0, "a wave's copies lie in whole parts of 16 rows");
+    constexpr int kPer8 = kPer16 / 2 < kOwn ? kPer16 / 2 : kOwn;       // a wave's copies of 8 rows
+    static_assert(kCopies % kOwn == 0 && kPer16 % kOwn == 0 && kOwn % kPer8 == 0, "whole parts of 8 rows");
     uint32_t koff[kOwn], voff[kOwn];
     const int piece = lane % kUnits16, prow = lane / kUnits16;
     const uint32_t slot_bytes = (uint32_t)(a.kv.slot_stride * 2);
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-        const int rg = (wl * kCopies + i) % kPer16 * kRpi + prow;
-        koff[i] = rg * slot_bytes + (piece ^ swizzle_k<D>(rg)) * 16;
-        voff[i] = rg * slot_bytes + (piece ^ swizzle_v<D>(rg)) * 16;
+        const int r16 = (wl * kCopies + i) % kPer16 * kRpi + prow;
+        koff[i] = (r16 & 7) * slot_bytes + (piece ^ swizzle_k<D>(r16)) * 16;
+        voff[i] = (r16 & 7) * slot_bytes + (piece ^ swizzle_v<D>(r16)) * 16;
     }
-    // Copies of a tile into K's (V's) buffer; a key that is not there comes
-    // from some mapped address, its score and value are dropped below.
-    const auto issue = [&](const Place& p, bool is_v, int buf) __attribute__((always_inline)) {
-        const uint16_t* const from = is_v ? vbase : kbase;
-        const uint32_t to = group + (2 * is_v + buf) * S::kTile;
+    // Copies of a tile into a buffer of K and of V; a key that is not there
+    // comes from some mapped address, its score and value are dropped below.
+    const auto issue = [&](const Place& p, int buf) __attribute__((always_inline)) {
+        const uint32_t to = group + buf * S::kTile;
         const bool ok = is_valid(p);
-        if (a.by16) {
-            // 16 rows that begin at a multiple of 16 lie in one page
+        if (a.by8) {
+            // 8 rows that begin at a multiple of 8 lie in one page
 #pragma unroll
-            for (int g = 0; g < kCopies / kOwn; ++g) {
-                const int at = wl * kCopies + g * kOwn, row = at / kPer16 * 16;
+            for (int g = 0; g < kCopies / kPer8; ++g) {
+                const int at = wl * kCopies + g * kPer8, row = at * kRpi & ~7;
                 const int page = __builtin_amdgcn_readlane(ok ? p.page : 0, row);
                 const int in = __builtin_amdgcn_readlane(ok ? p.in : 0, row);
-                const char* base = (const char*)(from + page * a.kv.page_stride) + (int64_t)in * slot_bytes;
+                const int64_t off = page * a.kv.page_stride + in * a.kv.slot_stride;
+                const char* const kp = (const char*)(kbase + off);
+                const char* const vp = (const char*)(vbase + off);
 #pragma unroll
-                for (int i = 0; i < kOwn; ++i) copy_to_lds(base, is_v ? voff[i] : koff[i], to + (at + i) * 1024);
+                for (int i = 0; i < kPer8; ++i) {
+                    copy_to_lds(kp, koff[(g * kPer8 + i) % kOwn], to + (at + i) * 1024);
+                    copy_to_lds(vp, voff[(g * kPer8 + i) % kOwn], to + 2 * S::kTile + (at + i) * 1024);
+                }
             }
         } else {
             const int64_t off = ok ? p.page * a.kv.page_stride + p.in * a.kv.slot_stride : 0;
@@ -353,7 +359,8 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
             for (int i = 0; i < kCopies; ++i) {
                 const int at = wl * kCopies + i, trow = at * kRpi + prow;
                 const int64_t o = (int64_t)((u64)(uint32_t)__shfl(lo, trow) | (u64)(uint32_t)__shfl(hi, trow) << 32);
-                copy_to_lds(from + o + (piece ^ (is_v ? swizzle_v<D>(trow) : swizzle_k<D>(trow))) * 8, to + at * 1024);
+                copy_to_lds(kbase + o + (piece ^ swizzle_k<D>(trow)) * 8, to + at * 1024);
+                copy_to_lds(vbase + o + (piece ^ swizzle_v<D>(trow)) * 8, to + 2 * S::kTile + at * 1024);
             }
         }
     };
@@ -524,15 +531,13 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     Place place = look_up(wk);
     u64 valid = __ballot(is_valid(place)), valid1 = 0;     // of this round's tile and of the next
     if (wk < tiles) {
-        issue(place, false, 0);
-        issue(place, true, 0);
+        issue(place, 0);
     }
     place = look_up(wk + WK);
     if constexpr (kAlone) {
         valid1 = __ballot(is_valid(place));
         if (wk + WK < tiles) {
-            issue(place, false, 1);
-            issue(place, true, 1);
+            issue(place, 1);
             place = look_up(wk + 2 * WK);
         }
     }
@@ -549,8 +554,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
         if constexpr (!kAlone) {
             if (t + WK < tiles) {
                 valid = __ballot(is_valid(place));
-                issue(place, false, (i + 1) & 1);
-                issue(place, true, (i + 1) & 1);
+                issue(place, (i + 1) & 1);
                 place = look_up(t + 2 * WK);
             }
         }
@@ -568,8 +572,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
             if (t + 2 * WK < tiles) {
                 valid1 = __ballot(is_valid(place));
                 wait_reads();
-                issue(place, false, i & 1);
-                issue(place, true, i & 1);
+                issue(place, i & 1);
                 place = look_up(t + 3 * WK);
             }
         }

@@ -53,7 +53,7 @@ struct AttentionArgs {
     int64_t q_stride, out_stride;
     int Hq, G;
     float scale_log2;              // scale * log2(e)
-    bool by16;                     // slots 16 n .. 16 n + 15 lie in one page, within 2^31 bytes
+    bool by8;                      // slots 8 n .. 8 n + 7 lie in one page, within 2^31 bytes
     float* lse;
 };
 
