@@ -644,7 +644,7 @@ static dt_status check_chunk(const dt_chunk* c, bool pointers) {
     if (!c || c->B < 0 || c->lead < 0 || c->n_max < 0) return DT_ERR_INVALID_ARG;
     const int64_t rows = (int64_t)c->lead + c->n_max;
     if (rows < 1) return DT_ERR_INVALID_ARG;
-    if (c->B > 65535 || rows > kMaxChunkRows) return DT_ERR_UNSUPPORTED;
+    if (c->B > 65535 || rows > kMaxChunkRows || c->B * rows > kMaxBatchRows) return DT_ERR_UNSUPPORTED;
     if (pointers && c->B > 0 && (!c->ctx_len || misaligned(c->ctx_len, 4) || misaligned(c->n_nodes, 4) ||
                                  misaligned(c->mask, 4) || misaligned(c->depths, 4)))
         return DT_ERR_INVALID_ARG;

@@ -665,9 +665,14 @@ __global__ void __launch_bounds__(64 * WM * WK * WD, (PER_CU * WM * WK * WD + 3)
     if (blockIdx.x == 0 && threadIdx.x == 0) *plan = c;    // for combine_kernel
     if constexpr (LOOP) {
         for (int y = blockIdx.x >> 3;; y += gridDim.x >> 3) {
-            const Job job = job_of(a, q0, S::kMt, c, blockIdx.x & 7, y, lane);
+            // the arguments are read again for every job: kept over the loop
+            // they would cost the tile loop its registers
+            auto p = __builtin_amdgcn_kernarg_segment_ptr();
+            asm volatile("" : "+s"(p));
+            const AttentionArgs& args = *(const AttentionArgs*)p;
+            const Job job = job_of(args, q0, S::kMt, c, blockIdx.x & 7, y, lane);
             if (job.b < 0) return;
-            attend<T, D, WM, WK, WD, KT>(a, job, c, lds, partial);
+            attend<T, D, WM, WK, WD, KT>(args, job, c, lds, partial);
             __syncthreads();                               // the next job's copies overwrite what this one reads
         }
     } else {
@@ -761,6 +766,7 @@ __global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, const int
 // ---------------------------------------------------------------------------
 
 constexpr int kCus = 256;
+constexpr int64_t kMaxGrid = 1 << 20;
 constexpr int kPlanBytes = 256;    // of the workspace: the chunk's size
 
 // Row tile by the rows of a key head: up to 32 rows the waves share out the
@@ -797,8 +803,9 @@ hipError_t run(const AttentionArgs& a, void* workspace, hipStream_t stream) {
     // them in turn, and none is started for nothing.  Many segments of many
     // sizes: a workgroup a job, handed out as others end.
     const int64_t most = 8 * max_jobs(a, S::kMt, slots), mtiles = ((int64_t)a.c.rows * a.G + S::kMt - 1) / S::kMt;
-    const bool loop = most > slots && 2 * a.c.B * a.kv.Hkv * mtiles < slots;
-    const int64_t grid = loop ? slots : most;
+    const bool few = most > slots && 2 * a.c.B * a.kv.Hkv * mtiles < slots;
+    const bool loop = few || most > kMaxGrid;
+    const int64_t grid = few ? slots : (most > kMaxGrid ? kMaxGrid : most);
     const auto kernel = loop ? attention_kernel<T, D, WM, WK, WD, KT, PER_CU, true>
                              : attention_kernel<T, D, WM, WK, WD, KT, PER_CU, false>;
     int* const plan = (int*)workspace;

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
         for (int i0 = tid; i0 < n; i0 += kDeep * 256) {
             uint32_t t[kDeep];
 #pragma unroll
-            for (int j = 0; j < kDeep; ++j) t[j] = i0 + 256 * j < n ? (uint32_t)(h[i0 + 256 * j] - v0) : ~0u;
+            for (int j = 0; j < kDeep; ++j) t[j] = i0 + 256 * j < n ? (uint32_t)h[i0 + 256 * j] - (uint32_t)v0 : ~0u;
 #pragma unroll
             for (int j = 0; j < kDeep; ++j) {
                 if (t[j] >= (uint32_t)len) continue;
@@ -192,13 +192,13 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
     const int32_t* const bias_ids = a.bias_ids + (int64_t)b * a.n_bias;
     if (BIAS) {
         for (int i = tid; i < a.n_bias; i += 256) {
-            const uint32_t t = (uint32_t)(bias_ids[i] - v0);
+            const uint32_t t = (uint32_t)bias_ids[i] - (uint32_t)v0;
             if (t < (uint32_t)len) atomicOr(&s_biased[t >> 5], 1u << (t & 31));
         }
     }
     if (a.node_tokens) {
         for (int i = tid; i < nn; i += 256) {
-            const uint32_t t = (uint32_t)(a.node_tokens[(int64_t)b * a.n_max + i] - v0);
+            const uint32_t t = (uint32_t)a.node_tokens[(int64_t)b * a.n_max + i] - (uint32_t)v0;
             if (t >= (uint32_t)len) continue;
             s_node[atomicAdd(&s_nodes, 1)] = (uint32_t)i << 16 | t;
             touch(t);
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
         }
         __syncthreads();
         for (int i = tid; i < a.n_bias; i += 256) {
-            const uint32_t t = (uint32_t)(bias_ids[i] - v0);
+            const uint32_t t = (uint32_t)bias_ids[i] - (uint32_t)v0;
             if (t < (uint32_t)len) atomicMax(&s_bias[rank_of((int)t)], (uint32_t)i + 1);
         }
         __syncthreads();

@@ -94,6 +94,7 @@ struct CommitArgs {
 };
 
 constexpr int kMaxChunkRows = 65536;
+constexpr int64_t kMaxBatchRows = 1 << 24;
 constexpr int kMaxPassHeads = 4096;
 constexpr int kMaxCommitNodes = 1024;
 constexpr int64_t kMaxSlots = 1 << 30;

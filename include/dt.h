@@ -342,7 +342,7 @@ typedef struct dt_kv_cache {
 typedef struct dt_chunk {
     int32_t B;                 /* requests, 0 <= B <= 65535 */
     int32_t lead;              /* >= 0 */
-    int32_t n_max;             /* >= 0; 1 <= lead + n_max <= 65536 */
+    int32_t n_max;             /* >= 0; 1 <= lead + n_max <= 65536, B * (lead + n_max) <= 2^24 */
     const int32_t* ctx_len;    /* [B] tokens in the cache; < 0: the request has no rows */
     const int32_t* n_nodes;    /* [B], clamped to 0..n_max; NULL = n_max for all */
     const uint32_t* mask;      /* [B][n_max][ceil(n_max/32)] as dt_tree_out; NULL = every row sees

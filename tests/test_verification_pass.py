@@ -128,7 +128,7 @@ BAD_CACHES = [
 BAD_CHUNKS = [
     (dict(B=-1), BAD), (dict(lead=-1), BAD), (dict(n_max=-1), BAD), (dict(lead=0, n_max=0), BAD),
     (dict(ctx_len=None), BAD), (dict(ctx_len=FAKE + 1), BAD), (dict(n_nodes=FAKE + 2), BAD),
-    (dict(B=65536), LIMIT), (dict(lead=65530), LIMIT),
+    (dict(B=65536), LIMIT), (dict(lead=65530), LIMIT), (dict(B=4096, n_max=4096), LIMIT),
 ]
 
 
@@ -621,6 +621,116 @@ def test_attention_long_contexts(device, ragged):
     kv = bd.KVCache(dk, dv, torch.from_numpy(table).to(device))
     got, lse = run_attention(device, ctx, lead, n_max, nn, seen, q, kv, 1)
     check_attention(ctx, lead, n_max, nn, seen, q, k, v, table, P, got, lse, D ** -0.5, dtype, 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["one", "few", "tree", "chunk"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_behind_a_wide_page_table(device, kind, D):
+    """A page table for far longer contexts than there are: the split is
+    derived from the lengths, and few segments go over resident workgroups."""
+    say(f"[case] wide table {kind} {D}")
+    spec = dict(one=([2900], 1, 0, None, None, 8, 2, D, 16, BF16, "slots"),
+                few=([700, 1], 1, 15, [15, 9], "tree", 4, 1, D, 16, F16, "slots"),
+                tree=([1500], 1, 64, [61], "tree", 4, 1, D, 8, BF16, "slots"),
+                chunk=([300], 0, 200, [199], None, 4, 1, D, 24, F16, "slots"))[kind]
+    ctx, lead, n_max, nn, _, Hq, Hkv, _, P, dtype, _ = spec
+    k, v, table, seen, q = attention_problem(90, spec=spec)
+    wide = np.full((len(ctx), 20000), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    dk, dv = pair_on_device(k, v, device)
+    kv = bd.KVCache(dk, dv, torch.from_numpy(wide).to(device))
+    got, lse = run_attention(device, ctx, lead, n_max, nn, seen, q, kv, 0)
+    check_attention(ctx, lead, n_max, nn, seen, q, k, v, wide, P, got, lse, D ** -0.5, dtype, 0)
+
+
+@pytest.mark.gpu
+def test_attention_of_many_requests(device):
+    """More requests than a wave has lanes, of very different lengths, some
+    without rows, some without nodes; also more than the chunk search takes."""
+    for B, ctx_of in ((150, lambda i: [-1, 0, 17, 900][i % 4] + i % 3), (700, lambda i: (i * 7) % 90)):
+        say(f"[case] {B} requests")
+        ctx = [max(ctx_of(i), -1) for i in range(B)]
+        nn = [(i * 5) % 4 for i in range(B)]
+        spec = (ctx, 1, 3, nn, "tree", 2, 1, 64, 16, BF16, "slots")
+        k, v, table, seen, q = attention_problem(91, spec=spec)
+        dk, dv = pair_on_device(k, v, device)
+        kv = bd.KVCache(dk, dv, torch.from_numpy(table).to(device))
+        got, lse = run_attention(device, ctx, 1, 3, nn, seen, q, kv, 0)
+        check_attention(ctx, 1, 3, nn, seen, q, k, v, table, 16, got, lse, 0.125, BF16, 0)
+
+
+@pytest.mark.gpu
+def test_lengths_beyond_the_table(device):
+    """ctx_len up to the largest int32: slots behind the table are dropped on
+    writing and unseen on reading."""
+    say("[case] lengths beyond the table")
+    P, D, far = 16, 64, 2 ** 31 - 1
+    gen = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(3, P, 1, D, generator=gen).to(BF16).to(device) for _ in range(2))
+    was = k.clone(), v.clone()
+    table = torch.tensor([[2, 0, 1], [1, 2, 0]], dtype=torch.int32, device=device)
+    kv = bd.KVCache(k, v, table)
+    x = torch.randn(2, 5, 1, D, generator=gen).to(BF16).to(device)
+    chunk = bd.Chunk(torch.tensor([far, far - 3], dtype=torch.int32, device=device), 5)
+    freqs = bd.dt_rope_frequencies(D, 10000.0)[0].to(device)
+    q = torch.empty_like(x)
+    bd.dt_kv_append(kv, chunk, x, x, q=x, q_out=q, freqs=freqs)
+    torch.cuda.synchronize()
+    assert torch.equal(k, was[0]) and torch.equal(v, was[1])
+    want, size = ref.append_head(x[0, 4, 0].cpu().double().numpy(), None, 0, far + 4, freqs.cpu().numpy(), False, 1.0)
+    assert np.all(np.abs(q[0, 4, 0].cpu().double().numpy() - want) <= ref.append_tolerance(want, size, BF16))
+    got, lse = run_attention(device, [far, far - 3], 5, 0, None, None, x.cpu(), kv, 0)
+    host = table.cpu().numpy()
+    for b in range(2):
+        K, V = (torch.cat([t[p] for p in host[b]]).cpu().double().numpy()[:, 0] for t in (k, v))
+        for r in range(5):
+            w, _, spread, slack, vmax = ref.attend_row(x[b, r, 0].cpu().double().numpy(), K, V, D ** -0.5)
+            assert np.all(np.abs(got[b, r, 0] - w) <= ref.attend_tolerance(w, spread, slack, vmax, 48, BF16))
+
+
+@pytest.mark.gpu
+def test_calls_in_flight_on_two_streams(device):
+    """Appends, attention and logits of two batches on two streams, each with
+    its own workspace, give each call's own results; so does a side stream
+    passed to the call instead of the current one."""
+    say("[case] two streams")
+    jobs = []
+    for i, spec in enumerate((([4000, 35, 812], 1, 20, [20, 7, 15], "tree", 8, 2, 128, 16, BF16, "slots"),
+                              ([3000, 700], 1, 0, None, None, 8, 2, 128, 16, BF16, "slots"))):
+        k, v, table, seen, q = attention_problem(95 + i, spec=spec)
+        dk, dv = pair_on_device(k, v, device)
+        kv = bd.KVCache(dk, dv, torch.from_numpy(table).to(device))
+        i32 = dict(dtype=torch.int32, device=device)
+        mask = None if seen is None else torch.from_numpy(ref.pack_bits(seen)).to(device)
+        chunk = bd.Chunk(torch.tensor(spec[0], **i32), spec[1], spec[2],
+                         None if spec[3] is None else torch.tensor(spec[3], **i32), mask=mask)
+        ws = torch.empty(bd.dt_attention_workspace(kv, chunk, 8), dtype=torch.uint8, device=device)
+        dq = to_device(q, device)
+        x = torch.randn(4, 3, 20001, device=device)
+        hist = torch.randint(0, 20001, (4, 500), **i32)
+        hlen = torch.full((4,), 500, **i32)
+        freq = torch.full((4,), 0.25, device=device)
+        jobs.append((kv, chunk, dq, torch.zeros_like(dq), ws, x, torch.zeros_like(x), hist, hlen, freq,
+                     torch.cuda.Stream()))
+
+    def call(j, **kw):
+        bd.dt_tree_attention(j[0], j[1], j[2], j[3], workspace=j[4], **kw)
+        bd.dt_process_logits(j[5], j[6], history=j[7], history_len=j[8], frequency=j[9], **kw)
+
+    alone = []
+    for j in jobs:
+        call(j)
+        torch.cuda.synchronize()
+        alone.append((j[3].clone(), j[6].clone()))
+        j[3].zero_(), j[6].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for j in jobs:
+            call(j, stream=j[10])
+    torch.cuda.synchronize()
+    for j, (o, y) in zip(jobs, alone):
+        assert torch.equal(j[3], o) and torch.equal(j[6], y)
 
 
 @pytest.mark.gpu
