@@ -447,7 +447,8 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int x = 0; x < 16; ++x) top = fmaxf(top, s[n][x]);
-        top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
+        const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+        top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * a.scale_log2;
         // The sums are kept relative to an m that may lag the maximum by
         // kLazy: weights stay below 2^8, exact in relative terms for both
         // types, and most tiles leave o alone.
