@@ -141,6 +141,18 @@ __device__ inline int partials_of(const AttentionArgs& a, const Request& q, int 
     return splits > 1 ? q.mtiles * a.kv.Hkv * splits : 0;
 }
 
+// Row tiles of nearly equal size: the blocks of 32 rows are dealt out so that
+// tiles differ by one block at most (trees of 64 nodes and a root with four
+// heads to a key head have 260 rows: three tiles of three blocks instead of
+// 4, 4 and 1).  The first `more` tiles have base + 1 blocks.
+struct Tiling {
+    int base, more;
+};
+__device__ inline Tiling tiling_of(int mrows, int mtiles) {
+    const int blocks = (mrows + kRowsPerWave - 1) / kRowsPerWave, base = blocks / mtiles;
+    return {base, blocks - base * mtiles};
+}
+
 struct Job {
     int b, head, mt, split, splits, slot;   // slot: of its partial result
     Request q;
@@ -257,9 +269,12 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     const int mrows = job.q.rows * a.G;
 
     // this lane's query
-    const int m0 = job.mt * S::kMt + wm * kRowsPerWave;
+    const Tiling tiling = tiling_of(mrows, job.q.mtiles);
+    const int first_block = job.mt * tiling.base + (job.mt < tiling.more ? job.mt : tiling.more);
+    const int blocks = tiling.base + (job.mt < tiling.more);
+    const int m0 = (first_block + wm) * kRowsPerWave;
     const int mrow = m0 + col;
-    const bool live = mrow < mrows;
+    const bool live = wm < blocks && mrow < mrows;
     const int r = live ? mrow / a.G : 0, g = live ? mrow - r * a.G : 0;
     const int64_t row = (int64_t)b * a.c.rows + r;
     const int h = job.head * a.G + g;
@@ -282,12 +297,12 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     }
     all = uniform(all);
     any = uniform(any);
-    const bool work = m0 < mrows;
+    const bool work = wm < blocks && m0 < mrows;
     const int64_t limit = (int64_t)ctx + r + 1;            // causal rows: first unseen key
     const int64_t first_node = (int64_t)ctx + lead;        // slot of node 0
 
     // the chunk's tiles, shortened to what the workgroup's rows see
-    int last_row = ((job.mt + 1) * S::kMt - 1) / a.G;
+    int last_row = ((first_block + blocks) * kRowsPerWave - 1) / a.G;
     if (last_row > job.q.rows - 1) last_row = job.q.rows - 1;
     int64_t end = (int64_t)ctx + (a.c.mask && last_row >= lead ? job.q.rows : last_row + 1);
     if (end > job.q.keys) end = job.q.keys;
@@ -717,7 +732,13 @@ __global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, const int
             const int b = b0 + at, splits = __shfl(my_splits, at), mtiles = __shfl(mine.mtiles, at);
             const int item = local - __shfl(upto, at) + __shfl(n, at);
             const int r = item / a.Hq, h = item - r * a.Hq;
-            const int hk = h / a.G, mrow = r * a.G + (h - hk * a.G), mt = mrow / MT, in = mrow - mt * MT;
+            const int hk = h / a.G, mrow = r * a.G + (h - hk * a.G), block = mrow / kRowsPerWave;
+            const Tiling tiling = tiling_of(__shfl(mine.rows, at) * a.G, mtiles);
+            const int long_ones = tiling.more * (tiling.base + 1);     // blocks of the larger tiles
+            const int mt = block < long_ones ? block / (tiling.base + 1)
+                                             : tiling.more + (block - long_ones) / tiling.base;
+            const int first_block = mt * tiling.base + (mt < tiling.more ? mt : tiling.more);
+            const int in = mrow - first_block * kRowsPerWave;
             const int64_t first = (int64_t)partials_before + __shfl(partials_upto, at) - __shfl(partials, at) +
                                   (int64_t)hk * splits * mtiles + mt;
             const float* part = partial + first * (MT * (D + 2));
