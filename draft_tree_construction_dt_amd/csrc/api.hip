@@ -738,7 +738,7 @@ extern "C" dt_status dt_rope_frequencies(int32_t kind, int32_t rot_dim, double b
 
 extern "C" dt_status dt_kv_append(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_append_params* p) {
     if (!p) return DT_ERR_INVALID_ARG;
-    dt_status st = check_cache(kv, true);
+    dt_status st = check_cache(kv, !chunk || chunk->B != 0);
     if (st != DT_OK) return st;
     if ((st = check_chunk(chunk, true)) != DT_OK) return st;
     if (p->layer < 0 || p->layer >= kv->layers || !isfinite(p->eps) || p->eps < 0 || !isfinite(p->rot_scale))
@@ -793,7 +793,7 @@ extern "C" dt_status dt_tree_attention(const dt_kv_cache* kv, const dt_chunk* ch
     if (!p) return DT_ERR_INVALID_ARG;
     dt_status st = check_attention_shape(kv, chunk, p->Hq);
     if (st != DT_OK) return st;
-    if ((st = check_cache(kv, true)) != DT_OK) return st;
+    if ((st = check_cache(kv, chunk->B != 0)) != DT_OK) return st;
     if ((st = check_chunk(chunk, true)) != DT_OK) return st;
     if (p->layer < 0 || p->layer >= kv->layers || !isfinite(p->scale) || !(p->scale > 0)) return DT_ERR_INVALID_ARG;
     if (misaligned(p->lse, 4)) return DT_ERR_INVALID_ARG;
@@ -876,7 +876,7 @@ extern "C" dt_status dt_process_logits(const dt_logits_params* p) {
 extern "C" dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_commit_params* p) {
     if (!p) return DT_ERR_INVALID_ARG;
     dt_status st;
-    if (kv && (st = check_cache(kv, true)) != DT_OK) return st;
+    if (kv && (st = check_cache(kv, !chunk || chunk->B != 0)) != DT_OK) return st;
     if ((st = check_chunk(chunk, true)) != DT_OK) return st;
     if (chunk->lead < 1 || p->L < 1) return DT_ERR_INVALID_ARG;
     if (chunk->n_max > kMaxCommitNodes) return DT_ERR_UNSUPPORTED;

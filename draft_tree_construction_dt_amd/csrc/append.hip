@@ -21,7 +21,8 @@ namespace {
 
 constexpr int kMaxPairs = 128;     // rot_dim <= 256
 constexpr int kDeep = 4;           // groups of heads of a wave in flight
-constexpr int kWaves = 2048;       // waves that fill the chip: fewer rows are shared by waves
+constexpr int kWaves = 2048;       // waves that fill the chip: fewer rows are shared by waves (one token
+                                   // on one wave: 12.8 us)
 
 template <class T, int D>
 __global__ void __launch_bounds__(256) append_kernel(AppendArgs a, int parts) {

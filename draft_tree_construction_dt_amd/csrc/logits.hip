@@ -9,14 +9,14 @@
 // tokens lie in the chunk at all (most chunks have none).
 //
 // The kernel is bound by memory: every logit is read and written once.  What
-// stands in the way is latency, so the tables are kept small (8 workgroups a
-// compute unit): counts in 16 bits where the history is short enough, biases
-// by their rank among the chunk's biased tokens.  The counts are kept as
-// [t % 8][t / 8], so that a wave's reads of a vector's j-th token are
-// consecutive words whatever the row's alignment.  Measured: 64 requests x 8
-// rows of 151936 bf16 logits behind 2048-4096 tokens, half of the rows masked,
-// in 91 us (3.5 TB/s; a copy of the same bytes takes 65); the same without
-// history, biases and masks 75 us.
+// stands in the way is latency, so the tables are kept small (7 or 8
+// workgroups a compute unit): biases are found by their rank among the chunk's
+// biased tokens (with a word a token instead the case below took 116 us).
+// The counts are kept as [t % 8][t / 8], so that a wave's reads of a vector's
+// j-th token are consecutive words whatever the row's alignment.  Measured: 64
+// requests x 8 rows of 151936 bf16 logits behind 2048-4096 tokens, half of the
+// rows masked, in 91 us (3.5 TB/s; a copy of the same bytes takes 65); the same
+// without history, biases and masks 75 us.
 #include <math.h>
 
 #include "pass.h"
@@ -28,7 +28,6 @@ namespace {
 constexpr int kChunk = 4096;               // tokens of a workgroup
 constexpr int kWords = kChunk / 32;        // of a bit a token
 constexpr int64_t kWorkgroups = 2048;
-constexpr int kMaxShort = 32767;           // occurrences that 15 bits count
 // A lane goes through its vector's few entries one by one; a wave in which a
 // lane has more does all tokens of its vectors at once (the benchmark's draft
 // logits behind 4096 tokens, inputs in the last-level cache: all at once
@@ -79,24 +78,9 @@ struct Io<uint16_t> {
 };
 
 // How often each token of the chunk was generated, and a flag (the highest
-// bit of its count) for one that occurs in the prompt: 32 bits a token, or 16
-// with tokens t and t + kChunk / 2 in one word.
-template <bool WIDE>
-struct Counts {
-    static constexpr int kSize = WIDE ? kChunk : kChunk / 2;
-    static constexpr uint32_t kPrompt = WIDE ? 0x80000000u : 0x8000u;
-    static __device__ inline int word(int t) {
-        const int u = WIDE ? t : t & (kChunk / 2 - 1);
-        return (u & 7) * (kSize / 8) + (u >> 3);
-    }
-    static __device__ inline int shift(int t) { return WIDE ? 0 : (t / (kChunk / 2)) * 16; }
-    static __device__ inline uint32_t get(const uint32_t* s, int t) {
-        const uint32_t w = s[word(t)] >> shift(t);
-        return WIDE ? w : w & 0xFFFFu;
-    }
-    static __device__ inline void add(uint32_t* s, int t, int by) { atomicAdd(&s[word(t)], (uint32_t)by << shift(t)); }
-    static __device__ inline void prompt(uint32_t* s, int t) { atomicOr(&s[word(t)], kPrompt << shift(t)); }
-};
+// bit of its count) for one that occurs in the prompt.
+constexpr uint32_t kPrompt = 0x80000000u;
+__device__ inline int place(int t) { return (t & 7) * (kChunk / 8) + (t >> 3); }
 
 // Eight bits (of which the caller wants the first few) from bit `at` of a
 // bitmap in LDS, `last` the last bit that is wanted.
@@ -105,13 +89,12 @@ __device__ inline uint32_t bits_at(const uint32_t* bitmap, int at, int last) {
     return (p[at >> 3] | (uint32_t)p[last >> 3] << 8) >> (at & 7);
 }
 
-template <class T, bool WIDE, bool BIAS>
+template <class T, bool BIAS>
 __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
-    using C = Counts<WIDE>;
     constexpr int kVec = Io<T>::kVec, kPer = kChunk / kVec / 256;    // full vectors of a thread and row
     extern __shared__ uint32_t lds[];
     uint32_t* const s_cnt = lds;
-    uint32_t* const s_touched = s_cnt + C::kSize;          // tokens with a count, or on some node's path
+    uint32_t* const s_touched = s_cnt + kChunk;            // tokens with a count, or on some node's path
     uint32_t* const s_biased = s_touched + kWords;         // tokens with a bias
     uint32_t* const s_rank = s_biased + (BIAS ? kWords : 0);         // biased tokens before each 32
     uint32_t* const s_bias = s_rank + (BIAS ? kWords : 0);           // their biases, by rank
@@ -186,8 +169,8 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
 #pragma unroll
             for (int j = 0; j < kDeep; ++j) {
                 if (t[j] >= (uint32_t)len) continue;
-                if (i0 + 256 * j < np) C::prompt(s_cnt, (int)t[j]);
-                else C::add(s_cnt, (int)t[j], 1);
+                if (i0 + 256 * j < np) atomicOr(&s_cnt[place((int)t[j])], kPrompt);
+                else atomicAdd(&s_cnt[place((int)t[j])], 1u);
                 touch(t[j]);
             }
         }
@@ -234,7 +217,7 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
                 pres = a.presence ? a.presence[b] : 0.0f, inv = 1.0f / rep;
     // the penalties of token t; false where there are none
     const auto penalise = [&](int t, float& x) {
-        const uint32_t c = C::get(s_cnt, t), n = c & ~C::kPrompt;
+        const uint32_t c = s_cnt[place(t)], n = c & ~kPrompt;
         const float y = c ? x * (x > 0 ? inv : rep) : x;
         x = n ? y - __builtin_fmaf(freq, (float)n, pres) : y;
         return c != 0;
@@ -245,15 +228,15 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
         const uint8_t* const allow_next = allow_of(i);
         if (r + step < rows) load(r + step, allow_next, next);
         const bool path = nodes > 0 && r >= a.lead;
-        const auto walk = [&](int by) {
+        const auto walk = [&](uint32_t by) {
             const uint32_t* const m = a.node_mask + ((int64_t)b * a.n_max + r - a.lead) * a.mask_words;
             for (int k = tid; k < nodes; k += 256) {
                 const uint32_t e = s_node[k], node = e >> 16;
-                if (m[node >> 5] >> (node & 31) & 1) C::add(s_cnt, (int)(e & 0xFFFF), by);
+                if (m[node >> 5] >> (node & 31) & 1) atomicAdd(&s_cnt[place((int)(e & 0xFFFF))], by);
             }
         };
         if (path) {
-            walk(1);
+            walk(1u);
             __syncthreads();
         }
         const int miss = miss_of(r);
@@ -320,7 +303,7 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
         if (miss > 0 && tid < miss && kChunk - miss + tid < len) single(kChunk - miss + tid);
         if (path) {
             __syncthreads();
-            walk(-1);
+            walk(~0u);
             __syncthreads();
         }
         cur = next;
@@ -328,7 +311,7 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
     }
 }
 
-template <class T, bool WIDE>
+template <class T>
 hipError_t run(const LogitsArgs& a, hipStream_t stream) {
     const int64_t chunks = (a.V + kChunk - 1) / kChunk;
     // a table serves several rows once there are some workgroups a compute unit
@@ -338,19 +321,17 @@ hipError_t run(const LogitsArgs& a, hipStream_t stream) {
     // (the draft logits of 64 requests 101 -> 93 us)
     const dim3 grid((unsigned)a.B, (unsigned)chunks, (unsigned)z);
     const int biases = a.n_bias < kChunk ? a.n_bias : kChunk;
-    const size_t words = Counts<WIDE>::kSize + kWords + (a.n_bias > 0 ? 2 * kWords + biases : 0) +
+    const size_t words = kChunk + kWords + (a.n_bias > 0 ? 2 * kWords + biases : 0) +
                          (a.node_tokens ? a.n_max : 0);
-    if (a.n_bias > 0) logits_kernel<T, WIDE, true><<<grid, 256, words * 4, stream>>>(a);
-    else logits_kernel<T, WIDE, false><<<grid, 256, words * 4, stream>>>(a);
+    if (a.n_bias > 0) logits_kernel<T, true><<<grid, 256, words * 4, stream>>>(a);
+    else logits_kernel<T, false><<<grid, 256, words * 4, stream>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_logits(const LogitsArgs& a, int dtype, hipStream_t stream) {
-    const bool wide = (int64_t)a.history_max + (a.node_tokens ? a.n_max : 0) > kMaxShort;
-    if (dtype == DT_DTYPE_F32) return wide ? run<float, true>(a, stream) : run<float, false>(a, stream);
-    return wide ? run<uint16_t, true>(a, stream) : run<uint16_t, false>(a, stream);
+    return dtype == DT_DTYPE_F32 ? run<float>(a, stream) : run<uint16_t>(a, stream);
 }
 
 }  // namespace dt

@@ -265,6 +265,13 @@ def test_binding_checks_tensors():
         bd.dt_kv_append(kv, chunk, q[:, :, :3], q[:, :, :2])
     with pytest.raises(bd.DtError):
         bd.dt_kv_append(bd.KVCache(k, k.clone(), table[:1]), chunk, q[:, :, :2], q[:, :, :2])
+    none = bd.KVCache(k, k.clone(), table[:0]), bd.Chunk(ctx[:0], lead=3)       # an empty batch: nothing is launched
+    bd.dt_tree_attention(*none, q[:0], out[:0], workspace=None if bd.dt_attention_workspace(*none, 4) == 0 else
+                         torch.empty(bd.dt_attention_workspace(*none, 4), dtype=torch.uint8))
+    bd.dt_kv_append(*none, q[:0, :, :2], q[:0, :, :2], q=q[:0], q_out=out[:0])
+    bd.dt_process_logits(torch.zeros(0, 3, 50), torch.zeros(0, 3, 50))
+    bd.dt_commit_path(*none, None, None, torch.zeros(0, 3, dtype=torch.int32), torch.zeros(0, 4, dtype=torch.int32),
+                      torch.zeros(0, dtype=torch.int32))
     x = torch.zeros(2, 3, 50)
     for bad in (dict(out=x.bfloat16()), dict(history=torch.zeros(2, 5)), dict(frequency=torch.zeros(3)),
                 dict(lead=4), dict(allow=torch.zeros(6, 1, dtype=torch.int32)),
@@ -658,6 +665,24 @@ def test_attention_of_many_requests(device):
         kv = bd.KVCache(dk, dv, torch.from_numpy(table).to(device))
         got, lse = run_attention(device, ctx, 1, 3, nn, seen, q, kv, 0)
         check_attention(ctx, 1, 3, nn, seen, q, k, v, table, 16, got, lse, 0.125, BF16, 0)
+
+
+@pytest.mark.gpu
+def test_attention_of_the_largest_batch(device):
+    """65535 requests of one token each: a row that sees one key is its value."""
+    say("[case] largest batch")
+    B, Hkv, D = 65535, 8, 64
+    gen = torch.Generator(device=device).manual_seed(1)
+    k, v = (torch.empty(B, 1, Hkv, D, dtype=BF16, device=device).normal_(generator=gen) for _ in range(2))
+    table = torch.randperm(B, device=device).to(torch.int32)[:, None].contiguous()
+    kv = bd.KVCache(k, v, table)
+    chunk = bd.Chunk(torch.zeros(B, dtype=torch.int32, device=device))
+    q = torch.empty(B, 1, Hkv, D, dtype=BF16, device=device).normal_(generator=gen)
+    out = torch.zeros_like(q)
+    ws = torch.empty(bd.dt_attention_workspace(kv, chunk, Hkv), dtype=torch.uint8, device=device)
+    bd.dt_tree_attention(kv, chunk, q, out, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:, 0], v[table[:, 0].long(), 0])
 
 
 @pytest.mark.gpu
