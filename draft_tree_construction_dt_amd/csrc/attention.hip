@@ -31,10 +31,10 @@
 // A segment in one chunk is written at once, others by combine_kernel.
 //
 // Measured (bf16, heads of 128, 4 query heads to a key head, pages of 16): 64
-// requests' single tokens over 33-16383 keys, 2.15 GB of cache, in 406 us, 5.3
+// requests' single tokens over 33-16383 keys, 2.15 GB of cache, in 404 us, 5.3
 // TB/s (a copy reads and writes 4.9); two chunks of 2048 over 6-14 K keys in
-// 732-775 us, 915-967 TFLOP/s (a large matrix product: 1402), matrix cores 47%
-// and vector units 48% busy; one token over 4096 keys in 17 us, all latency.
+// 732-775 us, 915-967 TFLOP/s (a large matrix product: 1402), matrix cores 46%
+// and vector units 47% busy; one token over 4096 keys in 17 us, all latency.
 #include <math.h>
 
 #include "pass.h"

@@ -714,6 +714,50 @@ def test_lengths_beyond_the_table(device):
             assert np.all(np.abs(got[b, r, 0] - w) <= ref.attend_tolerance(w, spread, slack, vmax, 48, BF16))
 
 
+@pytest.mark.parametrize("index,current,moved", [(-1, 0, []), (0, 0, []), (1, 0, [1]), (0, 1, [0])])
+def test_calls_are_made_on_their_tensors_device(monkeypatch, index, current, moved):
+    """A device's default stream has a null handle, so the call has to be made
+    with that device current, and leaves the current one as it was."""
+    seen = []
+
+    class Device:
+        def __init__(self, i):
+            self.i = i
+
+        def __enter__(self):
+            seen.append(self.i)
+
+        def __exit__(self, *exc):
+            seen.append("left")
+
+    monkeypatch.setattr(bd, "_current_device", lambda: current)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+
+    def call(x, y):
+        assert seen == moved
+        return x + y
+
+    assert bd._on_device(index, call, 2, 3) == 5
+    assert seen == (moved + ["left"] if moved else [])
+
+
+def test_every_call_goes_through_its_device(monkeypatch):
+    """The four entry points that launch are called by way of their tensors' device."""
+    seen = []
+    monkeypatch.setattr(bd, "_on_device", lambda index, call, *args: seen.append((index, call.__name__)) or 0)
+    k = torch.zeros(2, 16, 1, 64, dtype=BF16)
+    kv = bd.KVCache(k, torch.zeros_like(k), torch.zeros(1, 2, dtype=torch.int32))
+    chunk = bd.Chunk(torch.zeros(1, dtype=torch.int32))
+    x = torch.zeros(1, 1, 1, 64, dtype=BF16)
+    i32 = torch.zeros(1, 1, dtype=torch.int32)
+    bd.dt_kv_append(kv, chunk, x, x)
+    bd.dt_tree_attention(kv, chunk, x, torch.empty_like(x))
+    bd.dt_process_logits(torch.zeros(1, 1, 32), torch.zeros(1, 1, 32))
+    bd.dt_commit_path(kv, chunk, None, None, i32, i32.clone(), torch.zeros(1, dtype=torch.int32))
+    assert seen == [(-1, name) for name in ("dt_kv_append", "dt_tree_attention", "dt_process_logits",
+                                            "dt_commit_path")]
+
+
 @pytest.mark.gpu
 def test_calls_in_flight_on_two_streams(device):
     """Appends, attention and logits of two batches on two streams, each with
