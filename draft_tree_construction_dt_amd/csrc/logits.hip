@@ -15,8 +15,8 @@
 // The counts are kept as [t % 8][t / 8], so that a wave's reads of a vector's
 // j-th token are consecutive words whatever the row's alignment.  Measured: 64
 // requests x 8 rows of 151936 bf16 logits behind 2048-4096 tokens, half of the
-// rows masked, in 91 us (3.5 TB/s; a copy of the same bytes takes 65); the same
-// without history, biases and masks 75 us.
+// rows masked, in 90 us (3.5 TB/s; a copy of the same bytes takes 65); the same
+// without history, biases and masks 68 us.
 #include <math.h>
 
 #include "pass.h"
@@ -29,9 +29,9 @@ constexpr int kChunk = 4096;               // tokens of a workgroup
 constexpr int kWords = kChunk / 32;        // of a bit a token
 constexpr int64_t kWorkgroups = 2048;
 // A lane goes through its vector's few entries one by one; a wave in which a
-// lane has more does all tokens of its vectors at once (the benchmark's draft
-// logits behind 4096 tokens, inputs in the last-level cache: all at once
-// 91 us, one by one 78, chosen 70).
+// lane has more does all tokens of its vectors at once (16 requests' draft logits
+// behind 4096 tokens: chosen 33 us, all at once 38, one by one 37.5; with 64
+// requests memory is the bound and all three take 91).
 constexpr int kFew = 3;
 
 template <class T>
@@ -318,7 +318,8 @@ hipError_t run(const LogitsArgs& a, hipStream_t stream) {
     int64_t z = (kWorkgroups + chunks * a.B - 1) / (chunks * a.B);
     z = z < a.rows ? z : a.rows;
     // the chunks of low ids first: they hold most entries and take longest
-    // (the draft logits of 64 requests 101 -> 93 us)
+    // (the draft logits of 64 requests 98 -> 91 us; 32 trees behind 8000 tokens
+    // lose: 151 -> 158)
     const dim3 grid((unsigned)a.B, (unsigned)chunks, (unsigned)z);
     const int biases = a.n_bias < kChunk ? a.n_bias : kChunk;
     const size_t words = kChunk + kWords + (a.n_bias > 0 ? 2 * kWords + biases : 0) +
