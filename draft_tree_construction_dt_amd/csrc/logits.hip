@@ -236,6 +236,9 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
             }
         };
         if (path) {
+            // The row before, if it has no path, has no barrier of its own: its
+            // counts have to be read by every wave before this row's are added.
+            if (i > 1 && r - step < a.lead) __syncthreads();
             walk(1u);
             __syncthreads();
         }
