@@ -389,6 +389,19 @@ def _on_device(index: int, call, *args):
         return call(*args)
 
 
+def _reachable(index: int, B: int, call):
+    """`call`, or a refusal in its place where the tensors lie in host memory,
+    which kernels cannot reach (an empty batch launches none)."""
+    if index >= 0 or B == 0:
+        return call
+
+    def refuse(*_):
+        raise DtError(DT_ERR_INVALID_ARG, f"{refuse.__name__}: the tensors must be on a GPU")
+
+    refuse.__name__ = call.__name__
+    return refuse
+
+
 class KVCache:
     """A paged cache of keys and values (dt_kv_cache): k and v of shape
     [pages][page_size][Hkv][D], or [layers][pages][page_size][Hkv][D] for one
@@ -500,7 +513,8 @@ def dt_kv_append(kv: KVCache, chunk: Chunk, k: torch.Tensor, v: torch.Tensor, q:
         _need(q.dim() == 4, w, "q must be [B][lead + n_max][heads][D]")
         Hq = int(q.shape[2])
     heads, kv_heads = (B, rows, Hq, D), (B, rows, kv.Hkv, D)
-    st = _on_device(index, _load().dt_kv_append, kv._ref, chunk._ref, _pack_append(
+    call = _reachable(index, B, _load().dt_kv_append)
+    st = _on_device(index, call, kv._ref, chunk._ref, _pack_append(
         0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if q_out is None else q_out.data_ptr(),
         _row_stride(q, heads, kv, w, "q"), _row_stride(k, kv_heads, kv, w, "k"), _row_stride(v, kv_heads, kv, w, "v"),
         _row_stride(q_out, heads, kv, w, "q_out"), Hq, _at(q_norm, (D,), dtype, index, w, "q_norm"),
@@ -529,7 +543,8 @@ def dt_tree_attention(kv: KVCache, chunk: Chunk, q: torch.Tensor, out: torch.Ten
     heads = (chunk.B, chunk.rows, Hq, kv.D)
     _need(workspace is None or (workspace.get_device() == index and workspace.is_contiguous()), w,
           "workspace must be contiguous, on the cache's device")
-    st = _on_device(index, _load().dt_tree_attention, kv._ref, chunk._ref, _pack_attention(
+    call = _reachable(index, chunk.B, _load().dt_tree_attention)
+    st = _on_device(index, call, kv._ref, chunk._ref, _pack_attention(
         q.data_ptr(), out.data_ptr(), _row_stride(q, heads, kv, w, "q"), _row_stride(out, heads, kv, w, "out"), Hq,
         kv.D ** -0.5 if scale is None else scale, _at(lse, heads[:3], torch.float32, index, w, "lse"), layer,
         0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
@@ -562,7 +577,8 @@ def dt_process_logits(logits: torch.Tensor, out: torch.Tensor, history: Optional
     hmax = 0 if history is None else history.shape[1]
     nb = 0 if bias_ids is None else bias_ids.shape[1]
     arows = 0 if allow is None else allow.shape[0]
-    st = _on_device(dev, _load().dt_process_logits, _pack_logits(
+    call = _reachable(dev, B, _load().dt_process_logits)
+    st = _on_device(dev, call, _pack_logits(
         _at(logits, logits.shape, logits.dtype, dev, w, "logits"), _at(out, logits.shape, logits.dtype, dev, w, "out"),
         B, lead, n_max, V, _LOGIT_TYPES[logits.dtype],
         _at(n_nodes, each, i32, dev, w, "n_nodes"), _at(history, (B, hmax), i32, dev, w, "history"), hmax,
@@ -589,7 +605,8 @@ def dt_commit_path(kv: Optional[KVCache], chunk: Chunk, tokens: Optional[torch.T
     _pass_devices(kv, chunk, w)
     _need(accepted.dim() == 2, w, "accepted must be int32 [B][L]")
     B, L = chunk.B, accepted.shape[1]
-    st = _on_device(dev, _load().dt_commit_path, 0 if kv is None else kv._ref, chunk._ref, _pack_commit(
+    call = _reachable(dev, B, _load().dt_commit_path)
+    st = _on_device(dev, call, 0 if kv is None else kv._ref, chunk._ref, _pack_commit(
         _at(tokens, (B, chunk.n_max), i32, dev, w, "tokens"), _at(parents, (B, chunk.n_max), i32, dev, w, "parents"),
         _at(target, (B, chunk.rows), i32, dev, w, "target"), L, _at(accepted, (B, L), i32, dev, w, "accepted"),
         _at(lengths, (B,), i32, dev, w, "lengths"), _at(nodes, (B, L), i32, dev, w, "nodes"), _stream_of(stream, dev)))
