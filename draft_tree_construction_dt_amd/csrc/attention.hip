@@ -474,19 +474,22 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
         const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
         top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * a.scale_log2;
         // The sums are kept relative to an m that may lag the maximum by
-        // kLazy: weights stay below 2^8, exact in relative terms for both
-        // types, and most tiles leave o alone.
+        // kLazy: weights stay within 2^8 and most tiles leave o alone.
+        // Their rounding to the cache's type is what its matrix instruction
+        // takes; l sums them before it.
         if (__any(top > m + kLazy)) rescale(top);
         const float base = m == -INFINITY ? 0.0f : m;
         s16x8 p[NB * 2];
+        float sum = 0;                                     // of the tile: next to a large l its weights are not lost one by one
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
                 const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][x], a.scale_log2, -base));
-                l += e;
+                sum += e;
                 p[2 * n + (x >> 3)][x & 7] = (short)T::put(e);
             }
+        l += sum;
         bool odd = false;
         if constexpr (masked) {
             // An unseen key's weight is 0, but 0 times an infinity or NaN is

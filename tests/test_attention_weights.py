@@ -1,0 +1,70 @@
+"""dt_tree_attention's weights at the ends of the types' ranges, against the
+definition in 64 bits (pass_ref.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import pass_ref as ref
+import test_verification_pass as tvp
+
+bd = tvp.bd
+BF16 = torch.bfloat16
+
+
+def sink_problem(keys, rows, heads, B, D, dtype, sink, low, high, seed):
+    """One key with score 0 among `keys` whose scores (natural) lie between
+    low and high for every query, the same for every request and head; values 1
+    for all in the even elements, and -1 for the sink, 1 for the rest in the
+    odd ones."""
+    gen = torch.Generator().manual_seed(seed)
+    score = low + (high - low) * torch.rand(keys, generator=gen)
+    score[sink] = 0
+    k = torch.zeros(keys, D)
+    k[:, 0] = score * D ** 0.5 / 8
+    v = torch.ones(keys, D)
+    v[sink, 1::2] = -1
+    q = torch.zeros(B, rows, heads, D)
+    q[..., 0] = 8
+    return q.to(dtype), k.to(dtype), v.to(dtype)
+
+
+def shared_cache(k, v, P, heads, B, device, seed):
+    """A cache whose requests share the pages (in random order) and whose heads
+    share the elements: it is only read."""
+    keys, D = k.shape
+    pages = keys // P
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(seed))
+    pools = []
+    for t in (k, v):
+        back = torch.empty(pages, P, 1, D, dtype=t.dtype)
+        back[order] = t.view(pages, P, 1, D)
+        pools.append(back.to(device).expand(pages, P, heads, D))
+    return bd.KVCache(pools[0], pools[1], order.to(torch.int32)[None].repeat(B, 1).to(device))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("rows,D", [(1, 64), (1, 128), (1, 256), (40, 128), (70, 64), (70, 128), (70, 256)])
+@pytest.mark.parametrize("low,high", [(-17.36, -17.36), (-21.0, -12.0)])
+def test_many_small_weights_beside_a_large_one(device, dtype, rows, D, low, high):
+    """The weights that a key with a far larger one leaves to the others are
+    small each, but not together: 262144 of e^-17.36 make 0.75% of the sum.
+    64 requests of 8 heads are so many that none is cut into chunks, each with
+    a maximum of its own."""
+    keys, B, heads = 262144, 64, 8
+    print("[case] sink", dtype, rows, D, low, high, flush=True)
+    for seed, sink in enumerate((0, keys // 2 + 11)):
+        q, k, v = sink_problem(keys, rows, heads, B, D, dtype, sink, low, high, seed)
+        kv = shared_cache(k, v, 64, heads, B, device, seed)
+        got, lse = tvp.run_attention(device, [keys - rows] * B, rows, 0, None, None, q, kv, 0)
+        K, V = k[:, :1].double().numpy(), v[:, :2].double().numpy()      # the others' products are zeros, and repeat
+        for r in sorted({0, rows - 1}):
+            n = keys - rows + r + 1
+            want, wl, spread, slack, vmax = ref.attend_row(q[0, r, 0, :1].double().numpy(), K[:n], V[:n], D ** -0.5)
+            # sums go by blocks of 16 keys and more
+            steps = keys // 16
+            tol = ref.attend_tolerance(want, spread, slack, vmax, steps, dtype)
+            err = np.abs(got[:, r].reshape(-1, 2) - want)
+            assert np.all(err <= tol), (sink, r, err.max(0), tol)
+            assert np.all(np.abs(lse[:, r] - wl) <= slack + ref.U32 * (4 * abs(wl) + steps + 16))
