@@ -59,6 +59,16 @@ constexpr int kMaxSearch = 512;    // requests up to which the chunk's size is s
 constexpr int kRowsPerWave = 32;
 constexpr float kLazy = 8.0f;      // log2 of the largest weight before the sums are rescaled
 
+// Weights are 2^kLift times e^(score - m).  f16 has no weights below 2^-24 and
+// full ones from 2^-14 only: with the lift they reach 2^15, just inside the
+// type, and a key at 2^-21 of the largest is still as exact as any, one at
+// 2^-31 still there (131072 keys at 2^-25 each beside one of weight 1 lost 0.3%
+// of the result without).  bf16's exponents need none.
+template <class T>
+constexpr float kLift = 0.0f;
+template <>
+constexpr float kLift<F16> = 7.0f;
+
 __device__ inline f32x16 mfma(Bf16, s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
 }
@@ -474,11 +484,11 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
         const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
         top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * a.scale_log2;
         // The sums are kept relative to an m that may lag the maximum by
-        // kLazy: weights stay within 2^8 and most tiles leave o alone.
+        // kLazy: weights stay within 2^(8 + kLift) and most tiles leave o alone.
         // Their rounding to the cache's type is what its matrix instruction
         // takes; l sums them before it.
         if (__any(top > m + kLazy)) rescale(top);
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = m == -INFINITY ? 0.0f : m - kLift<T>;
         s16x8 p[NB * 2];
         float sum = 0;                                     // of the tile: next to a large l its weights are not lost one by one
 #pragma unroll
@@ -609,6 +619,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     for (; i < fast && (valid & kFull) == kFull; ++i) round(i, False());
     for (; i < rounds; ++i) round(i, True());
     l += __shfl_xor(l, 32);
+    m -= kLift<T>;                                         // of the sums as they are
 
     if constexpr (WK > 1) {
         // the key groups' results meet in LDS; group 0 goes on with the sum
