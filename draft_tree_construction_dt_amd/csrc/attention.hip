@@ -57,17 +57,22 @@ constexpr float kOneRound = 16;    // units a slot up to which the work is cut i
 constexpr float kSplitCost = 4;    // a partial result's way through memory, in units
 constexpr int kMaxSearch = 512;    // requests up to which the chunk's size is searched for
 constexpr int kRowsPerWave = 32;
-constexpr float kLazy = 8.0f;      // log2 of the largest weight before the sums are rescaled
+constexpr float kLazy = 8.0f;      // log2 of how far the maximum may run ahead of the sums
 
-// Weights are 2^kLift times e^(score - m).  f16 has no weights below 2^-24 and
-// full ones from 2^-14 only: with the lift they reach 2^15, just inside the
-// type, and a key at 2^-21 of the largest is still as exact as any, one at
-// 2^-31 still there (131072 keys at 2^-25 each beside one of weight 1 lost 0.3%
-// of the result without).  bf16's exponents need none.
-template <class T>
-constexpr float kLift = 0.0f;
-template <>
-constexpr float kLift<F16> = 7.0f;
+// f16 has no weights below 2^-24 and full ones from 2^-14 only, so its weights
+// are 2^kLift times e^(score - maximum): they reach 2^15, just inside the type,
+// and a key at 2^-21 of the largest is still as exact as any, one at 2^-31
+// still there (262144 keys at 2^-25 beside one of weight 1 lost 1.1% of the
+// result without).  bf16's exponents need none.  Scores from kFar on are
+// themselves off by so much that weights could pass the type: those are not
+// lifted, and the sums follow every larger score.
+constexpr float kLift = 7.0f;
+constexpr float kFar = 1048576.0f;
+__device__ inline float lift(Bf16, float) { return 0.0f; }
+__device__ inline float lift(F16, float top) { return fabsf(top) < kFar ? kLift : 0.0f; }
+// log2 of the largest weight before the sums are rescaled
+__device__ inline float room(Bf16, float) { return kLazy; }
+__device__ inline float room(F16, float m) { return fabsf(m) < kFar ? kLazy + kLift : 0.0f; }
 
 __device__ inline f32x16 mfma(Bf16, s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
@@ -412,11 +417,11 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     f32x16 o[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d] = f32x16{};
-    float m = -INFINITY, l = 0;                            // m in units of log2; l of this lane's keys
+    float m = -INFINITY, l = 0;                            // o and l are sums of 2^(score - m), scores in units of log2; l of this lane's keys
 
     constexpr u64 kFull = KT == 64 ? ~0ull : 0xFFFFFFFFull;
     const auto rescale = [&](float top) __attribute__((always_inline)) {
-        const float mm = fmaxf(m, top);
+        const float mm = fmaxf(m, top - lift(T(), top));
         const float w = mm == -INFINITY ? 1.0f : exp2f(m - mm);
         m = mm;
         l *= w;
@@ -483,12 +488,11 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
             for (int x = 0; x < 16; ++x) top = fmaxf(top, s[n][x]);
         const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
         top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * a.scale_log2;
-        // The sums are kept relative to an m that may lag the maximum by
-        // kLazy: weights stay within 2^(8 + kLift) and most tiles leave o alone.
-        // Their rounding to the cache's type is what its matrix instruction
-        // takes; l sums them before it.
-        if (__any(top > m + kLazy)) rescale(top);
-        const float base = m == -INFINITY ? 0.0f : m - kLift<T>;
+        // m may lag the maximum: most tiles leave o alone.  The weights'
+        // rounding to the cache's type is what its matrix instruction takes; l
+        // sums them before it.
+        if (__any(top > m + room(T(), m))) rescale(top);
+        const float base = m == -INFINITY ? 0.0f : m;
         s16x8 p[NB * 2];
         float sum = 0;                                     // of the tile: next to a large l its weights are not lost one by one
 #pragma unroll
@@ -619,7 +623,6 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     for (; i < fast && (valid & kFull) == kFull; ++i) round(i, False());
     for (; i < rounds; ++i) round(i, True());
     l += __shfl_xor(l, 32);
-    m -= kLift<T>;                                         // of the sums as they are
 
     if constexpr (WK > 1) {
         // the key groups' results meet in LDS; group 0 goes on with the sum

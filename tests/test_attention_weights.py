@@ -71,3 +71,31 @@ def test_many_small_weights_beside_a_large_one(device, dtype, rows, D, low, high
             err = np.abs(got[:, r].reshape(-1, 2) - want)
             assert np.all(err <= tol), (sink, r, err.max(0), tol)
             assert np.all(np.abs(lse[:, r] - wl) <= slack + ref.U32 * (4 * abs(wl) + steps + 16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("rows,D", [(1, 64), (1, 128), (1, 256), (40, 128), (70, 64), (70, 128), (70, 256)])
+def test_scores_far_from_zero_stay_finite(device, dtype, rows, D):
+    """Scores of up to 2^27 that grow by a few units from tile to tile: their
+    last bits are whole units, so the weights can only be told to be weights,
+    and the result a mean of the values."""
+    keys, heads, B, P = 3000, 1, 1, 16
+    print("[case] far scores", dtype, rows, D, flush=True)
+    gen = torch.Generator().manual_seed(rows + D)
+    for far in (19, 22, 24, 25, 26, 27):
+        for step in (0.02, 0.09, 0.3):
+            k = torch.zeros(keys + rows, D)
+            k[:, 0] = 2.0 ** (far - 13)
+            k[:, 1] = step * torch.arange(keys + rows) * (1 + 0.3 * torch.rand(keys + rows, generator=gen))
+            v = 1 + torch.rand(keys + rows, D, generator=gen)
+            q = torch.zeros(B, rows, heads, D)
+            q[..., 0], q[..., 1] = 2.0 ** 13, 1
+            pad = -(keys + rows) % P
+            k, v = (torch.nn.functional.pad(t, (0, 0, 0, pad)).to(dtype) for t in (k, v))
+            kv = shared_cache(k, v, P, heads, B, device, far)
+            got, lse = tvp.run_attention(device, [keys], rows, 0, None, None, q.to(dtype), kv, 0, scale=1.0)
+            # the weights' rounding beside their unrounded sum, twice, and the result's own
+            slack = 4 * ref.HALF_STEP[dtype]
+            assert np.all(np.isfinite(lse)), (far, step)
+            assert np.all((got >= 1 - 2 * slack) & (got <= 2 + 2 * slack)), (far, step, got.min(), got.max())
