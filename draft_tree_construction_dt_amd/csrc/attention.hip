@@ -525,13 +525,18 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
         } else if constexpr (masked) {
             // The finite values are summed as always; whether a query sees
             // an infinity (NaN: of both signs) is counted by two more
-            // products of truth values.
+            // products, a seen key as 1, or, where its weight is 0, as 256
+            // (more than a tile has keys): 0 times an infinity is NaN, as it
+            // is in the tiles seen in full.
+            static_assert(KT < 256, "a count of ones stays below 256");
             s16x8 seen[NB * 2];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    seen[2 * n + (x >> 3)][x & 7] = (see[n] >> (8 * (x >> 2) + (x & 3)) & 1) ? (short)T::kOne : (short)0;
+                for (int x = 0; x < 16; ++x) {
+                    const short one = p[2 * n + (x >> 3)][x & 7] == 0 ? (short)T::k256 : (short)T::kOne;
+                    seen[2 * n + (x >> 3)][x & 7] = (see[n] >> (8 * (x >> 2) + (x & 3)) & 1) ? one : (short)0;
+                }
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 f32x16 up = {}, down = {};
@@ -554,8 +559,8 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
                 }
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                    if (up[x] > 0) o[d][x] += INFINITY;
-                    if (down[x] > 0) o[d][x] -= INFINITY;
+                    if (up[x] > 0) o[d][x] += up[x] < 256 ? INFINITY : NAN;
+                    if (down[x] > 0) o[d][x] -= down[x] < 256 ? INFINITY : NAN;
                 }
             }
         }

@@ -128,7 +128,7 @@ __device__ inline int64_t slot_offset(const CacheArgs& kv, int b, int64_t slot) 
 
 // The two 16-bit types of heads.
 struct Bf16 {
-    static constexpr uint32_t kExponent = 0x7F80, kFraction = 0x007F, kOne = 0x3F80;
+    static constexpr uint32_t kExponent = 0x7F80, kFraction = 0x007F, kOne = 0x3F80, k256 = 0x4380;
     static __device__ inline float get(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
     static __device__ inline uint16_t put(float x) {
         const __bf16 h = (__bf16)x;                  // to nearest, ties to even
@@ -136,7 +136,7 @@ struct Bf16 {
     }
 };
 struct F16 {
-    static constexpr uint32_t kExponent = 0x7C00, kFraction = 0x03FF, kOne = 0x3C00;
+    static constexpr uint32_t kExponent = 0x7C00, kFraction = 0x03FF, kOne = 0x3C00, k256 = 0x5C00;
     static __device__ inline float get(uint16_t x) { return (float)__builtin_bit_cast(_Float16, x); }
     static __device__ inline uint16_t put(float x) {
         const _Float16 h = (_Float16)x;

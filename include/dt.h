@@ -431,7 +431,9 @@ typedef struct dt_attention_params {
  * Scores, the softmax and the sums are fp32; the weights are rounded to the
  * cache's type for the second product, the result once.  A row that sees
  * nothing gives zeros (lse -inf).  Whatever lies in slots that a row does not
- * see, infinities and NaN included, does not reach it.  Finite scores beyond
+ * see, infinities and NaN included, does not reach it; an infinity in v that it
+ * sees reaches it times its weight, that is as NaN where the weight has become 0
+ * in the cache's type (less than about 2^-31 of the largest in f16).  Finite scores beyond
  * 2^27 in magnitude, whose last bits are many units, give unspecified (but
  * memory-safe) results.
  * q may not overlap out.  Pointers 16-byte aligned (lse 4), strides multiples

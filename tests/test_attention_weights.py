@@ -99,3 +99,36 @@ def test_scores_far_from_zero_stay_finite(device, dtype, rows, D):
             slack = 4 * ref.HALF_STEP[dtype]
             assert np.all(np.isfinite(lse)), (far, step)
             assert np.all((got >= 1 - 2 * slack) & (got <= 2 + 2 * slack)), (far, step, got.min(), got.max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("rows,D", [(1, 64), (1, 128), (1, 256), (40, 128), (70, 64), (70, 128), (70, 256)])
+def test_seen_infinities_reach_a_row_times_their_weight(device, dtype, rows, D):
+    """An infinity in v is the same in a tile that every query sees in full and
+    in one that has unseen keys: infinite, and NaN where the weight is 0."""
+    print("[case] seen infinities", dtype, rows, D, flush=True)
+    keys, P, lead = 250, 16, 1
+    seen = np.tril(np.ones((1, rows - 1, rows - 1), bool)) if rows > 1 else None
+    # scores of the infinity's key, all others 0: e^-20 is 2^-29, still a weight in f16 (lifted to 2^-22),
+    # e^-28 = 2^-40 is not, e^-120 = 2^-173 in neither type
+    for score, weight in ((-5.0, True), (-20.0, True), (-28.0, dtype == BF16), (-120.0, False)):
+        for at in (100, keys):                                    # in a whole tile; the chunk's first row
+            k = torch.zeros(keys + rows, D)
+            k[at, 0] = score * D ** 0.5 / 8
+            v = torch.ones(keys + rows, D)
+            v[at, 3], v[at, 4] = np.inf, -np.inf
+            q = torch.zeros(1, rows, 1, D)
+            q[..., 0] = 8
+            pad = -(keys + rows) % P
+            k, v = (torch.nn.functional.pad(t, (0, 0, 0, pad)).to(dtype) for t in (k, v))
+            kv = shared_cache(k, v, P, 1, 1, device, 5)
+            got, lse = tvp.run_attention(device, [keys], lead, rows - 1, None, seen, q.to(dtype), kv, 0)
+            assert np.all(np.isfinite(lse)), (score, at)
+            want = (np.inf, -np.inf) if weight else (np.nan, np.nan)
+            for x, w in zip((3, 4), want):
+                col = got[0, :, 0, x]
+                assert np.all(np.isnan(col)) if np.isnan(w) else np.all(col == w), (score, at, x, col)
+            rest = [x for x in range(D) if x not in (3, 4)]
+            # ones all: the weights' rounding beside their unrounded sum
+            assert np.all(np.abs(got[0, :, 0][:, rest] - 1) <= 4 * ref.HALF_STEP[dtype]), (score, at)
