@@ -214,11 +214,11 @@ __global__ void __launch_bounds__(256) logits_kernel(LogitsArgs a) {
         __syncthreads();
     }
     const float rep = a.repetition ? a.repetition[b] : 1.0f, freq = a.frequency ? a.frequency[b] : 0.0f,
-                pres = a.presence ? a.presence[b] : 0.0f, inv = 1.0f / rep;
+                pres = a.presence ? a.presence[b] : 0.0f;
     // the penalties of token t; false where there are none
     const auto penalise = [&](int t, float& x) {
         const uint32_t c = s_cnt[place(t)], n = c & ~kPrompt;
-        const float y = c ? x * (x > 0 ? inv : rep) : x;
+        const float y = c ? (x > 0 ? x / rep : x * rep) : x;
         x = n ? y - __builtin_fmaf(freq, (float)n, pres) : y;
         return c != 0;
     };
