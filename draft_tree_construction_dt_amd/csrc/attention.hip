@@ -56,6 +56,7 @@ constexpr int kMinUnits = 4;       // a chunk has at least 256 keys
 constexpr float kOneRound = 16;    // units a slot up to which the work is cut into one round
 constexpr float kSplitCost = 4;    // a partial result's way through memory, in units
 constexpr int kMaxSearch = 512;    // requests up to which the chunk's size is searched for
+constexpr float kMaxUnits = (float)(kMaxSlots / kUnit);    // no segment has more: sizes stay far from int's end
 constexpr int kRowsPerWave = 32;
 constexpr float kLazy = 8.0f;      // log2 of how far the maximum may run ahead of the sums
 
@@ -128,11 +129,11 @@ __device__ inline int chunk_units(const AttentionArgs& a, const Request& q0, int
     if (each < kOneRound || a.c.B > kMaxSearch) {
         // rounding adds at most one chunk a segment
         const int room = 2 * segs < slots ? slots - segs : slots;
-        const int c = (int)((float)work / (float)room) + 1;
+        const int c = (int)fminf((float)work / (float)room, kMaxUnits) + 1;
         return c < kMinUnits ? kMinUnits : c;
     }
     // sizes each * (1 .. 1.94) / (1 .. 4); the longest segment whole is one, too
-    const float want = each * (1.0f + 0.0625f * (lane & 15)) / (float)(1 + (lane >> 4));
+    const float want = fminf(each * (1.0f + 0.0625f * (lane & 15)) / (float)(1 + (lane >> 4)), kMaxUnits);
     int c = lane == 0 ? longest : (int)want + 1;
     c = c < kMinUnits ? kMinUnits : c;
     const float inv = 1.0f / (float)c;

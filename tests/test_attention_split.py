@@ -14,6 +14,7 @@ bd = pytest.importorskip("draft_tree_construction_dt_amd.binding")
 
 BF16, F16 = torch.bfloat16, torch.float16
 UNIT, CUS, PLAN_BYTES = 64, 256, 256
+MOST = 2 ** 30 // UNIT                                           # units of the longest segment there can be
 f32 = np.float32
 
 
@@ -35,11 +36,11 @@ def plan(ctx, live, rows, G, Hkv, D, cap):
     searched = not (each < 16 or len(ctx) > 512)
     if not searched:
         room = slots - segs if 2 * segs < slots else slots
-        c = max(4, int(f32(work) / f32(room)) + 1)
+        c = max(4, int(min(f32(work) / f32(room), f32(MOST))) + 1)
     else:
         best = None
         for lane in range(64):
-            want = each * f32(1 + 0.0625 * (lane & 15)) / f32(1 + (lane >> 4))
+            want = min(each * f32(1 + 0.0625 * (lane & 15)) / f32(1 + (lane >> 4)), f32(MOST))
             size = max(4, longest if lane == 0 else int(want) + 1)
             inv = f32(1) / f32(size)
             jobs = sum(m * Hkv * int(f32(u + size - 1) * inv) for _, m, u in requests)
@@ -82,6 +83,18 @@ def test_partial_results_fit_the_workspace(seed):
         assert chunks <= segments + 4 * slots
         assert partials <= workspace_partials(B, 1, rows - 1, G, Hkv, D), (ctx[:4], rows, G, Hkv, D, c)
     assert searches > 10
+
+
+@pytest.mark.parametrize("B,rows,G,Hkv,keys", [(1, 65536, 2048, 1, 2 ** 30), (255, 65536, 1, 64, 2 ** 30 - 1),
+                                               (4096, 4096, 127, 1, 2 ** 30), (2048, 8192, 4, 16, 2 ** 29)])
+def test_chunks_of_the_most_work_there_can_be(B, rows, G, Hkv, keys):
+    """The largest calls that dt.h admits: a share of a slot passes 2^31 units,
+    a chunk's size does not, and nothing is cut below the workspace."""
+    assert B * rows <= 2 ** 24 and B * rows * G * Hkv < 2 ** 31
+    c, _, _, chunks, partials, slots, mt = plan([keys - rows] * B, [rows] * B, rows, G, Hkv, 128, 2 ** 30)
+    assert 4 <= c <= MOST + 1
+    assert chunks <= B * Hkv * -(-rows * G // mt) + 4 * slots
+    assert partials <= workspace_partials(B, 0, rows, G, Hkv, 128)
 
 
 CASES = {
