@@ -623,6 +623,13 @@ private:
 static bool misaligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
 static bool bad_stride(int64_t s) { return s < 0 || (s & 7) != 0; }
 
+// Two layers, pages, slots or heads at less than a head's distance share
+// elements: fine to read, but a call that writes them would race with itself.
+static bool shares_elements(const dt_kv_cache* kv) {
+    return (kv->layers > 1 && kv->layer_stride < kv->D) || (kv->num_pages > 1 && kv->page_stride < kv->D) ||
+           (kv->page_size > 1 && kv->slot_stride < kv->D) || (kv->Hkv > 1 && kv->head_stride < kv->D);
+}
+
 // A cache's shape; its pointers too where `pointers` is set.
 static dt_status check_cache(const dt_kv_cache* kv, bool pointers) {
     if (!kv) return DT_ERR_INVALID_ARG;
@@ -740,6 +747,7 @@ extern "C" dt_status dt_kv_append(const dt_kv_cache* kv, const dt_chunk* chunk, 
     if (!p) return DT_ERR_INVALID_ARG;
     dt_status st = check_cache(kv, !chunk || chunk->B != 0);
     if (st != DT_OK) return st;
+    if (shares_elements(kv)) return DT_ERR_INVALID_ARG;
     if ((st = check_chunk(chunk, true)) != DT_OK) return st;
     if (p->layer < 0 || p->layer >= kv->layers || !isfinite(p->eps) || p->eps < 0 || !isfinite(p->rot_scale))
         return DT_ERR_INVALID_ARG;
@@ -877,6 +885,7 @@ extern "C" dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk
     if (!p) return DT_ERR_INVALID_ARG;
     dt_status st;
     if (kv && (st = check_cache(kv, !chunk || chunk->B != 0)) != DT_OK) return st;
+    if (kv && shares_elements(kv)) return DT_ERR_INVALID_ARG;
     if ((st = check_chunk(chunk, true)) != DT_OK) return st;
     if (chunk->lead < 1 || p->L < 1) return DT_ERR_INVALID_ARG;
     if (chunk->n_max > kMaxCommitNodes) return DT_ERR_UNSUPPORTED;

@@ -317,7 +317,8 @@ dt_status dt_verify_length(const dt_tree_out* tree, int32_t B, int32_t budget, d
  *     + h * head_stride + d,      page = page_table[b * max_pages + s / page_size]
  * and likewise for v.  Strides count elements and are multiples of 8 and not
  * negative (the stride of an axis of length one is not read); k and v are
- * 16-byte aligned.  Tokens whose page lies outside [0, num_pages), or whose
+ * 16-byte aligned.  Calls that write (dt_kv_append, dt_commit_path) need every
+ * element at a place of its own, and refuse strides below D.  Tokens whose page lies outside [0, num_pages), or whose
  * slot lies behind the table (max_pages * page_size), are dropped on writing
  * and unseen on reading.  Two tokens written in one call must not share a
  * slot; pages that are only read may be shared by requests. */

@@ -1,6 +1,8 @@
 """What the Python entry points of the verification pass refuse before anything
 is launched (no GPU needed)."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -52,3 +54,27 @@ def test_host_tensors_are_refused(monkeypatch, name):
     assert not reached
     monkeypatch.setattr(bd, "_load", lambda: real)
     _calls(0)[name]()                                             # an empty batch launches nothing and is fine
+
+
+@pytest.mark.parametrize("axis", ["layer_stride", "page_stride", "slot_stride", "head_stride"])
+@pytest.mark.parametrize("stride", [0, 8, 120])
+def test_caches_that_share_elements_are_read_only(axis, stride):
+    """Heads, slots, pages or layers that overlap cannot be written: two
+    workgroups would move the same element.  A batch of no requests launches
+    nothing, so that the read is seen to be accepted."""
+    fake, lib = 0x100000, bd._load()
+    kv = bd._KVCache(k=fake, v=fake, page_table=fake, layer_stride=1 << 20, page_stride=16384, slot_stride=1024,
+                     head_stride=128, layers=2, num_pages=9, page_size=16, max_pages=8, Hkv=8, D=128,
+                     dtype=bd.DT_DTYPE_BF16)
+    chunk = bd._Chunk(B=0, lead=1, n_max=8)
+    append = bd._AppendParams(k=fake, v=fake, k_stride=1024, v_stride=1024, eps=1e-6, rot_scale=1.0)
+    attend = bd._AttentionParams(q=fake, out=2 * fake, q_stride=4096, out_stride=4096, Hq=32, scale=0.1,
+                                 workspace=fake, workspace_bytes=1 << 40)
+    commit = bd._CommitParams(tokens=fake, parents=fake, target=fake, L=9, accepted=fake, lengths=fake)
+    of = lambda p: (ctypes.byref(kv), ctypes.byref(chunk), ctypes.byref(p))      # noqa: E731
+    assert lib.dt_kv_append(*of(append)) == lib.dt_commit_path(*of(commit)) == bd.DT_OK
+    setattr(kv, axis, stride)
+    assert lib.dt_kv_append(*of(append)) == lib.dt_commit_path(*of(commit)) == bd.DT_ERR_INVALID_ARG
+    assert lib.dt_tree_attention(*of(attend)) == bd.DT_OK
+    kv.layers = kv.num_pages = kv.page_size = kv.Hkv = 1           # strides of axes of length one are not read
+    assert lib.dt_kv_append(*of(append)) == lib.dt_commit_path(*of(commit)) == bd.DT_OK
