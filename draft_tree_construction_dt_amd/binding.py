@@ -369,9 +369,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_of(stream, index: int) -> int:
-    """Raw handle of `stream`, or of the device's current one."""
+    """Raw handle of `stream`, which must be the device's, or of its current one."""
+    if isinstance(stream, int):
+        return stream
     if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
+        _need(index < 0 or stream.device_index == index, "stream", "must belong to the tensors' device")
+        return stream.cuda_stream
     if index < 0:
         return 0
     return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream

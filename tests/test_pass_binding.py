@@ -2,6 +2,7 @@
 is launched (no GPU needed)."""
 
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -78,3 +79,13 @@ def test_caches_that_share_elements_are_read_only(axis, stride):
     assert lib.dt_tree_attention(*of(attend)) == bd.DT_OK
     kv.layers = kv.num_pages = kv.page_size = kv.Hkv = 1           # strides of axes of length one are not read
     assert lib.dt_kv_append(*of(append)) == lib.dt_commit_path(*of(commit)) == bd.DT_OK
+
+
+def test_streams_of_another_device_are_refused():
+    """The library launches on its stream's device, which another device's
+    tensors need not be mapped on."""
+    stream = SimpleNamespace(cuda_stream=0x1230, device_index=1)
+    assert bd._stream_of(stream, 1) == 0x1230 and bd._stream_of(0x77, 0) == 0x77
+    with pytest.raises(bd.DtError) as e:
+        bd._stream_of(stream, 0)
+    assert e.value.status == bd.DT_ERR_INVALID_ARG
