@@ -175,3 +175,56 @@ def test_searched_splits(device, name):
                 err = np.abs(got[b, r, h] - want)
                 assert np.all(err <= tol), (b, r, h, float((err - tol).max()))
                 assert abs(lse[b, r, h] - wl) <= slack + ref.U32 * (4 * abs(wl) + steps + 16), (b, r, h)
+
+
+@pytest.mark.gpu
+def test_captured_calls_follow_their_lengths(device):
+    """A captured call is replayed for lengths that were written after its
+    capture, shorter and far longer ones: the split follows the device's values."""
+    print("[case] captured lengths", flush=True)
+    B, Hkv, G, D, P, lead, n_max = 5, 2, 4, 128, 16, 1, 30
+    rs = np.random.RandomState(8)
+    gen = torch.Generator(device=device).manual_seed(8)
+    pages = 500
+    k, v = (torch.empty(pages, P, Hkv, D, dtype=BF16, device=device).normal_(generator=gen) for _ in range(2))
+    table = torch.from_numpy(rs.randint(0, pages, (B, 1300)).astype(np.int32)).to(device)
+    i32 = dict(dtype=torch.int32, device=device)
+    kv = bd.KVCache(k, v, table)
+    seen = torch.from_numpy(ref.pack_bits(ref.random_tree(rs, B, n_max, [n_max] * B)[2])).to(device)
+    chunk = bd.Chunk(torch.full((B,), 7, **i32), lead, n_max, torch.full((B,), 3, **i32), mask=seen)
+    q = torch.empty(B, lead + n_max, Hkv * G, D, dtype=BF16, device=device).normal_(generator=gen)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device=device)
+    ws = torch.empty(bd.dt_attention_workspace(kv, chunk, Hkv * G), dtype=torch.uint8, device=device)
+    call = lambda: bd.dt_tree_attention(kv, chunk, q, out, lse=lse, workspace=ws)      # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for ctx, nn in (([0, 1, 2, 3, 4], [0, 30, 5, 1, 2]), ([20000, 9000, 300, 64, 15000], [30, 29, 0, 12, 30]),
+                    ([7] * 5, [3] * 5), ([-1, 20000, -1, 2, 700], [30] * 5), ([12000] * 5, [17] * 5)):
+        chunk.ctx_len.copy_(torch.tensor(ctx, **i32))
+        chunk.n_nodes.copy_(torch.tensor(nn, **i32))
+        results = []
+        for run in (call, graph.replay, graph.replay):
+            out.fill_(7)
+            lse.fill_(7)
+            run()
+            torch.cuda.synchronize()
+            results.append((out.clone(), lse.clone()))
+        for o, s in results[1:]:
+            assert torch.equal(o.view(torch.int16), results[0][0].view(torch.int16)) and torch.equal(s, results[0][1])
+        for b in range(B):
+            live = 0 if ctx[b] < 0 else lead + nn[b]
+            assert bool((results[0][0][b, live:] == 7).all())
+            assert bool(torch.isfinite(results[0][1][b, :live]).all())
+            if live:                                              # the root row sees all slots up to its own
+                n = ctx[b] + 1
+                at = torch.arange(n, device=device)
+                K, V = (t[table[b].long()[at // P], at % P].double().cpu().numpy() for t in (k, v))
+                want, wl, spr, slack, vmax = ref.attend_row(q[b, 0, 0].double().cpu().numpy(), K[:, 0], V[:, 0],
+                                                            D ** -0.5)
+                steps = n // 16 + n // 256 + 64
+                tol = ref.attend_tolerance(want, spr, slack, vmax, steps, BF16)
+                assert np.all(np.abs(results[0][0][b, 0, 0].double().cpu().numpy() - want) <= tol)
+                assert abs(float(results[0][1][b, 0, 0]) - wl) <= slack + ref.U32 * (4 * abs(wl) + steps + 16)
