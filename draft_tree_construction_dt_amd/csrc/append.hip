@@ -21,8 +21,12 @@ namespace {
 
 constexpr int kMaxPairs = 128;     // rot_dim <= 256
 constexpr int kDeep = 4;           // groups of heads of a wave in flight
-constexpr int kWaves = 2048;       // waves that fill the chip: fewer rows are shared by waves (one token
-                                   // on one wave: 12.8 us)
+// Fewer rows than this are shared by waves, as many as make about this number.
+// Captured calls of 32 + 16 heads of 128, a wave a row / shared: one row 11.2 /
+// 5.3 us, 512 rows 14.1 / 8.0, 960 15.6 / 11.5, 1984 18.5 / 17.0.  Up to 8192
+// waves instead: 512 rows 11.5, 1984 18.9, 2112 19.3 (a wave a row 20.6), 4160
+// the same.
+constexpr int kWaves = 2048;
 
 template <class T, int D>
 __global__ void __launch_bounds__(256) append_kernel(AppendArgs a, int parts) {

@@ -33,8 +33,9 @@
 // Measured (bf16, heads of 128, 4 query heads to a key head, pages of 16): 64
 // requests' single tokens over 33-16383 keys, 2.15 GB of cache, in 404 us, 5.3
 // TB/s (a copy reads and writes 4.9); two chunks of 2048 over 6-14 K keys in
-// 732-775 us, 915-967 TFLOP/s (a large matrix product: 1402), matrix cores 46%
-// and vector units 47% busy; one token over 4096 keys in 17 us, all latency.
+// 718-775 us, 915-986 TFLOP/s (a large matrix product: 1402), matrix cores 47%
+// and vector units 48% busy; one token over 4096 keys in 17 us, all latency
+// (behind a page table of 1 M slots the same).
 #include <math.h>
 
 #include "pass.h"
@@ -55,7 +56,12 @@ constexpr int kUnit = 64;          // keys of the split's unit of work
 constexpr int kMinUnits = 4;       // a chunk has at least 256 keys
 constexpr float kOneRound = 16;    // units a slot up to which the work is cut into one round
 constexpr float kSplitCost = 4;    // a partial result's way through memory, in units
-constexpr int kMaxSearch = 512;    // requests up to which the chunk's size is searched for
+// Requests up to which the chunk's size is searched for.  Every workgroup reads
+// the batch's lengths and searches for itself, so both grow with the square of
+// the batch: one token over 4000 keys (pages of a small pool) for each of 64
+// requests 164 us, 256 753, 512 1947, 513 (no search) 1106, 1024 2450; over 100
+// keys 64 26, 256 333, 512 1148, 513 340, 4096 11 ms; 65535 of one key 1.4 s.
+constexpr int kMaxSearch = 512;
 constexpr float kMaxUnits = (float)(kMaxSlots / kUnit);    // no segment has more: sizes stay far from int's end
 constexpr int kRowsPerWave = 32;
 constexpr float kLazy = 8.0f;      // log2 of how far the maximum may run ahead of the sums
@@ -489,9 +495,10 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
             for (int x = 0; x < 16; ++x) top = fmaxf(top, s[n][x]);
         const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
         top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * a.scale_log2;
-        // m may lag the maximum: most tiles leave o alone.  The weights'
-        // rounding to the cache's type is what its matrix instruction takes; l
-        // sums them before it.
+        // m may lag the maximum: most tiles leave o alone.  The weights are
+        // rounded to the cache's type for its matrix instruction and summed
+        // unrounded (the results' error against 64 bits is 1.3 times what
+        // weights in fp32 would leave, most of it their own rounding).
         if (__any(top > m + room(T(), m))) rescale(top);
         const float base = m == -INFINITY ? 0.0f : m;
         s16x8 p[NB * 2];

@@ -15,8 +15,11 @@
 // The counts are kept as [t % 8][t / 8], so that a wave's reads of a vector's
 // j-th token are consecutive words whatever the row's alignment.  Measured: 64
 // requests x 8 rows of 151936 bf16 logits behind 2048-4096 tokens, half of the
-// rows masked, in 90 us (3.5 TB/s; a copy of the same bytes takes 65); the same
-// without history, biases and masks 68 us.
+// rows masked, in 92 us (3.5 TB/s; a copy of the same bytes takes 65); the same
+// without history, biases and masks 68 us; 64 trees of 64 nodes over the same
+// vocabulary 631 us (4.0 TB/s).  Every workgroup scans its request's whole
+// history: one row of 151936 logits behind 1000, 10000 and 100000 tokens takes
+// 9.7, 14 and 70 us, one row of each of 64 requests 13, 28 and 212.
 #include <math.h>
 
 #include "pass.h"
@@ -30,8 +33,8 @@ constexpr int kWords = kChunk / 32;        // of a bit a token
 constexpr int64_t kWorkgroups = 2048;
 // A lane goes through its vector's few entries one by one; a wave in which a
 // lane has more does all tokens of its vectors at once (16 requests' draft logits
-// behind 4096 tokens: chosen 33 us, all at once 38, one by one 37.5; with 64
-// requests memory is the bound and all three take 91).
+// behind 4096 tokens: chosen 34 us, all at once 39, one by one 39; with 64
+// requests memory is the bound and all three take 92).
 constexpr int kFew = 3;
 
 template <class T>
@@ -321,8 +324,8 @@ hipError_t run(const LogitsArgs& a, hipStream_t stream) {
     int64_t z = (kWorkgroups + chunks * a.B - 1) / (chunks * a.B);
     z = z < a.rows ? z : a.rows;
     // the chunks of low ids first: they hold most entries and take longest
-    // (the draft logits of 64 requests 98 -> 91 us; 32 trees behind 8000 tokens
-    // lose: 151 -> 158)
+    // (the draft logits of 64 requests 101 -> 92 us; 32 trees behind 8000 tokens
+    // lose: 154 -> 161)
     const dim3 grid((unsigned)a.B, (unsigned)chunks, (unsigned)z);
     const int biases = a.n_bias < kChunk ? a.n_bias : kChunk;
     const size_t words = kChunk + kWords + (a.n_bias > 0 ? 2 * kWords + biases : 0) +

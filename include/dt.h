@@ -437,6 +437,8 @@ typedef struct dt_attention_params {
  * in the cache's type (less than about 2^-31 of the largest in f16).  Finite scores beyond
  * 2^27 in magnitude, whose last bits are many units, give unspecified (but
  * memory-safe) results.
+ * The work is split by the lengths on the device, in time that grows with the
+ * square of B: meant for some hundred requests (65535 take over a second).
  * q may not overlap out.  Pointers 16-byte aligned (lse 4), strides multiples
  * of 8 and at least Hq * D.
  * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above, or
