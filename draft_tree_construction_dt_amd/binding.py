@@ -110,6 +110,31 @@ class _CommitParams(ctypes.Structure):
     _fields_ = _fields([("p", "tokens parents target"), ("i", "L"), ("p", "accepted lengths nodes stream")])
 
 
+class _LatentCache(ctypes.Structure):
+    _fields_ = _fields([("p", "c page_table"), ("l", "layer_stride page_stride slot_stride"),
+                        ("i", "layers num_pages page_size max_pages Dc Dr dtype")])
+
+
+class _LatentAppendParams(ctypes.Structure):
+    _fields_ = _fields([("p", "latent k_rot q_rot q_out"),
+                        ("l", "latent_stride k_stride q_stride q_head_stride q_out_stride q_out_head_stride"),
+                        ("i", "Hq"), ("p", "norm"), ("f", "eps"), ("p", "freqs"), ("i", "interleaved"),
+                        ("f", "rot_scale"), ("i", "layer"), ("p", "stream")])
+
+
+class _LatentParams(ctypes.Structure):
+    _fields_ = _fields([("p", "q out weight"), ("l", "q_stride out_stride"), ("i", "Hq Dn max_keys"), ("f", "scale"),
+                        ("p", "lse"), ("i", "layer"), ("p", "workspace"), ("z", "workspace_bytes"), ("p", "stream")])
+
+
+class _SampleParams(ctypes.Structure):
+    _fields_ = _fields([("p", "logits"), ("i", "B lead n_max V dtype"),
+                        ("p", "n_nodes u temperature top_k top_p min_p tokens logp workspace"),
+                        ("z", "workspace_bytes"), ("p", "stream")])
+
+
+_pack_latent_append, _pack_latent, _pack_sample = (
+    _packer(c) for c in (_LatentAppendParams, _LatentParams, _SampleParams))
 _pack_append, _pack_attention, _pack_logits, _pack_commit = (
     _packer(c) for c in (_AppendParams, _AttentionParams, _LogitsParams, _CommitParams))
 
@@ -122,7 +147,9 @@ class _TreeOut(ctypes.Structure):
 
 EXPORTED = ("dt_build_tree", "dt_build_tree_noalloc", "dt_workspace_size", "dt_status_string", "dt_position_topk",
             "dt_ngram_update", "dt_verify_length", "dt_rope_frequencies", "dt_kv_append", "dt_tree_attention",
-            "dt_attention_workspace", "dt_process_logits", "dt_commit_path")
+            "dt_attention_workspace", "dt_process_logits", "dt_commit_path", "dt_latent_append", "dt_latent_attention",
+            "dt_latent_workspace", "dt_latent_prefill", "dt_latent_prefill_workspace", "dt_latent_commit",
+            "dt_sample_rows", "dt_sample_workspace")
 DT_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _lib = None
@@ -161,11 +188,17 @@ def _load():
         lib.dt_rope_frequencies.restype = ctypes.c_int
         lib.dt_rope_frequencies.argtypes = [ctypes.c_int32, ctypes.c_int32] + [ctypes.c_double] * 5 + \
             [ctypes.c_void_p, ctypes.POINTER(ctypes.c_float)]
-        for fn in (lib.dt_kv_append, lib.dt_tree_attention, lib.dt_commit_path):
+        for fn in (lib.dt_kv_append, lib.dt_tree_attention, lib.dt_commit_path, lib.dt_latent_append,
+                   lib.dt_latent_attention, lib.dt_latent_prefill, lib.dt_latent_commit):
             fn.restype = ctypes.c_int
             fn.argtypes = [ctypes.c_void_p] * 3            # kv, chunk, params (a structure or its bytes)
         lib.dt_attention_workspace.restype = ctypes.c_size_t
         lib.dt_attention_workspace.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32]
+        lib.dt_latent_workspace.restype = lib.dt_latent_prefill_workspace.restype = ctypes.c_size_t
+        lib.dt_latent_workspace.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32]
+        lib.dt_latent_prefill_workspace.argtypes = [ctypes.c_void_p, ctypes.c_void_p] + [ctypes.c_int32] * 3
+        lib.dt_sample_rows.restype, lib.dt_sample_workspace.restype = ctypes.c_int, ctypes.c_size_t
+        lib.dt_sample_rows.argtypes = lib.dt_sample_workspace.argtypes = [ctypes.c_void_p]
         lib.dt_process_logits.restype = ctypes.c_int
         lib.dt_process_logits.argtypes = [ctypes.c_void_p]
         _lib = lib
@@ -464,15 +497,16 @@ class Chunk:
         return cls(ctx_len, lead, int(tree.tokens.shape[1]), tree.n_nodes, tree.mask, tree.depths)
 
 
-def _row_stride(t: Optional[torch.Tensor], shape, kv: KVCache, where: str, name: str) -> int:
-    """Row stride of a [B][rows][H][D] tensor whose rows' heads are contiguous."""
+def _row_stride(t: Optional[torch.Tensor], shape, kv, where: str, name: str, spaced: bool = False) -> int:
+    """Row stride of a [B][rows][H][D] tensor whose rows' heads are contiguous
+    (`spaced`: evenly spaced)."""
     if t is None:
         return 0
     if t.shape != shape or t.dtype is not kv.dtype or t.get_device() != kv.index:
         raise DtError(DT_ERR_INVALID_ARG, f"{where}: {name} must be {kv.dtype} [B][lead + n_max][heads][D] = "
                                           f"{tuple(shape)} on the cache's device, not {t.dtype} {tuple(t.shape)}")
     batch, row, head, one = t.stride()
-    if one != 1 or (head != kv.D and shape[2] != 1):
+    if one != 1 or (head != shape[3] and shape[2] != 1 and not spaced):
         raise DtError(DT_ERR_INVALID_ARG, f"{where}: the heads of a row of {name} must be contiguous")
     if shape[0] == 1:
         return row
@@ -483,7 +517,7 @@ def _row_stride(t: Optional[torch.Tensor], shape, kv: KVCache, where: str, name:
     return row
 
 
-def _pass_devices(kv: Optional[KVCache], chunk: Chunk, where: str) -> None:
+def _pass_devices(kv, chunk: Chunk, where: str) -> None:
     _need(kv is None or (chunk.index == kv.index and kv.page_table.shape[0] >= chunk.B), where,
           "the chunk and the cache must be on one device, with a row of page_table for every request")
 
@@ -604,15 +638,193 @@ def dt_commit_path(kv: Optional[KVCache], chunk: Chunk, tokens: Optional[torch.T
     dt_commit_path in dt.h).  tokens and parents int32 [B][n_max] as
     dt_build_tree wrote them; target int32 [B][lead + n_max]; accepted and
     nodes int32 [B][L], lengths int32 [B] are written."""
-    w, dev, i32 = "dt_commit_path", chunk.index, torch.int32
-    _pass_devices(kv, chunk, w)
+    _commit("dt_commit_path", kv, chunk, tokens, parents, target, accepted, lengths, nodes, stream)
+
+
+def _commit(w: str, cache, chunk: Chunk, tokens: Optional[torch.Tensor], parents: Optional[torch.Tensor],
+            target: torch.Tensor, accepted: torch.Tensor, lengths: torch.Tensor, nodes: Optional[torch.Tensor],
+            stream) -> None:
+    dev, i32 = chunk.index, torch.int32
+    _pass_devices(cache, chunk, w)
     _need(accepted.dim() == 2, w, "accepted must be int32 [B][L]")
     B, L = chunk.B, accepted.shape[1]
-    call = _reachable(dev, B, _load().dt_commit_path)
-    st = _on_device(dev, call, 0 if kv is None else kv._ref, chunk._ref, _pack_commit(
+    call = _reachable(dev, B, getattr(_load(), w))
+    st = _on_device(dev, call, 0 if cache is None else cache._ref, chunk._ref, _pack_commit(
         _at(tokens, (B, chunk.n_max), i32, dev, w, "tokens"), _at(parents, (B, chunk.n_max), i32, dev, w, "parents"),
         _at(target, (B, chunk.rows), i32, dev, w, "target"), L, _at(accepted, (B, L), i32, dev, w, "accepted"),
         _at(lengths, (B,), i32, dev, w, "lengths"), _at(nodes, (B, L), i32, dev, w, "nodes"), _stream_of(stream, dev)))
+    if st != DT_OK:
+        raise DtError(st, w)
+
+
+# ---------------------------------------------------------------------------
+# latent attention and drawn tokens (third part of dt.h)
+# ---------------------------------------------------------------------------
+
+class LatentCache:
+    """A paged cache of latents (dt_latent_cache): c of shape [pages][page_size]
+    [Dc + Dr], or [layers][pages][page_size][Dc + Dr] for one allocation of all
+    layers, bf16 or f16, with contiguous tokens, of whose elements the last Dr
+    are the rotated part; page_table int32 [B][max_pages].  Holds the tensors;
+    make another for other tensors."""
+
+    __slots__ = ("c", "page_table", "device", "index", "dtype", "Dc", "Dr", "layers", "_struct", "_ref")
+
+    def __init__(self, c: torch.Tensor, page_table: torch.Tensor, Dr: int):
+        w = "LatentCache"
+        _need(c.dim() in (3, 4), w, "c must be [pages][page_size][Dc + Dr] or [layers][pages][page_size][Dc + Dr]")
+        _need(c.dtype in _HEAD_TYPES, w, "c must be bfloat16 or float16")
+        _need(c.stride(-1) == 1, w, "tokens must be contiguous")
+        _need(0 < int(Dr) < c.shape[-1], w, "Dr must be 1 .. Dc + Dr - 1")
+        _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.is_contiguous(), w,
+              "page_table must be contiguous int32 [B][max_pages]")
+        _need(page_table.device == c.device, w, "c and page_table on one device")
+        self.c, self.page_table = c, page_table
+        self.device, self.dtype, self.Dr, self.Dc = c.device, c.dtype, int(Dr), int(c.shape[-1]) - int(Dr)
+        self.layers, self.index = int(c.shape[0]) if c.dim() == 4 else 1, c.get_device()
+        self._struct = _LatentCache(c.data_ptr(), page_table.data_ptr(), c.stride(0) if c.dim() == 4 else 0,
+                                    c.stride(-3), c.stride(-2), self.layers, c.shape[-3], c.shape[-2],
+                                    page_table.shape[1], self.Dc, self.Dr, _HEAD_TYPES[c.dtype])
+        self._ref = ctypes.addressof(self._struct)
+
+
+def dt_latent_append(cache: LatentCache, chunk: Chunk, latent: torch.Tensor, k_rot: torch.Tensor,
+                     q_rot: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                     norm: Optional[torch.Tensor] = None, eps: float = 1e-6, freqs: Optional[torch.Tensor] = None,
+                     interleaved: bool = False, rot_scale: float = 1.0, layer: int = 0, stream=None) -> None:
+    """Norm the chunk's latents, turn the keys' and the queries' rotated parts,
+    put latents and keys' parts into the cache (see dt_latent_append in dt.h).
+    latent [B][lead + n_max][Dc] and k_rot [B][lead + n_max][Dr], evenly spaced
+    rows; q_rot and q_out [B][lead + n_max][heads][Dr], evenly spaced heads
+    (slices of whole queries); norm [Dc]; freqs float64 [Dr / 2] on the device."""
+    w, index, dtype = "dt_latent_append", cache.index, cache.dtype
+    _pass_devices(cache, chunk, w)
+    B, rows, Dr, Hq, q_head, out_head = chunk.B, chunk.rows, cache.Dr, 0, 0, 0
+    _need(latent.dim() == 3 and k_rot.dim() == 3, w, "latent and k_rot must be [B][lead + n_max][elements]")
+    if q_rot is not None:
+        _need(q_rot.dim() == 4, w, "q_rot must be [B][lead + n_max][heads][Dr]")
+        Hq, q_head = int(q_rot.shape[2]), q_rot.stride(2)
+    if q_out is not None:
+        _need(q_out.dim() == 4, w, "q_out must be [B][lead + n_max][heads][Dr]")
+        out_head = q_out.stride(2)
+    heads = (B, rows, Hq, Dr)
+    call = _reachable(index, B, _load().dt_latent_append)
+    st = _on_device(index, call, cache._ref, chunk._ref, _pack_latent_append(
+        latent.data_ptr(), k_rot.data_ptr(), 0 if q_rot is None else q_rot.data_ptr(),
+        0 if q_out is None else q_out.data_ptr(),
+        _row_stride(latent.unsqueeze(2), (B, rows, 1, cache.Dc), cache, w, "latent"),
+        _row_stride(k_rot.unsqueeze(2), (B, rows, 1, Dr), cache, w, "k_rot"),
+        _row_stride(q_rot, heads, cache, w, "q_rot", True), q_head,
+        _row_stride(q_out, heads, cache, w, "q_out", True), out_head, Hq,
+        _at(norm, (cache.Dc,), dtype, index, w, "norm"), eps, _at(freqs, (Dr // 2,), torch.float64, index, w, "freqs"),
+        bool(interleaved), rot_scale, layer, _stream_of(stream, index)))
+    if st != DT_OK:
+        raise DtError(st, w)
+
+
+def dt_latent_workspace(cache: LatentCache, chunk: Chunk, Hq: int) -> int:
+    return int(_load().dt_latent_workspace(cache._ref, chunk._ref, int(Hq)))
+
+
+def _latent_attention(w: str, cache: LatentCache, chunk: Chunk, q: torch.Tensor, out: torch.Tensor, weight: int, Dn: int,
+                      max_keys: int, dq: int, dout: int, scale: float, lse: Optional[torch.Tensor], layer: int,
+                      workspace: Optional[torch.Tensor], stream) -> None:
+    index = cache.index
+    _pass_devices(cache, chunk, w)
+    _need(q.dim() == 4, w, "q must be [B][lead + n_max][heads][elements]")
+    B, rows, Hq = chunk.B, chunk.rows, int(q.shape[2])
+    _need(workspace is None or (workspace.get_device() == index and workspace.is_contiguous()), w,
+          "workspace must be contiguous, on the cache's device")
+    call = _reachable(index, B, getattr(_load(), w))
+    st = _on_device(index, call, cache._ref, chunk._ref, _pack_latent(
+        q.data_ptr(), out.data_ptr(), weight, _row_stride(q, (B, rows, Hq, dq), cache, w, "q"),
+        _row_stride(out, (B, rows, Hq, dout), cache, w, "out"), Hq, Dn, max_keys, scale,
+        _at(lse, (B, rows, Hq), torch.float32, index, w, "lse"), layer,
+        0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _stream_of(stream, index)))
+    if st != DT_OK:
+        raise DtError(st, w)
+
+
+def dt_latent_attention(cache: LatentCache, chunk: Chunk, q: torch.Tensor, out: torch.Tensor, scale: float,
+                        lse: Optional[torch.Tensor] = None, layer: int = 0, workspace: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Attention of the chunk's rows over the latents, absorbed form (see
+    dt_latent_attention in dt.h).  q [B][lead + n_max][Hq][Dc + Dr] and out
+    [B][lead + n_max][Hq][Dc]; scale is that of the heads before the
+    absorption; lse float32 [B][lead + n_max][Hq] or None; workspace of
+    dt_latent_workspace() bytes."""
+    _latent_attention("dt_latent_attention", cache, chunk, q, out, 0, 0, 0, cache.Dc + cache.Dr, cache.Dc, scale, lse,
+                      layer, workspace, stream)
+
+
+def dt_latent_prefill_workspace(cache: LatentCache, chunk: Chunk, Hq: int, Dn: int, max_keys: int) -> int:
+    return int(_load().dt_latent_prefill_workspace(cache._ref, chunk._ref, int(Hq), int(Dn), int(max_keys)))
+
+
+def dt_latent_prefill(cache: LatentCache, chunk: Chunk, q: torch.Tensor, weight: torch.Tensor, out: torch.Tensor,
+                      scale: float, max_keys: int, lse: Optional[torch.Tensor] = None, layer: int = 0,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention of the chunk's rows over each head's keys and values made from
+    the latents, expanded form (see dt_latent_prefill in dt.h).  q [B][lead +
+    n_max][Hq][Dn + Dr], weight [Hq][2 * Dn][Dc] (a head's key rows, then its
+    value rows) and out [B][lead + n_max][Hq][Dn]; max_keys at least the longest
+    request's slots; workspace of dt_latent_prefill_workspace() bytes."""
+    w = "dt_latent_prefill"
+    _need(q.dim() == 4 and out.dim() == 4, w, "q and out must be [B][lead + n_max][heads][elements]")
+    Dn = int(out.shape[3])
+    at = _at(weight, (int(q.shape[2]), 2 * Dn, cache.Dc), cache.dtype, cache.index, w, "weight")
+    _latent_attention(w, cache, chunk, q, out, at, Dn, int(max_keys), Dn + cache.Dr, Dn, scale, lse, layer, workspace,
+                      stream)
+
+
+def dt_latent_commit(cache: LatentCache, chunk: Chunk, tokens: Optional[torch.Tensor], parents: Optional[torch.Tensor],
+                     target: torch.Tensor, accepted: torch.Tensor, lengths: torch.Tensor,
+                     nodes: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dt_commit_path for a cache of latents."""
+    _commit("dt_latent_commit", cache, chunk, tokens, parents, target, accepted, lengths, nodes, stream)
+
+
+def _sample_shape(logits: torch.Tensor, lead: Optional[int], where: str):
+    _need(logits.dim() == 3 and logits.dtype in _LOGIT_TYPES, where, "logits must be float32 or bfloat16 [B][rows][V]")
+    B, rows, V = logits.shape
+    lead = rows if lead is None else int(lead)
+    _need(0 <= lead <= rows, where, "lead must be 0..rows")
+    return B, rows, V, lead
+
+
+def dt_sample_workspace(logits: torch.Tensor) -> int:
+    """Bytes of workspace that dt_sample_rows needs for these logits [B][rows][V]."""
+    B, rows, V, lead = _sample_shape(logits, None, "dt_sample_workspace")
+    return int(_load().dt_sample_workspace(_pack_sample(
+        0, B, lead, 0, V, _LOGIT_TYPES[logits.dtype], 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)))
+
+
+def dt_sample_rows(logits: torch.Tensor, u: torch.Tensor, tokens: torch.Tensor,
+                   temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+                   top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+                   logp: Optional[torch.Tensor] = None, lead: Optional[int] = None,
+                   n_nodes: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """A token for every row of logits [B][lead + n_max][V] (see dt_sample_rows
+    in dt.h).  lead defaults to every row (no tree).  u float32 [B][lead +
+    n_max] in [0, 1); temperature, top_p and min_p float32 [B], top_k int32 [B];
+    tokens int32 and logp float32 [B][lead + n_max] are written; workspace of
+    dt_sample_workspace() bytes (None where that is 0)."""
+    w, dev, i32, f32 = "dt_sample_rows", logits.get_device(), torch.int32, torch.float32
+    B, rows, V, lead = _sample_shape(logits, lead, w)
+    each, every = (B,), (B, rows)
+    _need(workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()), w,
+          "workspace must be contiguous, on the logits' device")
+    call = _reachable(dev, B, _load().dt_sample_rows)
+    st = _on_device(dev, call, _pack_sample(
+        _at(logits, logits.shape, logits.dtype, dev, w, "logits"), B, lead, rows - lead, V, _LOGIT_TYPES[logits.dtype],
+        _at(n_nodes, each, i32, dev, w, "n_nodes"), _at(u, every, f32, dev, w, "u"),
+        _at(temperature, each, f32, dev, w, "temperature"), _at(top_k, each, i32, dev, w, "top_k"),
+        _at(top_p, each, f32, dev, w, "top_p"), _at(min_p, each, f32, dev, w, "min_p"),
+        _at(tokens, every, i32, dev, w, "tokens"), _at(logp, every, f32, dev, w, "logp"),
+        0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _stream_of(stream, dev)))
     if st != DT_OK:
         raise DtError(st, w)
 

@@ -881,11 +881,10 @@ extern "C" dt_status dt_process_logits(const dt_logits_params* p) {
     return DT_OK;
 }
 
-extern "C" dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_commit_params* p) {
-    if (!p) return DT_ERR_INVALID_ARG;
+// What dt_commit_path and dt_latent_commit share: the checks behind those of the
+// cache, and the launch; `a` holds the cache.
+static dt_status commit(const dt_chunk* chunk, const dt_commit_params* p, CommitArgs a) {
     dt_status st;
-    if (kv && (st = check_cache(kv, !chunk || chunk->B != 0)) != DT_OK) return st;
-    if (kv && shares_elements(kv)) return DT_ERR_INVALID_ARG;
     if ((st = check_chunk(chunk, true)) != DT_OK) return st;
     if (chunk->lead < 1 || p->L < 1) return DT_ERR_INVALID_ARG;
     if (chunk->n_max > kMaxCommitNodes) return DT_ERR_UNSUPPORTED;
@@ -895,13 +894,7 @@ extern "C" dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk
     for (const void* q : {(const void*)p->tokens, (const void*)p->parents, (const void*)p->target,
                           (const void*)p->accepted, (const void*)p->lengths, (const void*)p->nodes})
         if (misaligned(q, 4)) return DT_ERR_INVALID_ARG;
-    CommitArgs a{};
     a.c = chunk_args(chunk);
-    if (kv) {
-        a.kv = cache_args(kv, 0);
-        a.layer_stride = kv->layers > 1 ? kv->layer_stride : 0;
-        a.layers = kv->layers;
-    }
     a.tokens = p->tokens;
     a.parents = p->parents;
     a.target = p->target;
@@ -911,5 +904,273 @@ extern "C" dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk
     a.nodes = p->nodes;
     const DeviceScope scope((hipStream_t)p->stream);
     if (!scope.ok() || launch_commit(a, (hipStream_t)p->stream) != hipSuccess) return DT_ERR_HIP;
+    return DT_OK;
+}
+
+extern "C" dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_commit_params* p) {
+    if (!p) return DT_ERR_INVALID_ARG;
+    dt_status st;
+    if (kv && (st = check_cache(kv, !chunk || chunk->B != 0)) != DT_OK) return st;
+    if (kv && shares_elements(kv)) return DT_ERR_INVALID_ARG;
+    CommitArgs a{};
+    if (kv) {
+        a.kv = cache_args(kv, 0);
+        a.layer_stride = kv->layers > 1 ? kv->layer_stride : 0;
+        a.layers = kv->layers;
+    }
+    return commit(chunk, p, a);
+}
+
+// ---------------------------------------------------------------------------
+// latents
+// ---------------------------------------------------------------------------
+
+// A cache of latents as one of keys with one head, for the checks and arguments
+// that the two have in common.
+static dt_kv_cache as_keys(const dt_latent_cache* c) {
+    dt_kv_cache kv{};
+    kv.k = kv.v = c->c;
+    kv.page_table = c->page_table;
+    kv.layer_stride = c->layer_stride;
+    kv.page_stride = c->page_stride;
+    kv.slot_stride = c->slot_stride;
+    kv.layers = c->layers;
+    kv.num_pages = c->num_pages;
+    kv.page_size = c->page_size;
+    kv.max_pages = c->max_pages;
+    kv.Hkv = 1;
+    kv.D = 128;
+    kv.dtype = c->dtype;
+    return kv;
+}
+
+static dt_status check_latents(const dt_latent_cache* c, bool pointers) {
+    if (!c || c->Dc < 1 || c->Dr < 1) return DT_ERR_INVALID_ARG;
+    const dt_kv_cache kv = as_keys(c);
+    const dt_status st = check_cache(&kv, pointers);
+    if (st != DT_OK) return st;
+    if ((c->Dc != 256 && c->Dc != 512) || (c->Dr != 32 && c->Dr != 64)) return DT_ERR_UNSUPPORTED;
+    return DT_OK;
+}
+
+static bool shares_latents(const dt_latent_cache* c) {
+    const int64_t n = (int64_t)c->Dc + c->Dr;
+    return (c->layers > 1 && c->layer_stride < n) || (c->num_pages > 1 && c->page_stride < n) ||
+           (c->page_size > 1 && c->slot_stride < n);
+}
+
+static CacheArgs latent_args(const dt_latent_cache* c, int layer) {
+    const dt_kv_cache kv = as_keys(c);
+    CacheArgs a = cache_args(&kv, layer);
+    a.D = c->Dc + c->Dr;
+    a.v = a.k + c->Dc;
+    return a;
+}
+
+// Rows of `heads` pieces of D elements, `head` apart, `stride` from row to row.
+static bool bad_pieces(const void* p, int64_t stride, int64_t head, int64_t rows, int64_t heads, int D) {
+    if (!p || misaligned(p, 16)) return true;
+    if (heads > 1 && (bad_stride(head) || head < D || head > INT64_MAX / 8192)) return true;
+    return rows > 1 && (bad_stride(stride) || stride < (heads > 1 ? (heads - 1) * head : 0) + D);
+}
+
+extern "C" dt_status dt_latent_append(const dt_latent_cache* cache, const dt_chunk* chunk,
+                                      const dt_latent_append_params* p) {
+    if (!p) return DT_ERR_INVALID_ARG;
+    dt_status st = check_latents(cache, !chunk || chunk->B != 0);
+    if (st != DT_OK) return st;
+    if (shares_latents(cache)) return DT_ERR_INVALID_ARG;
+    if ((st = check_chunk(chunk, true)) != DT_OK) return st;
+    if (p->layer < 0 || p->layer >= cache->layers || !isfinite(p->eps) || p->eps < 0 || !isfinite(p->rot_scale))
+        return DT_ERR_INVALID_ARG;
+    if (misaligned(p->freqs, 8) || misaligned(p->norm, 16)) return DT_ERR_INVALID_ARG;
+    if ((p->q_rot == nullptr) != (p->q_out == nullptr)) return DT_ERR_INVALID_ARG;
+    const int Hq = p->q_rot ? p->Hq : 0;
+    if (p->q_rot && Hq < 1) return DT_ERR_INVALID_ARG;
+    if (Hq > kMaxPassHeads) return DT_ERR_UNSUPPORTED;
+    if (chunk->B == 0) return DT_OK;
+    const int64_t rows = (int64_t)chunk->B * (chunk->lead + chunk->n_max);
+    if (bad_pieces(p->latent, p->latent_stride, 0, rows, 1, cache->Dc) ||
+        bad_pieces(p->k_rot, p->k_stride, 0, rows, 1, cache->Dr))
+        return DT_ERR_INVALID_ARG;
+    if (p->q_rot && (bad_pieces(p->q_rot, p->q_stride, p->q_head_stride, rows, Hq, cache->Dr) ||
+                     bad_pieces(p->q_out, p->q_out_stride, p->q_out_head_stride, rows, Hq, cache->Dr) ||
+                     (p->q_rot == p->q_out && ((rows > 1 && p->q_stride != p->q_out_stride) ||
+                                               (Hq > 1 && p->q_head_stride != p->q_out_head_stride)))))
+        return DT_ERR_INVALID_ARG;
+    LatentAppendArgs a{};
+    a.c = chunk_args(chunk);
+    a.kv = latent_args(cache, p->layer);
+    a.latent = (const uint16_t*)p->latent;
+    a.rot = (const uint16_t*)p->k_rot;
+    a.q = (const uint16_t*)p->q_rot;
+    a.q_out = (uint16_t*)p->q_out;
+    a.latent_stride = p->latent_stride;
+    a.rot_stride = p->k_stride;
+    a.q_stride = p->q_stride;
+    a.q_head = Hq > 1 ? p->q_head_stride : 0;
+    a.q_out_stride = p->q_out_stride;
+    a.q_out_head = Hq > 1 ? p->q_out_head_stride : 0;
+    a.Hq = Hq;
+    a.norm = (const uint16_t*)p->norm;
+    a.eps = p->eps;
+    a.rot_scale = p->rot_scale;
+    a.freqs = p->freqs;
+    a.interleaved = p->interleaved != 0;
+    const DeviceScope scope((hipStream_t)p->stream);
+    if (!scope.ok() ||
+        launch_latent_append(a, cache->dtype, cache->Dc, cache->Dr, (hipStream_t)p->stream) != hipSuccess)
+        return DT_ERR_HIP;
+    return DT_OK;
+}
+
+static dt_status check_latent_shape(const dt_latent_cache* cache, const dt_chunk* c, int32_t Hq) {
+    dt_status st = check_latents(cache, false);
+    if (st != DT_OK) return st;
+    const dt_kv_cache kv = as_keys(cache);
+    return check_attention_shape(&kv, c, Hq);
+}
+
+static dt_status check_prefill_shape(const dt_latent_cache* cache, const dt_chunk* c, int32_t Hq, int32_t Dn,
+                                     int32_t max_keys) {
+    const dt_status st = check_latent_shape(cache, c, Hq);
+    if (st != DT_OK) return st;
+    if (Dn < 1 || max_keys < 1) return DT_ERR_INVALID_ARG;
+    if (Dn != 64 && Dn != 128) return DT_ERR_UNSUPPORTED;
+    return DT_OK;
+}
+
+// The checks and arguments of both forms; heads of q have dq elements, of out dout.
+static dt_status latent_attention(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_latent_params* p, int dq,
+                                  int dout, AttentionArgs& a) {
+    dt_status st;
+    if ((st = check_latents(cache, chunk->B != 0)) != DT_OK) return st;
+    if ((st = check_chunk(chunk, true)) != DT_OK) return st;
+    if (p->layer < 0 || p->layer >= cache->layers || !isfinite(p->scale) || !(p->scale > 0)) return DT_ERR_INVALID_ARG;
+    if (misaligned(p->lse, 4)) return DT_ERR_INVALID_ARG;
+    if (chunk->B == 0) return DT_OK;
+    const int64_t rows = (int64_t)chunk->B * (chunk->lead + chunk->n_max);
+    if (bad_rows(p->q, p->q_stride, rows, p->Hq, dq) || bad_rows(p->out, p->out_stride, rows, p->Hq, dout) ||
+        p->q == p->out)
+        return DT_ERR_INVALID_ARG;
+    a.c = chunk_args(chunk);
+    a.kv = latent_args(cache, p->layer);
+    a.q = (const uint16_t*)p->q;
+    a.out = (uint16_t*)p->out;
+    a.q_stride = p->q_stride;
+    a.out_stride = p->out_stride;
+    a.Hq = a.G = p->Hq;
+    a.scale_log2 = (float)(p->scale * 1.4426950408889634074);
+    a.lse = p->lse;
+    return DT_OK;
+}
+
+static bool no_workspace(const void* workspace, size_t bytes, size_t need) {
+    return need > 0 && (!workspace || misaligned(workspace, 16) || bytes < need);
+}
+
+extern "C" size_t dt_latent_workspace(const dt_latent_cache* cache, const dt_chunk* chunk, int32_t Hq) {
+    if (check_latent_shape(cache, chunk, Hq) != DT_OK) return 0;
+    return latent_workspace(chunk_args(chunk), Hq, cache->Dc);
+}
+
+extern "C" dt_status dt_latent_attention(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_latent_params* p) {
+    if (!p) return DT_ERR_INVALID_ARG;
+    dt_status st = check_latent_shape(cache, chunk, p->Hq);
+    if (st != DT_OK) return st;
+    AttentionArgs a{};
+    if ((st = latent_attention(cache, chunk, p, cache->Dc + cache->Dr, cache->Dc, a)) != DT_OK || chunk->B == 0) return st;
+    if (no_workspace(p->workspace, p->workspace_bytes, latent_workspace(a.c, p->Hq, cache->Dc))) return DT_ERR_WORKSPACE;
+    const DeviceScope scope((hipStream_t)p->stream);
+    if (!scope.ok() || launch_latent_attention(a, cache->dtype, cache->Dc, cache->Dr, p->workspace,
+                                               (hipStream_t)p->stream) != hipSuccess)
+        return DT_ERR_HIP;
+    return DT_OK;
+}
+
+extern "C" size_t dt_latent_prefill_workspace(const dt_latent_cache* cache, const dt_chunk* chunk, int32_t Hq, int32_t Dn,
+                                              int32_t max_keys) {
+    if (check_prefill_shape(cache, chunk, Hq, Dn, max_keys) != DT_OK) return 0;
+    return prefill_workspace(chunk_args(chunk), Hq, Dn, max_keys);
+}
+
+extern "C" dt_status dt_latent_prefill(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_latent_params* p) {
+    if (!p) return DT_ERR_INVALID_ARG;
+    dt_status st = check_prefill_shape(cache, chunk, p->Hq, p->Dn, p->max_keys);
+    if (st != DT_OK) return st;
+    AttentionArgs a{};
+    if ((st = latent_attention(cache, chunk, p, p->Dn + cache->Dr, p->Dn, a)) != DT_OK || chunk->B == 0) return st;
+    if (!p->weight || misaligned(p->weight, 16)) return DT_ERR_INVALID_ARG;
+    if (no_workspace(p->workspace, p->workspace_bytes, prefill_workspace(a.c, p->Hq, p->Dn, p->max_keys)))
+        return DT_ERR_WORKSPACE;
+    a.G = 1;
+    a.kv.Hkv = p->Hq;
+    a.made_keys = p->max_keys;
+    if (a.kv.cap > p->max_keys) a.kv.cap = p->max_keys;
+    const DeviceScope scope((hipStream_t)p->stream);
+    if (!scope.ok() || launch_latent_prefill(a, p->weight, cache->dtype, cache->Dc, cache->Dr, p->Dn, p->workspace,
+                                             (hipStream_t)p->stream) != hipSuccess)
+        return DT_ERR_HIP;
+    return DT_OK;
+}
+
+extern "C" dt_status dt_latent_commit(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_commit_params* p) {
+    if (!p) return DT_ERR_INVALID_ARG;
+    const dt_status st = check_latents(cache, !chunk || chunk->B != 0);
+    if (st != DT_OK) return st;
+    if (shares_latents(cache)) return DT_ERR_INVALID_ARG;
+    CommitArgs a{};
+    a.kv = latent_args(cache, 0);
+    a.kv.v = nullptr;
+    a.layer_stride = cache->layers > 1 ? cache->layer_stride : 0;
+    a.layers = cache->layers;
+    return commit(chunk, p, a);
+}
+
+// ---------------------------------------------------------------------------
+// drawn tokens
+// ---------------------------------------------------------------------------
+
+static dt_status check_sample(const dt_sample_params* p) {
+    if (!p || p->B < 0 || p->lead < 0 || p->n_max < 0 || p->V < 1) return DT_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)p->lead + p->n_max;
+    if (rows < 1) return DT_ERR_INVALID_ARG;
+    if (p->dtype != DT_DTYPE_F32 && p->dtype != DT_DTYPE_BF16) return DT_ERR_INVALID_ARG;
+    if (p->B > 65535 || rows > kMaxChunkRows || p->B * rows > kMaxBatchRows || p->V >= kMaxV) return DT_ERR_UNSUPPORTED;
+    return DT_OK;
+}
+
+extern "C" size_t dt_sample_workspace(const dt_sample_params* p) {
+    if (check_sample(p) != DT_OK) return 0;
+    return sample_workspace((int64_t)p->B * (p->lead + p->n_max), p->V, p->dtype);
+}
+
+extern "C" dt_status dt_sample_rows(const dt_sample_params* p) {
+    const dt_status st = check_sample(p);
+    if (st != DT_OK) return st;
+    for (const void* q : {(const void*)p->n_nodes, (const void*)p->u, (const void*)p->temperature, (const void*)p->top_k,
+                          (const void*)p->top_p, (const void*)p->min_p, (const void*)p->tokens, (const void*)p->logp})
+        if (misaligned(q, 4)) return DT_ERR_INVALID_ARG;
+    if (p->B == 0) return DT_OK;
+    if (!p->logits || misaligned(p->logits, 16) || !p->u || !p->tokens) return DT_ERR_INVALID_ARG;
+    SampleArgs a{};
+    a.logits = p->logits;
+    a.B = p->B;
+    a.lead = p->lead;
+    a.n_max = p->n_max;
+    a.rows = p->lead + p->n_max;
+    a.V = p->V;
+    a.n_nodes = p->n_nodes;
+    a.u = p->u;
+    a.temperature = p->temperature;
+    a.top_k = p->top_k;
+    a.top_p = p->top_p;
+    a.min_p = p->min_p;
+    a.tokens = p->tokens;
+    a.logp = p->logp;
+    if (no_workspace(p->workspace, p->workspace_bytes, sample_workspace((int64_t)a.B * a.rows, a.V, p->dtype)))
+        return DT_ERR_WORKSPACE;
+    const DeviceScope scope((hipStream_t)p->stream);
+    if (!scope.ok() || launch_sample(a, p->dtype, p->workspace, (hipStream_t)p->stream) != hipSuccess) return DT_ERR_HIP;
     return DT_OK;
 }

@@ -1,5 +1,5 @@
-// dt_commit_path: the accepted path of each tree, and its keys and values
-// moved to the front of the chunk's slots.
+// dt_commit_path and dt_latent_commit: the accepted path of each tree, and its
+// keys and values (its latents) moved to the front of the chunk's slots.
 //
 // Every workgroup of a request walks the tree for itself, where it lies in
 // memory: a step reads the target's choice, then one wave scans the nodes for
@@ -60,9 +60,9 @@ __global__ void __launch_bounds__(256) commit_kernel(CommitArgs a) {
         s_at[1][i] = slot_offset(a.kv, b, first + i);
     }
     __syncthreads();
-    const int vecs = a.kv.D >> 3, cols = a.kv.Hkv * vecs;
-    for (int64_t job = (int64_t)blockIdx.y * 256 + tid; job < (int64_t)2 * a.layers * cols; job += (int64_t)gridDim.y * 256) {
-        const int layer = (int)(job / (2 * cols)), rest = (int)(job - (int64_t)layer * 2 * cols);
+    const int vecs = a.kv.D >> 3, cols = a.kv.Hkv * vecs, both = a.kv.v ? 2 * cols : cols;
+    for (int64_t job = (int64_t)blockIdx.y * 256 + tid; job < (int64_t)a.layers * both; job += (int64_t)gridDim.y * 256) {
+        const int layer = (int)(job / both), rest = (int)(job - (int64_t)layer * both);
         const int col = rest % cols;
         uint16_t* p = (rest < cols ? a.kv.k : a.kv.v) + layer * a.layer_stride + (col / vecs) * a.kv.head_stride +
                       (col % vecs) * 8;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) commit_kernel(CommitArgs a) {
 
 hipError_t launch_commit(const CommitArgs& a, hipStream_t stream) {
     int64_t groups = 1;
-    if (a.kv.k) groups = ((int64_t)2 * a.layers * a.kv.Hkv * (a.kv.D / 8) + 255) / 256;
+    if (a.kv.k) groups = ((int64_t)(a.kv.v ? 2 : 1) * a.layers * a.kv.Hkv * (a.kv.D / 8) + 255) / 256;
     commit_kernel<<<dim3((unsigned)a.c.B, (unsigned)(groups < 65535 ? groups : 65535)), 256, 0, stream>>>(a);
     return hipGetLastError();
 }

@@ -55,6 +55,26 @@ struct AttentionArgs {
     float scale_log2;              // scale * log2(e)
     bool by8;                      // slots 8 n .. 8 n + 7 lie in one page, within 2^31 bytes
     float* lse;
+    // latents only: kv.k points at them, kv.v at their rotated parts; each head's
+    // keys and values made from them, [B][Hq][made_keys][key, value]
+    const uint16_t* made;
+    int made_keys;
+};
+
+// One layer of a cache of latents: kv.k points at them, kv.v at their rotated parts.
+struct LatentAppendArgs {
+    ChunkArgs c;
+    CacheArgs kv;
+    const uint16_t* latent;
+    const uint16_t* rot;
+    const uint16_t* q;
+    uint16_t* q_out;
+    int64_t latent_stride, rot_stride, q_stride, q_head, q_out_stride, q_out_head;
+    int Hq;
+    const uint16_t* norm;
+    float eps, rot_scale;
+    const double* freqs;
+    int interleaved;
 };
 
 struct LogitsArgs {
@@ -79,9 +99,22 @@ struct LogitsArgs {
     int allow_rows;
 };
 
+struct SampleArgs {
+    const void* logits;
+    int B, lead, n_max, rows, V;
+    const int32_t* n_nodes;
+    const float* u;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* tokens;
+    float* logp;
+};
+
 struct CommitArgs {
     ChunkArgs c;
-    CacheArgs kv;                  // k = v = NULL: tokens only
+    CacheArgs kv;                  // k = NULL: tokens only; v = NULL: one pool
     int64_t layer_stride;
     int layers;
     const int32_t* tokens;
@@ -102,7 +135,15 @@ constexpr int64_t kMaxSlots = 1 << 30;
 hipError_t launch_append(const AppendArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_attention(const AttentionArgs& a, int dtype, void* workspace, hipStream_t stream);
 size_t attention_workspace(const ChunkArgs& c, int Hkv, int Hq, int D);
+hipError_t launch_latent_append(const LatentAppendArgs& a, int dtype, int C, int R, hipStream_t stream);
+hipError_t launch_latent_attention(const AttentionArgs& a, int dtype, int C, int R, void* workspace, hipStream_t stream);
+size_t latent_workspace(const ChunkArgs& c, int Hq, int C);
+hipError_t launch_latent_prefill(AttentionArgs a, const void* weight, int dtype, int C, int R, int N, void* workspace,
+                                 hipStream_t stream);
+size_t prefill_workspace(const ChunkArgs& c, int Hq, int N, int keys);
 hipError_t launch_logits(const LogitsArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_sample(const SampleArgs& a, int dtype, void* workspace, hipStream_t stream);
+size_t sample_workspace(int64_t rows, int V, int dtype);
 hipError_t launch_commit(const CommitArgs& a, hipStream_t stream);
 
 #ifdef __HIPCC__

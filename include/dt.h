@@ -521,6 +521,173 @@ typedef struct dt_commit_params {
  *   (n_max > 1024, or a limit above), DT_ERR_HIP. */
 dt_status dt_commit_path(const dt_kv_cache* kv, const dt_chunk* chunk, const dt_commit_params* p);
 
+/* ------------------------------------------------------------------------
+ * A target with latent attention, and a target whose tokens are drawn.
+ *
+ * Latent attention keeps one vector a token for all heads: a latent c of Dc
+ * elements, from which each head's keys and values are products, and a part r
+ * of Dr rotated elements that every head's key shares.  dt_latent_append,
+ * dt_latent_attention or dt_latent_prefill, and dt_latent_commit stand where
+ * dt_kv_append, dt_tree_attention and dt_commit_path stand for a cache of
+ * keys and values; the chunk is the same.
+ *
+ * dt_sample_rows stands where dt_position_topk with k = 1 stands for a target
+ * that is followed greedily: a token for every row, which dt_commit_path and
+ * dt_latent_commit take as `target`.  A node's row is drawn whether or not its
+ * node is reached, and the path follows the drawn tokens, so the accepted
+ * tokens have the target's own distribution whatever the tree.
+ * ------------------------------------------------------------------------ */
+
+/* A paged cache of latents.  Element i of the token in slot s of request b in
+ * layer l lies at
+ *   c + l * layer_stride + page * page_stride + (s % page_size) * slot_stride + i
+ * with page = page_table[b * max_pages + s / page_size]: the latent first
+ * (i < Dc), then the rotated part.  Strides, pages and slots as in dt_kv_cache;
+ * calls that write refuse strides below Dc + Dr. */
+typedef struct dt_latent_cache {
+    void* c;
+    const int32_t* page_table; /* device [B][max_pages] */
+    int64_t layer_stride;
+    int64_t page_stride;
+    int64_t slot_stride;
+    int32_t layers;            /* >= 1 */
+    int32_t num_pages;         /* >= 1 */
+    int32_t page_size;         /* >= 1; max_pages * page_size <= 2^30 */
+    int32_t max_pages;         /* >= 1 */
+    int32_t Dc;                /* elements of a latent: 256 or 512 */
+    int32_t Dr;                /* elements of the rotated part: 32 or 64 */
+    int32_t dtype;             /* DT_DTYPE_BF16 or DT_DTYPE_F16 */
+} dt_latent_cache;
+
+typedef struct dt_latent_append_params {
+    const void* latent;        /* [B][lead + n_max] rows of Dc */
+    const void* k_rot;         /* [B][lead + n_max] rows of Dr: the keys' part before its rotation */
+    const void* q_rot;         /* [B][lead + n_max] rows of Hq heads of Dr, or NULL (cache only) */
+    void* q_out;               /* as q_rot; may be q_rot itself with the same strides; NULL iff q_rot is */
+    int64_t latent_stride;     /* elements from row to row */
+    int64_t k_stride;
+    int64_t q_stride;
+    int64_t q_head_stride;     /* elements from head to head of a row */
+    int64_t q_out_stride;
+    int64_t q_out_head_stride;
+    int32_t Hq;                /* query heads, 1..4096 (not read when q_rot is NULL) */
+    const void* norm;          /* [Dc] weights of dtype, or NULL = no norm */
+    float eps;                 /* >= 0 */
+    const double* freqs;       /* device [Dr / 2] radians a position, or NULL = no rotation */
+    int32_t interleaved;       /* as in dt_append_params, with rot_dim = Dr */
+    float rot_scale;
+    int32_t layer;
+    void* stream;
+} dt_latent_append_params;
+
+/* The new tokens' latents on their way from the projection: for every row
+ *   c = latent * rsqrt(mean(latent^2) + eps) * norm   (norm given; else latent)
+ * to the row's cache slot, k_rot turned by the row's position behind it, and
+ * the queries' q_rot, every head, turned by it to q_out.  Pairs, angles and
+ * roundings as in dt_kv_append; without freqs k_rot and q_rot are copied bit by
+ * bit.  Pointers 16-byte aligned, strides multiples of 8; in buffers of
+ * more than one row at least what a row covers, heads at least Dr apart.
+ * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above), DT_ERR_HIP. */
+dt_status dt_latent_append(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_latent_append_params* p);
+
+typedef struct dt_latent_params {
+    const void* q;             /* [B][lead + n_max] rows of Hq heads, see below */
+    void* out;
+    const void* weight;        /* dt_latent_prefill only: [Hq][2 * Dn][Dc] of dtype */
+    int64_t q_stride;          /* elements from row to row; the heads of a row are contiguous */
+    int64_t out_stride;
+    int32_t Hq;                /* query heads, 1..4096 */
+    int32_t Dn;                /* dt_latent_prefill only: 64 or 128 */
+    int32_t max_keys;          /* dt_latent_prefill only: slots at or behind it are not seen, >= 1 */
+    float scale;               /* > 0, finite */
+    float* lse;                /* [B][lead + n_max][Hq] or NULL: log of the sum of exp(score) */
+    int32_t layer;
+    void* workspace;           /* 16-byte aligned device scratch of the size below */
+    size_t workspace_bytes;
+    void* stream;
+} dt_latent_params;
+
+/* Latent attention in its absorbed form: a head's query (q_c, q_r) has Dc + Dr
+ * elements (q_c is its unrotated part times the head's key weight), its result
+ * Dc (to be multiplied by the head's value weight):
+ *   out = sum_j softmax_j(scale * (q_c . c_j + q_r . r_j)) c_j
+ * over the slots j that the row sees, as in dt_tree_attention, as are the
+ * numerics, rows that see nothing, unseen infinities and NaN, and limits.
+ * q may not overlap out.  Pointers 16-byte aligned (lse 4), strides multiples
+ * of 8 and at least Hq times a head's elements.
+ * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above, or
+ *   B * (lead + n_max) * Hq >= 2^31), DT_ERR_WORKSPACE, DT_ERR_HIP. */
+dt_status dt_latent_attention(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_latent_params* p);
+
+/* Bytes of workspace dt_latent_attention needs (depends on Dc, on the chunk's
+ * B, lead and n_max and on Hq only); 0 if a call would be refused for these.
+ * Its contents are meaningless between calls. */
+size_t dt_latent_workspace(const dt_latent_cache* cache, const dt_chunk* chunk, int32_t Hq);
+
+/* Latent attention in its expanded form, for many rows (a piece of a prompt):
+ * with k_j = weight[h][0..Dn) . c_j and v_j = weight[h][Dn..2 Dn) . c_j, sums in
+ * fp32 and rounded to dtype, and q = (q_n, q_r) of Dn + Dr elements,
+ *   out = sum_j softmax_j(scale * (q_n . k_j + q_r . r_j)) v_j    (Dn elements)
+ * for every head h.  The keys and values are made in the workspace, 4 * Dn bytes
+ * a head, request and slot below max_keys: at least the longest request's
+ * ctx_len + rows for all to be seen.  Of a request without rows none are made.
+ * An infinity or NaN in a latent that is seen reaches the result as NaN.
+ * The rest is as in dt_latent_attention; weight is contiguous, 16-byte aligned.
+ * Errors: as dt_latent_attention, and DT_ERR_UNSUPPORTED for another Dn. */
+dt_status dt_latent_prefill(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_latent_params* p);
+
+/* Bytes of workspace dt_latent_prefill needs; 0 if a call would be refused. */
+size_t dt_latent_prefill_workspace(const dt_latent_cache* cache, const dt_chunk* chunk, int32_t Hq, int32_t Dn,
+                                   int32_t max_keys);
+
+/* dt_commit_path for a cache of latents (which may not be NULL). */
+dt_status dt_latent_commit(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_commit_params* p);
+
+typedef struct dt_sample_params {
+    const void* logits;        /* device [B][lead + n_max][V] of dtype, 16-byte aligned */
+    int32_t B;                 /* 0 <= B <= 65535 */
+    int32_t lead;              /* >= 0 */
+    int32_t n_max;             /* >= 0; 1 <= lead + n_max <= 65536, B * (lead + n_max) <= 2^24 */
+    int32_t V;                 /* 1 <= V < 2^26 */
+    int32_t dtype;             /* DT_DTYPE_F32 or DT_DTYPE_BF16 */
+    const int32_t* n_nodes;    /* [B], clamped to 0..n_max; NULL = n_max */
+    const float* u;            /* [B][lead + n_max] random numbers in [0, 1) */
+    const float* temperature;  /* [B] or NULL = 1; not above 0 (or NaN): the largest logit's token */
+    const int32_t* top_k;      /* [B] or NULL; not above 0: off */
+    const float* top_p;        /* [B] or NULL; 1 and more (or NaN): off */
+    const float* min_p;        /* [B] or NULL; not above 0 (or NaN): off */
+    int32_t* tokens;           /* [B][lead + n_max] */
+    float* logp;               /* [B][lead + n_max] or NULL: log of the probability the token was drawn with */
+    void* workspace;           /* 16-byte aligned device scratch of dt_sample_workspace() bytes */
+    size_t workspace_bytes;
+    void* stream;
+} dt_sample_params;
+
+/* A token for every row of a chunk, drawn by the row's random number u.  With
+ * the tokens in the order (logit desc, id asc) and w = exp((logit - largest
+ * logit) / temperature):
+ *   top_k   only the first top_k tokens stay;
+ *   top_p   of these a token stays iff the w of those before it sum to less
+ *           than top_p times the sum of all of these (the first always);
+ *   min_p   a token stays iff w >= min_p (the first always).
+ * The token drawn is the first BY ID, of those that stay, with which the sum of
+ * their w so far exceeds u times the sum of them all.  logp is the logarithm
+ * of its w over that sum.  Each w is rounded to a multiple of 2^(n - 62), 2^n
+ * the power of two from V on (2^-44 for V = 151936), and summed exactly, so no
+ * result depends on an order.  A row whose logits are all
+ * -inf gives token -1 and logp -inf.  Logits are finite or -inf; NaN and +inf
+ * give an unspecified token (but a memory-safe one, in -1..V-1), and u outside
+ * [0, 1) the first or the last token that stays.  Rows behind the last node are
+ * left as they were.
+ * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above),
+ *   DT_ERR_WORKSPACE, DT_ERR_HIP. */
+dt_status dt_sample_rows(const dt_sample_params* p);
+
+/* Bytes of workspace dt_sample_rows needs (depends on B, lead, n_max, V and
+ * dtype only); 0 if none is needed or a call would be refused for these.  Its
+ * contents are meaningless between calls. */
+size_t dt_sample_workspace(const dt_sample_params* p);
+
 #ifdef __cplusplus
 }
 #endif
