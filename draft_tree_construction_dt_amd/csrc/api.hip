@@ -1060,6 +1060,7 @@ static dt_status latent_attention(const dt_latent_cache* cache, const dt_chunk* 
     a.q_stride = p->q_stride;
     a.out_stride = p->out_stride;
     a.Hq = a.G = p->Hq;
+    a.by8 = cache->page_size % 8 == 0 && a.kv.slot_stride < (1 << 26);
     a.scale_log2 = (float)(p->scale * 1.4426950408889634074);
     a.lse = p->lse;
     return DT_OK;

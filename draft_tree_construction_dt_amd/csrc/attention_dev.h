@@ -238,7 +238,7 @@ struct False {
 template <int D>
 struct Heads {
     static constexpr int kKey = D, kRot = 0, kOut = D;
-    static constexpr bool kShared = false, kMade = false;
+    static constexpr bool kMade = false;
     static __device__ inline int swizzle_key(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
     static __device__ inline int swizzle_out(int row) { return D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2; }
     static __device__ inline int swizzle_rot(int) { return 0; }
@@ -249,25 +249,12 @@ template <int R>
 struct Rotated {
     static __device__ inline int swizzle_rot(int row) { return R == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
 };
-// Latents: C elements that are key and value of every head, then the rotated
-// part.  One tile serves both products, so one permutation has to: pieces move
-// by the row's number with its two pairs of bits swapped.  16 consecutive rows
-// have 16 different ones (a piece of each row at once, for scores), and rows 4 n
-// to 4 n + 3 move their 64-byte groups apart (a group of 4 rows at once, for
-// the transposing read).
-template <int C, int R>
-struct Latents : Rotated<R> {
-    static constexpr int kKey = C, kRot = R, kOut = C;
-    static constexpr bool kShared = true, kMade = false;
-    static __device__ inline int swizzle_key(int row) { return (row & 3) << 2 | ((row >> 2) & 3); }
-    static __device__ inline int swizzle_out(int row) { return swizzle_key(row); }
-};
 // Expanded: each head's N elements of key and N of value, made from the
 // latents, and the rotated part from the cache.
 template <int N, int R>
 struct Expanded : Rotated<R> {
     static constexpr int kKey = N, kRot = R, kOut = N;
-    static constexpr bool kShared = false, kMade = true;
+    static constexpr bool kMade = true;
     static __device__ inline int swizzle_key(int row) { return Heads<N>::swizzle_key(row); }
     static __device__ inline int swizzle_out(int row) { return Heads<N>::swizzle_out(row); }
 };
@@ -279,7 +266,7 @@ struct Shape {
     static constexpr int kKeyTile = KT * L::kKey * 2;      // bytes of a tile of keys, without their rotated part
     static constexpr int kRotTile = KT * L::kRot * 2;
     static constexpr int kTile = kKeyTile + kRotTile;
-    static constexpr int kOutTile = L::kShared ? 0 : KT * L::kOut * 2;
+    static constexpr int kOutTile = KT * L::kOut * 2;
     static constexpr int kGroup = 2 * (kTile + kOutTile);  // the keys' two buffers, the values' two
     static constexpr int kLds = kGroup * WK;
     static constexpr int kPartial = kMt * (L::kOut + 2);   // floats of a split's partial result
@@ -389,7 +376,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     const auto issue = [&](const Place& p, int buf) __attribute__((always_inline)) {
         const uint32_t to = group + buf * S::kTile;
         const bool ok = is_valid(p);
-        if constexpr (L::kRot > 0) {
+        if constexpr (L::kMade) {
             // the rotated parts: pieces of kRotRows rows a copy, the copies dealt to the waves
             constexpr int kRotUnits = L::kRot / 8, kRotRows = 64 / kRotUnits, kRotCopies = KT / kRotRows;
             const int64_t off = ok ? p.page * a.kv.page_stride + p.in * a.kv.slot_stride : 0;
@@ -405,33 +392,16 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
                 copy_to_lds(a.kv.v + offset_of(trow) + ((lane % kRotUnits) ^ L::swizzle_rot(trow)) * 8,
                             to + S::kKeyTile + at * 1024);
             }
-            if constexpr (L::kMade) {
-                // rows of key and value, one after the other; behind the last key the last again
-                const int k0 = p.tile;
-                const char* const base = (const char*)(made + (int64_t)k0 * (2 * D));
+            // rows of key and value, one after the other; behind the last key the last again
+            const int k0 = p.tile;
+            const char* const base = (const char*)(made + (int64_t)k0 * (2 * D));
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int at = wl * kCopies + i, trow = at * kRpi + prow;
-                    const uint32_t r0 = (uint32_t)(k0 + trow < k_end ? trow : k_end - 1 - k0) * (4 * D);
-                    copy_to_lds(base, r0 + (piece ^ L::swizzle_key(trow)) * 16, to + at * 1024);
-                    copy_to_lds(base, r0 + 2 * D + (piece ^ L::swizzle_out(trow)) * 16,
-                                group + 2 * S::kTile + buf * S::kOutTile + at * 1024);
-                }
-            } else if constexpr (kRpi == 1) {
-                // a row a copy: its offset is the wave's
-#pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int at = wl * kCopies + i;
-                    const int64_t o = (int64_t)((u64)(uint32_t)__builtin_amdgcn_readlane(lo, at) |
-                                                (u64)(uint32_t)__builtin_amdgcn_readlane(hi, at) << 32);
-                    copy_to_lds((const char*)(kbase + o), (piece ^ L::swizzle_key(at)) * 16, to + at * 1024);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int at = wl * kCopies + i, trow = at * kRpi + prow;
-                    copy_to_lds(kbase + offset_of(trow) + (piece ^ L::swizzle_key(trow)) * 8, to + at * 1024);
-                }
+            for (int i = 0; i < kCopies; ++i) {
+                const int at = wl * kCopies + i, trow = at * kRpi + prow;
+                const uint32_t r0 = (uint32_t)(k0 + trow < k_end ? trow : k_end - 1 - k0) * (4 * D);
+                copy_to_lds(base, r0 + (piece ^ L::swizzle_key(trow)) * 16, to + at * 1024);
+                copy_to_lds(base, r0 + 2 * D + (piece ^ L::swizzle_out(trow)) * 16,
+                            group + 2 * S::kTile + buf * S::kOutTile + at * 1024);
             }
             return;
         } else if (a.by8) {
@@ -479,19 +449,10 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
         return s < D / 16 ? kaddr[s % kKeyAddr] + s / kKeyAddr * 256 : raddr[s < D / 16 ? 0 : s - D / 16];
     };
     const int vrow = 4 * half + ((lane >> 2) & 3);
-    constexpr int kOutAddr = L::kShared && ND > 4 ? 4 : ND;
-    int vaddr[kOutAddr], vaddr8[L::kShared ? kOutAddr : 1];                     // of 4 rows, and of those 8 further on
+    int vaddr[ND];
 #pragma unroll
-    for (int d = 0; d < kOutAddr; ++d) {
-        const int in = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-        if constexpr (L::kShared) {
-            const int at = (wd * ND + d) * 64 + in;
-            vaddr[d] = vrow * kOut * 2 + (at ^ (L::swizzle_out(vrow) * 16));
-            vaddr8[d] = (vrow + 8) * kOut * 2 + (at ^ (L::swizzle_out(vrow + 8) * 16));
-        } else {
-            vaddr[d] = vrow * kOut * 2 + ((((wd * ND + d) * 4) ^ L::swizzle_out(vrow)) * 16) + in;
-        }
-    }
+    for (int d = 0; d < ND; ++d)
+        vaddr[d] = vrow * kOut * 2 + ((((wd * ND + d) * 4) ^ L::swizzle_out(vrow)) * 16) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
     char* const my = lds + wk * S::kGroup;
 
     f32x16 o[ND];
@@ -512,11 +473,8 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
     };
     const auto value = [&](const char* vt, int d, int x) __attribute__((always_inline)) {  // V^T of 32 elements and 16 keys
         typedef __attribute__((address_space(3))) s16x4 lds4;
-        const char* const at = vt + vaddr[d % kOutAddr] + d / kOutAddr * 256 + 16 * x * kOut * 2;
-        const char* const at8 = L::kShared ? vt + vaddr8[L::kShared ? d % kOutAddr : 0] + d / kOutAddr * 256 + 16 * x * kOut * 2
-                                           : at + 8 * kOut * 2;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)at);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)at8);
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x) * kOut * 2));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vt + vaddr[d] + (16 * x + 8) * kOut * 2));
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
     // A wave's products go before the other's vector work on the same SIMD
@@ -697,7 +655,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const Job& job, i
             f32x16 s[NB];
 #pragma unroll
             for (int n = 0; n < NB; ++n) s[n] = scores(my + (i & 1) * S::kTile, n);
-            tile(k0, s, L::kShared ? my + (i & 1) * S::kTile : my + 2 * S::kTile + (i & 1) * S::kOutTile, now, is_masked);
+            tile(k0, s, my + 2 * S::kTile + (i & 1) * S::kOutTile, now, is_masked);
         }
         if constexpr (kAlone) {
             valid = valid1;
@@ -913,23 +871,29 @@ int64_t max_jobs(const AttentionArgs& a, int mt, int slots) {
     return (jobs + 7) / 8 + a.c.B * mtiles;
 }
 
-// The kernel and the join; `slots` workgroups are resident at a time.
-template <class T, class L, int WM, int WK, int WD, int KT, int PER_CU>
-hipError_t run(const AttentionArgs& a, int slots, void* workspace, hipStream_t stream) {
-    using S = Shape<T, L, WM, WK, WD, KT>;
-    constexpr int D = L::kOut;
-    const int64_t jobs = 8 * max_jobs(a, S::kMt, slots);
+// The kernel and the join: row tiles of MT rows, results of D elements, `slots`
+// workgroups resident at a time.
+template <class T, int D, int MT, class Kernel>
+hipError_t run_kernel(Kernel kernel, const AttentionArgs& a, int threads, int lds, int slots, void* workspace,
+                      hipStream_t stream) {
+    const int64_t jobs = 8 * max_jobs(a, MT, slots);
     const int64_t x = jobs < kMaxGridX ? jobs : kMaxGridX;
-    const auto kernel = attention_kernel<T, L, WM, WK, WD, KT, PER_CU>;
     int* const plan = (int*)workspace;
     float* const partial = (float*)((char*)workspace + kPlanBytes);
-    kernel<<<dim3((unsigned)x, (unsigned)((jobs + x - 1) / x)), S::kThreads, S::kLds, stream>>>(a, slots, plan, partial);
+    kernel<<<dim3((unsigned)x, (unsigned)((jobs + x - 1) / x)), threads, lds, stream>>>(a, slots, plan, partial);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t waves = ((int64_t)a.c.B * a.c.rows * a.Hq * (D <= 256 ? D / 4 : 64) + 63) / 64;
     const unsigned groups = waves < 4 * 8 * kCus ? (unsigned)((waves + 3) / 4) : 8 * kCus;
-    combine_kernel<T, D, S::kMt><<<groups, 256, 0, stream>>>(a, plan, partial);
+    combine_kernel<T, D, MT><<<groups, 256, 0, stream>>>(a, plan, partial);
     return hipGetLastError();
+}
+
+template <class T, class L, int WM, int WK, int WD, int KT, int PER_CU>
+hipError_t run(const AttentionArgs& a, int slots, void* workspace, hipStream_t stream) {
+    using S = Shape<T, L, WM, WK, WD, KT>;
+    return run_kernel<T, L::kOut, S::kMt>(attention_kernel<T, L, WM, WK, WD, KT, PER_CU>, a, S::kThreads, S::kLds, slots,
+                                          workspace, stream);
 }
 
 // Bytes of the partial results and the plan.  partials_of(): at most work / c

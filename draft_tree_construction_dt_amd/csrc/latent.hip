@@ -13,7 +13,7 @@
 // cheaper one from about 170 rows on.
 //
 // Both run through the tile loop of attention_dev.h.
-#include "attention_dev.h"
+#include "latent_dev.h"
 
 namespace dt {
 namespace {
@@ -248,13 +248,15 @@ hipError_t with_sizes(int dtype, int C, int R, F f) {
     return dtype == DT_DTYPE_BF16 ? sizes(Bf16()) : sizes(F16());
 }
 
-// Row tile by the rows of a request: with up to 32 (64) of them four (two)
-// waves make the same scores and a quarter (half) of the outputs each.
-int latent_tile_rows(const ChunkArgs& c, int Hq) {
-    const int64_t m = (int64_t)c.rows * Hq;
-    return m <= 32 ? 32 : (m <= 64 ? 64 : 128);
+template <int C>
+constexpr int kLatentSlots = kCus * (C == 512 ? 1 : 2);
+
+template <class T, int C, int R>
+hipError_t run_latent(const AttentionArgs& a, void* workspace, hipStream_t stream) {
+    using S = Latent<C, R>;
+    const auto kernel = a.by8 ? latent_kernel<T, C, R, true> : latent_kernel<T, C, R, false>;
+    return run_kernel<T, C, S::kRows>(kernel, a, 256, S::kLds, kLatentSlots<C>, workspace, stream);
 }
-constexpr int kLatentSlots = kCus;
 
 int prefill_tile_rows(const ChunkArgs& c) { return c.rows <= 64 ? 64 : 128; }
 constexpr int kPrefillSlots = 2 * kCus;
@@ -274,18 +276,14 @@ hipError_t launch_latent_append(const LatentAppendArgs& a, int dtype, int C, int
 }
 
 size_t latent_workspace(const ChunkArgs& c, int Hq, int C) {
-    const int mt = latent_tile_rows(c, Hq);
-    return partial_bytes((int64_t)c.B * (((int64_t)c.rows * Hq + mt - 1) / mt), kLatentSlots, mt, C);
+    const int64_t segments = (int64_t)c.B * (((int64_t)c.rows * Hq + 63) / 64);
+    return partial_bytes(segments, C == 512 ? kLatentSlots<512> : kLatentSlots<256>, 64, C);
 }
 
 hipError_t launch_latent_attention(const AttentionArgs& a, int dtype, int C, int R, void* workspace, hipStream_t stream) {
     return with_sizes(dtype, C, R, [&](auto t, auto l) {
-        using T = decltype(t);
         using L = decltype(l);
-        const int mt = latent_tile_rows(a.c, a.G);
-        if (mt == 32) return run<T, L, 1, 1, 4, 64, 1>(a, kLatentSlots, workspace, stream);
-        if (mt == 64) return run<T, L, 2, 1, 2, 64, 1>(a, kLatentSlots, workspace, stream);
-        return run<T, L, 4, 1, 1, 32, 1>(a, kLatentSlots, workspace, stream);
+        return run_latent<decltype(t), L::kKey, L::kRot>(a, workspace, stream);
     });
 }
 
