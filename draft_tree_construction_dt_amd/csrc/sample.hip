@@ -5,10 +5,23 @@
 // some logit, and the first few by id of those at it.  With the weights held as
 // integers (w scaled by 2^shift, so that V of them fit 62 bits) every sum is
 // exact, whatever its order and grouping: the cut can be narrowed digit by digit
-// over the logits' bits with histograms in LDS, the drawn token part by part
-// over the ids, and neither ever meets two sums that should agree and do not.
+// over the logits' bits with histograms in LDS, the drawn token over the ids, and
+// neither ever meets two sums that should agree and do not.
 //
-// A workgroup takes a row.
+// A workgroup takes a row.  It reads it for the largest logit, and keeps each
+// thread's own largest: the j-th of those is a limit that j tokens at least
+// reach.  Then, by what the request asks for:
+//   top-k       the tokens at or above that limit go to a list in LDS, once
+//               through the row, and all else happens there;
+//   min-p only  the same with the limit that min_p sets;
+//   top-p       one pass makes every weight and a histogram of them over the
+//               logits, and the list: usually the cut lies within it.  If not
+//               (a flat row), the tokens of the cut's own bin are listed, and
+//               a last pass draws among all;
+//   none        one pass for the sums of 16 parts of the row, then the part's
+//               parts.
+// A list that overflows, or a larger top_k, narrows the cut over the row itself.
+#include <float.h>
 #include <math.h>
 
 #include "pass.h"
@@ -20,109 +33,156 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBins = 2048;        // of a histogram: 11 bits of a logit at a time
+constexpr int kBits = 11, kBins = 1 << kBits;              // of a histogram
 constexpr int kDeep = 4;           // 16-byte loads of a lane in flight
+constexpr int kList = 6144;        // tokens of the list
+// Threads whose largest logit reaches the list's limit.  For top_k as many as
+// that, up to 1000 (of 148 logits a thread, V = 151936, about 3800 tokens in no
+// order reach what 1000 of 1024 threads do); for top_p alone 896 (2100 tokens).
+constexpr int kMostK = 1000;
+constexpr int kForP = 896;
+constexpr int kTable = 64;
 
-// Bits whose order is that of the values (no NaN).
-__device__ inline uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x);
+// Bits whose order is that of the values (no NaN; -0 and 0 are one).
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
     return (int32_t)b < 0 ? ~b : b | 0x80000000u;
 }
-__device__ inline float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
-// e^((x - top) / temperature) * 2^shift, rounded: 2^(j / 64) from a table times
-// the series of 2^(f / 64), |f| <= 1/2, to the fourth power; the next term is
+// e^((x - top) / temperature) * 2^shift, rounded: 2^(j / 64) from a table in LDS
+// times the series of 2^f, |f| <= 1/128, to the fourth power; the next term is
 // below 2^-44.  In fp64: a sum over V weights is compared with u times the total,
 // and errors of 2^-24 a weight would move the drawn token in one row of a
-// thousand.
+// thousand.  No branches: eight logits' weights are made side by side.
+typedef const __attribute__((address_space(3))) double* Table;
 struct Weights {
     double top, rate;              // rate = 64 log2(e) / temperature
-    double least;                  // below it a weight is 0
-    int shift;
-    const double* table;           // LDS, 2^(j / 64)
+    double least;                  // 64 times the smallest exponent of a weight
+    Table table;                   // 2^(j / 64 + shift)
 
-    __device__ u64 operator()(float x) const {
-        const double t = ((double)x - top) * rate;
-        if (!(t > least)) return 0;
-        const double n = rint(t), g = (t - n) * (0.69314718055994530942 / 64);
-        const int i = (int)n;
-        const double p = 1 + g * (1 + g * (0.5 + g * (1.0 / 6 + g * (1.0 / 24))));
-        const double w = ldexp(table[i & 63] * p, (i >> 6) + shift);       // at most 2^50
-        return (u64)__double_as_longlong(w + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
+    __device__ __forceinline__ u64 operator()(float x) const {
+        constexpr double kRound = 6755399441055744.0, kOne = 0.69314718055994530942 / kTable;
+        constexpr double k2 = kOne * kOne / 2, k3 = k2 * kOne / 3, k4 = k3 * kOne / 4;
+        const double t = fmax(((double)x - top) * rate, least);            // (NaN, as inf - inf: the least)
+        const double r = t + kRound, f = t - (r - kRound);
+        const int i = (int)(uint32_t)__double_as_longlong(r);
+        const u64 e = (u64)__double_as_longlong(table[i & (kTable - 1)]) + ((u64)(uint32_t)(i >> 6) << 52);
+        const double w = __longlong_as_double((long long)e);
+        const double q = f * (kOne + f * (k2 + f * (k3 + f * k4)));
+        return (u64)__double_as_longlong(fma(w, q, w) + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
     }
 };
 
-// One row in memory, in groups of 16 aligned bytes; a group may begin before the
-// row or end behind it.
+// One row in memory, in groups of 16 aligned bytes; what the first and the last
+// group hold beside the row comes as -inf, and so do NaN.
 template <class E>
 struct Row {
     static constexpr int kEach = 16 / sizeof(E);
-    const E* base;                 // of group 0
+    static constexpr uint32_t kNone = sizeof(E) == 2 ? 0xFF80FF80u : 0xFF800000u;
+    typedef const __attribute__((address_space(1))) E* Elements;
+    typedef const __attribute__((address_space(1))) u32x4* Vectors;
+    Elements base;                 // of group 0
     int before, V, groups;         // elements of group 0 that are not the row's
 
-    __device__ Row(const void* logits, int64_t row, int V_) : V(V_) {
+    __device__ __forceinline__ Row(const void* logits, int64_t row, int V_) : V(V_) {
         const int64_t at = row * V_;
         before = (int)(at % kEach);
-        base = (const E*)logits + (at - before);
+        base = (Elements)((const E*)logits + (at - before));
         groups = (int)(((int64_t)before + V_ + kEach - 1) / kEach);
     }
-    static __device__ float get(uint32_t bits) {
+    static __device__ __forceinline__ float get(uint32_t bits) {
         return sizeof(E) == 2 ? __uint_as_float(bits << 16) : __uint_as_float(bits);
     }
-    // f(id, x) for every element of groups g0 .. g1 - 1 by one wave; the waves'
-    // lanes stay together (f may use the whole wave: what is not there comes
-    // as id -1, x = -inf).  NaN come as -inf, too.
+    __device__ __forceinline__ u32x4 load(int g) const {
+        if (g > 0 && g < groups - 1) return *(Vectors)(base + (int64_t)g * kEach);
+        u32x4 v = {kNone, kNone, kNone, kNone};
+        for (int e = 0; e < kEach; ++e) {
+            const int64_t id = (int64_t)g * kEach - before + e;
+            if (id < 0 || id >= V) continue;
+            const uint32_t b = base[(int64_t)g * kEach + e];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(E) == 2) {
+                    if (e == 2 * i) v[i] = (v[i] & 0xFFFF0000u) | b;
+                    if (e == 2 * i + 1) v[i] = (v[i] & 0xFFFFu) | b << 16;
+                } else if (e == i) {
+                    v[i] = b;
+                }
+            }
+        }
+        return v;
+    }
+    static __device__ __forceinline__ float at(const u32x4& v, int e) {
+        if constexpr (sizeof(E) == 2) return __uint_as_float(e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
+        else return __uint_as_float(v[e]);
+    }
+    // f(g, v) for groups g0 .. g1 - 1 by one wave, whose lanes stay together
+    // (f may use the whole wave; lanes without a group get -inf).
     template <class F>
-    __device__ void scan(int g0, int g1, int lane, F f) const {
+    __device__ __forceinline__ void groups_of(int g0, int g1, int lane, F f) const {
         for (int64_t first = g0; first < g1; first += kDeep * 64) {
             u32x4 v[kDeep];
 #pragma unroll
             for (int i = 0; i < kDeep; ++i) {
                 const int64_t g = first + i * 64 + lane;
-                v[i] = u32x4{0, 0, 0, 0};
-                if (g >= g1) continue;
-                const int64_t id = g * kEach - before;
-                if (id >= 0 && id + kEach <= V) {
-                    v[i] = *(const u32x4*)(base + g * kEach);
-                } else {
-                    for (int e = 0; e < kEach; ++e)
-                        if (id + e >= 0 && id + e < V) {
-                            const uint32_t b = base[g * kEach + e];
-                            if constexpr (sizeof(E) == 2) v[i][e >> 1] |= b << (16 * (e & 1));
-                            else v[i][e] = b;
-                        }
-                }
+                v[i] = u32x4{kNone, kNone, kNone, kNone};
+                if (g < g1) v[i] = load((int)g);
             }
 #pragma unroll
             for (int i = 0; i < kDeep; ++i) {
-                const int64_t g = first + i * 64 + lane, id0 = g * kEach - before;
                 if (first + i * 64 >= g1) break;
-#pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const uint32_t b = sizeof(E) == 2 ? (v[i][e >> 1] >> (16 * (e & 1))) & 0xFFFF : v[i][e];
-                    const bool there = g < g1 && id0 + e >= 0 && id0 + e < V;
-                    const float x = get(b) + 0.0f;         // (-0 as 0: they are equal)
-                    f(there ? (int)(id0 + e) : -1, there && x == x ? x : -INFINITY);
-                }
+                f((int)(first + i * 64) + lane, v[i]);
             }
         }
+    }
+    // f(id, x) for every element of them.
+    template <class F>
+    __device__ __forceinline__ void scan(int g0, int g1, int lane, F f) const {
+        groups_of(g0, g1, lane, [&](int g, const u32x4& v) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const float x = at(v, e);
+                f(g * kEach - before + e, x == x ? x : -INFINITY);
+            }
+        });
+    }
+    // the whole row, a part each wave
+    template <class F>
+    __device__ __forceinline__ void each(int wave, int lane, F f) const {
+        const int per = (groups + kWaves - 1) / kWaves, g0 = wave * per < groups ? wave * per : groups;
+        scan(g0, g0 + per < groups ? g0 + per : groups, lane, f);
     }
 };
 
 struct Shared {
-    double table[64];
-    uint32_t count[kBins];
+    double table[kTable];
     u64 weight[kBins];
+    uint32_t count[kBins];
+    float list[kList];
+    int ids[kList];
     u64 wave[2][kWaves];
     u64 found[4];
+    uint32_t listed;
 };
 
-__device__ inline u64 wave_add_u64(u64 v) {
+// The list, once it is complete.
+struct List {
+    const Shared& s;
+    int n;
+
+    template <class F>
+    __device__ __forceinline__ void each(int wave, int lane, F f) const {
+        for (int i = wave * 64 + lane; i < n; i += kThreads) f(s.ids[i], s.list[i]);
+    }
+};
+
+__device__ __forceinline__ u64 wave_add_u64(u64 v) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) v += dpp_step64(v, s);
     return (readlane64(v, 0) + readlane64(v, 16)) + (readlane64(v, 32) + readlane64(v, 48));
 }
-__device__ inline u64 wave_prefix_u64(u64 v, int lane) {
+__device__ __forceinline__ u64 wave_prefix_u64(u64 v, int lane) {
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
         const u64 o = (u64)(uint32_t)__shfl_up((int)(uint32_t)v, s) | (u64)(uint32_t)__shfl_up((int)(uint32_t)(v >> 32), s) << 32;
@@ -130,79 +190,97 @@ __device__ inline u64 wave_prefix_u64(u64 v, int lane) {
     }
     return v;
 }
+__device__ __forceinline__ u64 block_add(u64 v, Shared& s, int wave, int lane) {
+    v = wave_add_u64(v);
+    if (lane == 0) s.wave[0][wave] = v;
+    __syncthreads();
+    v = 0;
+    for (int i = 0; i < kWaves; ++i) v += s.wave[0][i];
+    __syncthreads();
+    return v;
+}
 
-// Where the order's beginning ends: at logits of this key, above which lie
-// `count` tokens of `weight` in all; `ties` tokens are at it.
+// Where a beginning of some order ends: at this key, above which lie `count`
+// tokens of `weight` in all; `ties` tokens are at it.
 struct Cut {
     uint32_t key;
     uint32_t count, ties;
     u64 weight;
 };
 
-// The first key, from the top, with which the tokens' number (or weight) reaches
-// `limit`, which the whole row reaches.
-template <class E, bool BY_WEIGHT>
-__device__ Cut descend(const Row<E>& row, const Weights& weights, u64 limit, Shared& s, int wave, int lane) {
-    const int tid = wave * 64 + lane, per = (row.groups + kWaves - 1) / kWaves;
-    const int g0 = wave * per, g1 = g0 + per < row.groups ? g0 + per : row.groups;
+// The bin, from the top, with which the tokens' number (or weight) reaches
+// `limit`, which all of them do; counts and weights before it go to `cut`.
+template <bool BY_WEIGHT>
+__device__ __forceinline__ int pick_bin(int bins, u64 limit, Cut& cut, Shared& s, int wave, int lane) {
+    // thread t's bins are the t-th pair from the top
+    const int b0 = bins - 1 - 2 * (wave * 64 + lane), b1 = b0 - 1;
+    const u64 c0 = b0 >= 0 ? s.count[b0] : 0, c1 = b1 >= 0 ? s.count[b1] : 0;
+    const u64 w0 = BY_WEIGHT && b0 >= 0 ? s.weight[b0] : 0, w1 = BY_WEIGHT && b1 >= 0 ? s.weight[b1] : 0;
+    const u64 cp = wave_prefix_u64(c0 + c1, lane), wp = BY_WEIGHT ? wave_prefix_u64(w0 + w1, lane) : 0;
+    if (lane == 63) {
+        s.wave[0][wave] = cp;
+        s.wave[1][wave] = wp;
+    }
+    __syncthreads();
+    u64 cx = cut.count + cp - c0 - c1, wx = cut.weight + wp - w0 - w1;     // before this thread's bins
+    for (int i = 0; i < wave; ++i) {
+        cx += s.wave[0][i];
+        wx += s.wave[1][i];
+    }
+    const u64 m0 = BY_WEIGHT ? wx : cx, m1 = m0 + (BY_WEIGHT ? w0 : c0), m2 = m1 + (BY_WEIGHT ? w1 : c1);
+    const bool in0 = m0 < limit && m1 >= limit, in1 = m1 < limit && m2 >= limit;
+    if (in0 || in1) {
+        s.found[0] = (u64)(in0 ? b0 : b1);
+        s.found[1] = in0 ? cx : cx + c0;
+        s.found[2] = in0 ? wx : wx + w0;
+        s.found[3] = in0 ? c0 : c1;
+    }
+    __syncthreads();
+    cut.count = (uint32_t)s.found[1];
+    cut.weight = s.found[2];
+    cut.ties = (uint32_t)s.found[3];
+    return (int)s.found[0] & (kBins - 1);
+}
+
+__device__ __forceinline__ void clear_bins(int bins, Shared& s, int tid) {
+    for (int i = tid; i < bins; i += kThreads) {
+        s.count[i] = 0;
+        s.weight[i] = 0;
+    }
+    __syncthreads();
+}
+
+// The first key, from the top, with which the number (or weight) of the tokens
+// of `from` that weigh something reaches `limit`, which all of them do.
+// of(id, x, key, weight) says which those are, and their keys, whose bits from
+// `bits` on are those of `prefix`.
+template <bool BY_WEIGHT, class Source, class Of>
+__device__ __forceinline__ Cut descend(const Source& from, u64 limit, uint32_t prefix, int bits, Of of, Shared& s, int wave, int lane) {
     Cut cut = {0, 0, 0, 0};
-    int above = 32;                                        // the bits at and above this are settled
-    for (int level = 0; level < 3; ++level) {
-        const int bits = level == 2 ? 10 : 11, shift = above - bits, bins = 1 << bits;
-        for (int i = tid; i < kBins; i += kThreads) {
-            s.count[i] = 0;
-            s.weight[i] = 0;
-        }
-        __syncthreads();
-        row.scan(g0, g1, lane, [&](int, float x) {
-            if (x == -INFINITY) return;
-            const uint32_t k = key_of(x);
-            if (above < 32 && (k >> above) != (cut.key >> above)) return;
-            const int bin = (k >> shift) & (bins - 1);
+    if (bits < 32) cut.key = prefix >> bits << bits;
+    while (bits > 0) {
+        const int take = bits < kBits ? bits : kBits, shift = bits - take;
+        clear_bins(1 << take, s, wave * 64 + lane);
+        from.each(wave, lane, [&](int id, float x) {
+            uint32_t k;
+            u64 w;
+            if (!of(id, x, k, w) || (bits < 32 && (k >> bits) != (cut.key >> bits))) return;
+            const int bin = (k >> shift) & ((1 << take) - 1);
             atomicAdd(&s.count[bin], 1u);
-            const u64 w = weights(x);
-            if (w) atomicAdd(&s.weight[bin], w);
+            if (BY_WEIGHT && w) atomicAdd(&s.weight[bin], w);
         });
         __syncthreads();
-        // thread t's bins are the t-th pair from the top
-        const int b0 = bins - 1 - 2 * tid, b1 = b0 - 1;
-        const u64 c0 = b0 >= 0 ? s.count[b0] : 0, c1 = b1 >= 0 ? s.count[b1] : 0;
-        const u64 w0 = b0 >= 0 ? s.weight[b0] : 0, w1 = b1 >= 0 ? s.weight[b1] : 0;
-        const u64 cp = wave_prefix_u64(c0 + c1, lane), wp = wave_prefix_u64(w0 + w1, lane);
-        if (lane == 63) {
-            s.wave[0][wave] = cp;
-            s.wave[1][wave] = wp;
-        }
-        __syncthreads();
-        u64 cb = cut.count, wb = cut.weight;
-        for (int i = 0; i < wave; ++i) {
-            cb += s.wave[0][i];
-            wb += s.wave[1][i];
-        }
-        const u64 cx = cb + cp - c0 - c1, wx = wb + wp - w0 - w1;      // before this thread's bins
-        const u64 m0 = BY_WEIGHT ? wx : cx, m1 = BY_WEIGHT ? wx + w0 : cx + c0, m2 = BY_WEIGHT ? wx + w0 + w1 : cx + c0 + c1;
-        const bool in0 = m0 < limit && m1 >= limit, in1 = m1 < limit && m2 >= limit;
-        if (in0 || in1) {
-            s.found[0] = (u64)(in0 ? b0 : b1);
-            s.found[1] = in0 ? cx : cx + c0;
-            s.found[2] = in0 ? wx : wx + w0;
-            s.found[3] = in0 ? c0 : c1;
-        }
-        __syncthreads();
-        cut.key |= (uint32_t)s.found[0] << shift;
-        cut.count = (uint32_t)s.found[1];
-        cut.weight = s.found[2];
-        cut.ties = (uint32_t)s.found[3];
-        above = shift;
+        cut.key |= (uint32_t)pick_bin<BY_WEIGHT>(1 << take, limit, cut, s, wave, lane) << shift;
+        bits = shift;
         __syncthreads();
     }
     return cut;
 }
 
-// The first id with which the sum of m(id, x) passes `target`, which the whole
-// row does, and the total; target = of(total).
+// The first id with which the sum of m(id, x) over the row passes `target`,
+// which all of it does; target = of(the sum of all).
 template <class E, class M, class Of>
-__device__ int locate(const Row<E>& row, M m, Of of, u64* total, Shared& s, int wave, int lane) {
+__device__ __forceinline__ int locate(const Row<E>& row, M m, Of of, u64* total, Shared& s, int wave, int lane) {
     int g0 = 0, g1 = row.groups;
     u64 before = 0, target = 0;
     for (int level = 0; level < 3; ++level) {
@@ -243,7 +321,7 @@ __device__ int locate(const Row<E>& row, M m, Of of, u64* total, Shared& s, int 
         u64 sofar = before + readlane64(upto, l) - readlane64(sum, l);
         row.scan(g + l, g + l + 1, lane, [&](int id, float x) {
             const u64 w = m(id, x);                        // (lane 0's: the others have no group)
-            if (lane == 0 && found < 0 && id >= 0) {
+            if (lane == 0 && found < 0 && w > 0) {
                 sofar += w;
                 if (sofar > target) found = id;
             }
@@ -253,6 +331,150 @@ __device__ int locate(const Row<E>& row, M m, Of of, u64* total, Shared& s, int 
     return found;
 }
 
+// What a request asks for, and the row's own measures.
+struct Ask {
+    int top_k;                     // 0: off
+    float top_p;                   // >= 1: off
+    u64 least;                     // weight that min_p asks for (0: off)
+    double u;
+    int first;                     // the largest logit's token, which always stays
+    int id_bits;
+    Weights weights;
+};
+
+__device__ __forceinline__ u64 limit_of(float top_p, u64 total) {
+    const double part = ceil((double)top_p * (double)total);
+    const u64 limit = part >= 1 ? (u64)part : 1;
+    return limit < total ? limit : total;
+}
+__device__ __forceinline__ u64 target_of(double u, u64 total) {
+    const double t = u * (double)total;
+    return t >= 1 ? (t < (double)total ? (u64)t : total - 1) : 0;
+}
+
+// What stays: all tokens above `value`, and those at it up to id `last`.
+struct Edge {
+    float value;
+    int last;
+};
+
+// The edge of top_k and top_p among the tokens of `from`, which hold everything
+// that top_k leaves, or, without it, everything at the edge of top_p and what is
+// above it but for tokens that weigh `above`, of all that weigh `total`.  Their
+// keys have the bits of `prefix` from `bits` on.
+template <class E, class Source>
+__device__ __forceinline__ Edge find_edge(const Source& from, const Ask& ask, int count, u64 total, u64 above, uint32_t prefix, int bits,
+                          Shared& s, int wave, int lane) {
+    // keys of a 16-bit type are told apart by their upper half
+    constexpr int kLow = sizeof(E) == 2 ? 16 : 0;
+    const auto by_logit = [&](int, float x, uint32_t& k, u64& w) {
+        if (x == -INFINITY) return false;
+        k = key_of(x) >> kLow;
+        return true;
+    };
+    const auto full = [&](uint32_t k) { return sizeof(E) == 2 ? (k & 0x8000u ? k << 16 : k << 16 | 0xFFFFu) : k; };
+    bits = bits > kLow ? bits - kLow : 1;
+    prefix >>= kLow;
+    Edge edge = {-INFINITY, INT32_MAX};
+    u64 tied = 0;
+    bool part = false;                                     // only `tied` of the tokens at the edge stay
+    if (ask.top_k > 0 && count > ask.top_k) {
+        const Cut c = descend<false>(from, (u64)ask.top_k, prefix, bits, by_logit, s, wave, lane);
+        edge.value = value_of(full(c.key));
+        tied = (u64)ask.top_k - c.count;
+        part = tied < c.ties;
+    }
+    if (ask.top_p < 1) {
+        if (ask.top_k > 0) {                               // of what top_k leaves
+            u64 sum = 0;
+            from.each(wave, lane, [&](int, float x) {
+                const u64 w = ask.weights(x);
+                sum += x > edge.value || (x == edge.value && !part) ? w : 0;
+            });
+            total = block_add(sum, s, wave, lane);
+            if (part) total += tied * ask.weights(edge.value);
+        }
+        const u64 limit = limit_of(ask.top_p, total) - above;
+        const Cut c = descend<true>(from, limit, prefix, bits, [&](int id, float x, uint32_t& k, u64& w) {
+            w = ask.weights(x);
+            return by_logit(id, x, k, w);
+        }, s, wave, lane);
+        const float value = value_of(full(c.key));
+        const u64 w = ask.weights(value), need = w ? (limit - c.weight + w - 1) / w : 0;
+        if (value == edge.value && part) {
+            tied = need < tied ? need : tied;
+        } else {
+            tied = need < c.ties ? need : c.ties;
+            part = tied < c.ties;
+        }
+        edge.value = value;
+    }
+    if (part) {
+        const Cut c = descend<false>(from, tied, 0, ask.id_bits, [&](int id, float x, uint32_t& k, u64&) {
+            k = ((1u << ask.id_bits) - 1) - (uint32_t)id;  // the lowest ids on top
+            return x == edge.value;
+        }, s, wave, lane);
+        edge.last = (int)(((1u << ask.id_bits) - 1) - c.key);
+    }
+    return edge;
+}
+
+__device__ __forceinline__ u64 kept_weight(const Ask& ask, const Edge& edge, int id, float x) {
+    const u64 w = ask.weights(x);
+    const bool stays = (x > edge.value || (x == edge.value && id <= edge.last)) && (w >= ask.least || id == ask.first);
+    return stays ? w : 0;
+}
+
+// The token drawn from the list, which holds all that stay.
+__device__ __forceinline__ int draw_listed(const List& list, const Ask& ask, const Edge& edge, u64* total, Shared& s, int wave, int lane) {
+    u64 sum = 0;
+    list.each(wave, lane, [&](int id, float x) { sum += kept_weight(ask, edge, id, x); });
+    *total = block_add(sum, s, wave, lane);
+    if (*total == 0) return ask.first;
+    const Cut c = descend<true>(list, target_of(ask.u, *total) + 1, 0, ask.id_bits, [&](int id, float x, uint32_t& k, u64& w) {
+        w = kept_weight(ask, edge, id, x);
+        k = ((1u << ask.id_bits) - 1) - (uint32_t)id;
+        return w > 0;
+    }, s, wave, lane);
+    return (int)(((1u << ask.id_bits) - 1) - c.key);
+}
+
+// All tokens for which wanted(x) into the list; whether they fit.  wanted sees
+// every logit on the way, -inf and NaN among them.
+template <class E, class F>
+__device__ __forceinline__ bool make_list(const Row<E>& row, F wanted, Shared& s, int wave, int lane) {
+    if (wave == 0 && lane == 0) s.listed = 0;
+    __syncthreads();
+    const int per = (row.groups + kWaves - 1) / kWaves, g0 = wave * per < row.groups ? wave * per : row.groups;
+    row.groups_of(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < Row<E>::kEach; ++e) mine |= wanted(Row<E>::at(v, e)) ? 1u << e : 0u;
+        if (mine) {
+            uint32_t to = atomicAdd(&s.listed, (uint32_t)__popc(mine));
+#pragma unroll
+            for (int e = 0; e < Row<E>::kEach; ++e)
+                if (mine >> e & 1) {
+                    if (to < kList) {
+                        s.list[to] = Row<E>::at(v, e);
+                        s.ids[to] = g * Row<E>::kEach - row.before + e;
+                    }
+                    ++to;
+                }
+        }
+    });
+    __syncthreads();
+    return s.listed <= kList;
+}
+
+// Each thread's largest logit.
+struct Largest {
+    float mine;
+
+    template <class F>
+    __device__ __forceinline__ void each(int, int, F f) const { f(0, mine); }
+};
+
 template <class E>
 __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shift) {
     __shared__ Shared s;
@@ -261,112 +483,144 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
     const int b = (int)(at / a.rows), r = (int)(at - (int64_t)b * a.rows);
     if (r >= a.lead && a.n_nodes && r >= a.lead + a.n_nodes[b]) return;
     const Row<E> row(a.logits, at, a.V);
-    const int per = (row.groups + kWaves - 1) / kWaves;
-    if (tid < 64) s.table[tid] = exp2(tid / 64.0);
+    if (tid < kTable) s.table[tid] = ldexp(exp2((double)tid / kTable), shift);
 
-    // the largest logit and its first id
-    u64 best = 0;
-    row.scan(wave * per, (wave + 1) * per < row.groups ? (wave + 1) * per : row.groups, lane, [&](int id, float x) {
-        if (x == -INFINITY) return;
-        const u64 k = (u64)key_of(x) << 32 | (uint32_t)~id;
-        best = k > best ? k : best;
+    // the largest logit and its first id: each lane's largest, and where it was met first
+    const int per = (row.groups + kWaves - 1) / kWaves, g0 = wave * per < row.groups ? wave * per : row.groups;
+    float mine = -INFINITY;
+    int where = 0;
+    row.groups_of(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
+        float x = Row<E>::at(v, 0);
+#pragma unroll
+        for (int e = 1; e < Row<E>::kEach; ++e) x = fmaxf(x, Row<E>::at(v, e));
+        where = x > mine ? g : where;
+        mine = x > mine ? x : mine;
     });
-    best = wave_max_u64(best);
-    if (lane == 0) s.wave[0][wave] = best;
+    const float wave_top = wave_max_f32(mine);
+    if (lane == 0) s.wave[0][wave] = key_of(wave_top);
+    if (tid == 0) s.found[0] = (u64)a.V;
     __syncthreads();
-    for (int i = 0; i < kWaves; ++i) best = s.wave[0][i] > best ? s.wave[0][i] : best;
-    __syncthreads();
+    u64 top_key = 0;
+    for (int i = 0; i < kWaves; ++i) top_key = s.wave[0][i] > top_key ? s.wave[0][i] : top_key;
+    const float top = value_of((uint32_t)top_key);
     const float temperature = a.temperature ? a.temperature[b] : 1.0f;
-    if (best == 0 || !(temperature > 0)) {
+    if (top == -INFINITY) {
         if (tid == 0) {
-            a.tokens[at] = best == 0 ? -1 : (int)~(uint32_t)best;
-            if (a.logp) a.logp[at] = best == 0 ? -INFINITY : 0.0f;
+            a.tokens[at] = -1;
+            if (a.logp) a.logp[at] = -INFINITY;
         }
         return;
     }
-    const int first = (int)~(uint32_t)best;
-    Weights weights;
-    weights.top = (double)value_of((uint32_t)(best >> 32));
-    weights.rate = 64 * 1.4426950408889634074 / (double)temperature;
-    weights.shift = shift;
-    weights.least = -64.0 * (shift + 2);
-    weights.table = s.table;
-
-    // the cut: all tokens above `key`, and those at it up to `last`
+    if (mine == top) {
+        const u32x4 v = row.load(where);
+        int e0 = 0;
+#pragma unroll
+        for (int e = Row<E>::kEach - 1; e >= 0; --e) e0 = Row<E>::at(v, e) == top ? e : e0;
+        atomicMin(&s.found[0], (u64)(where * (int64_t)Row<E>::kEach - row.before + e0));
+    }
+    __syncthreads();
+    Ask ask;
+    ask.first = (int)s.found[0];
+    if (!(temperature > 0)) {
+        if (tid == 0) {
+            a.tokens[at] = ask.first;
+            if (a.logp) a.logp[at] = 0.0f;
+        }
+        return;
+    }
     const int top_k = a.top_k ? a.top_k[b] : 0;
-    const float top_p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f;
-    const u64 least = min_p > 0 ? (u64)ceil(ldexp((double)(min_p < 2.0f ? min_p : 2.0f), shift)) : 0;
-    uint32_t key = 0;                                      // (below every finite logit's)
-    int last = a.V;
-    bool cut_ties = false;
-    u64 tied = 0;
-    u64 total = 0;
-    if (top_k > 0 && top_k < a.V) {
-        u64 there = 0;
-        // fewer finite logits than that: nothing to cut
-        row.scan(wave * per, (wave + 1) * per < row.groups ? (wave + 1) * per : row.groups, lane,
-                 [&](int, float x) { there += x != -INFINITY; });
-        there = wave_add_u64(there);
-        if (lane == 0) s.wave[0][wave] = there;
-        __syncthreads();
-        there = 0;
-        for (int i = 0; i < kWaves; ++i) there += s.wave[0][i];
-        __syncthreads();
-        if (there > (u64)top_k) {
-            const Cut c = descend<E, false>(row, weights, (u64)top_k, s, wave, lane);
-            key = c.key;
-            tied = (u64)top_k - c.count;
-            cut_ties = tied < c.ties;
-            total = c.weight + tied * weights(value_of(key));
+    const float min_p = a.min_p ? a.min_p[b] : 0.0f;
+    ask.top_k = top_k > 0 && top_k < a.V ? top_k : 0;
+    ask.top_p = a.top_p ? a.top_p[b] : 1.0f;
+    ask.least = min_p > 0 ? (u64)ceil(ldexp((double)(min_p < 2.0f ? min_p : 2.0f), shift)) : 0;
+    ask.u = a.u[at];
+    ask.id_bits = 32 - __clz(a.V - 1 > 0 ? a.V - 1 : 1);
+    ask.weights = {(double)top, kTable * 1.4426950408889634074 / (double)temperature, -(double)kTable * (shift + 2), (Table)s.table};
+    const bool by_p = ask.top_p < 1;
+
+    Edge edge = {-INFINITY, INT32_MAX};
+    u64 total = 0, all = 0, above = 0;
+    int token = -1, n = 0;
+    // what the list holds: nothing, all that stays, or the tokens around the edge
+    enum { kNothing, kAll, kEdge } holds = kNothing;
+    uint32_t low = 0;                                      // the smallest key there
+    if (ask.top_k <= kMostK && (by_p || ask.top_k > 0)) {
+        // the logit that j threads' largest reach (its upper 22 bits)
+        const u64 j = ask.top_k > 0 ? ask.top_k : kForP;
+        const Largest largest{mine};
+        float limit = -FLT_MAX;
+        if (block_add(mine > -INFINITY, s, wave, lane) >= j) {
+            const Cut c = descend<false>(largest, j, 0, 22, [&](int, float x, uint32_t& k, u64&) {
+                k = key_of(x) >> 10;
+                return x > -INFINITY;
+            }, s, wave, lane);
+            limit = value_of(c.key << 10);
         }
-    }
-    if (top_p < 1) {
-        if (key == 0) {
-            row.scan(wave * per, (wave + 1) * per < row.groups ? (wave + 1) * per : row.groups, lane,
-                     [&](int, float x) { total += weights(x); });
-            total = wave_add_u64(total);
-            if (lane == 0) s.wave[0][wave] = total;
-            __syncthreads();
-            total = 0;
-            for (int i = 0; i < kWaves; ++i) total += s.wave[0][i];
-            __syncthreads();
-        }
-        const double part = ceil((double)top_p * (double)total);
-        const u64 limit = part >= 1 ? (u64)part : 1;
-        const Cut c = descend<E, true>(row, weights, limit < total ? limit : total, s, wave, lane);
-        const u64 w = weights(value_of(c.key)), need = w ? (limit - c.weight + w - 1) / w : 0;
-        const uint32_t before = key;
-        key = c.key;
-        if (before == key && cut_ties) {
-            tied = need < tied ? need : tied;
+        low = key_of(limit);
+        if (ask.top_k > 0) {
+            if (make_list(row, [&](float x) { return x >= limit; }, s, wave, lane)) holds = kAll;
+            n = (int)s.listed;
         } else {
-            tied = need < c.ties ? need : c.ties;
-            cut_ties = tied < c.ties;
+            // bins over the logits that weigh anything, the largest in the last
+            const float width = (kBins - 1) / ((shift + 1) * 0.6931472f * temperature);
+            const auto bin_of = [&](float x) { return kBins - 1 - (int)fminf((top - x) * width, (float)(kBins - 1)); };
+            clear_bins(kBins, s, tid);
+            const bool fits = make_list(row, [&](float x) {
+                const u64 w = ask.weights(x);
+                if (w) atomicAdd(&s.weight[bin_of(x)], w);
+                return x >= limit;
+            }, s, wave, lane);
+            n = (int)s.listed;
+            for (int i = tid; i < kBins; i += kThreads) all += s.weight[i];
+            all = block_add(all, s, wave, lane);
+            Cut c = {0, 0, 0, 0};
+            const int bin = pick_bin<true>(kBins, limit_of(ask.top_p, all), c, s, wave, lane);
+            __syncthreads();
+            if (fits && bin_of(limit) < bin) {             // the list holds the cut and all above
+                holds = kAll;
+            } else if (make_list(row, [&](float x) { return bin_of(x) == bin && x > -INFINITY && ask.weights(x) > 0; }, s, wave, lane)) {
+                holds = kEdge;
+                n = (int)s.listed;
+                above = c.weight;
+                low = 0;
+            }
+        }
+    } else if (ask.top_k == 0 && ask.least > 0) {
+        // what min_p leaves, and a little more for the roundings of this limit
+        const double below = (double)temperature * fmin(log((double)min_p), 0.0);
+        const float limit = fmaxf((float)((double)top + below - 1e-6 * (fabs((double)top) - below) - 1e-37), -FLT_MAX);
+        if (make_list(row, [&](float x) { return x >= limit; }, s, wave, lane)) holds = kAll;
+        n = (int)s.listed;
+    }
+    const List list{s, n};
+    if (by_p || ask.top_k > 0) {
+        if (holds != kNothing) {
+            const int bits = 32 - __clz((low ^ (uint32_t)top_key) | 1);
+            edge = find_edge<E>(list, ask, n, all, above, low, bits, s, wave, lane);
+        } else {
+            u64 there = 0;
+            all = 0;
+            row.each(wave, lane, [&](int, float x) {
+                there += x != -INFINITY;
+                all += ask.weights(x);
+            });
+            there = block_add(there, s, wave, lane);
+            all = block_add(all, s, wave, lane);
+            edge = find_edge<E>(row, ask, (int)there, all, 0, 0, 32, s, wave, lane);
         }
     }
-    if (cut_ties) {
-        u64 n;
-        const uint32_t k = key;
-        const u64 want = tied;
-        last = locate(row, [&](int, float x) { return (u64)(key_of(x) == k); }, [&](u64) { return want - 1; }, &n, s, wave, lane);
+    if (holds == kAll) {
+        token = draw_listed(list, ask, edge, &total, s, wave, lane);
+    } else {
+        token = locate(row, [&](int id, float x) { return kept_weight(ask, edge, id, x); },
+                       [&](u64 sum) { return target_of(ask.u, sum); }, &total, s, wave, lane);
     }
-    const auto kept = [&](int id, float x) -> u64 {
-        if (x == -INFINITY) return 0;
-        const uint32_t k = key_of(x);
-        if (k < key || (k == key && id > last)) return 0;
-        const u64 w = weights(x);
-        return w >= least || id == first ? w : 0;
-    };
-    const double u = a.u[at];
-    const int token = locate(row, kept, [&](u64 all) {
-        const double t = u * (double)all;
-        return t >= 1 ? (t < (double)all ? (u64)t : all - 1) : 0;
-    }, &total, s, wave, lane);
     if (tid == 0) {
-        a.tokens[at] = token < 0 ? first : token;
+        token = token < 0 || token >= a.V ? ask.first : token;
+        a.tokens[at] = token;
         if (a.logp) {
-            const float x = Row<E>::get(((const E*)a.logits)[at * a.V + (token < 0 ? first : token)]);
-            a.logp[at] = (float)(((double)x - weights.top) / (double)temperature - log(ldexp((double)total, -shift)));
+            const float x = Row<E>::get(((const E*)a.logits)[at * a.V + token]);
+            a.logp[at] = (float)(((double)x - (double)top) / (double)temperature - log(ldexp((double)total, -shift)));
         }
     }
 }
