@@ -42,6 +42,7 @@ constexpr int kList = 6144;        // tokens of the list
 constexpr int kMostK = 1000;
 constexpr int kForP = 896;
 constexpr int kTable = 64;
+constexpr int kShort = 256;        // tokens of a list whose pairs are compared
 
 // Bits whose order is that of the values (no NaN; -0 and 0 are one).
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -64,7 +65,7 @@ struct Weights {
     __device__ __forceinline__ u64 operator()(float x) const {
         constexpr double kRound = 6755399441055744.0, kOne = 0.69314718055994530942 / kTable;
         constexpr double k2 = kOne * kOne / 2, k3 = k2 * kOne / 3, k4 = k3 * kOne / 4;
-        const double t = fmax(((double)x - top) * rate, least);            // (NaN, as inf - inf: the least)
+        const double y = ((double)x - top) * rate, t = y > least ? y : least;      // (NaN, as inf - inf: the least)
         const double r = t + kRound, f = t - (r - kRound);
         const int i = (int)(uint32_t)__double_as_longlong(r);
         const u64 e = (u64)__double_as_longlong(table[i & (kTable - 1)]) + ((u64)(uint32_t)(i >> 6) << 52);
@@ -182,19 +183,26 @@ __device__ __forceinline__ u64 wave_add_u64(u64 v) {
     for (int s = 0; s < 4; ++s) v += dpp_step64(v, s);
     return (readlane64(v, 0) + readlane64(v, 16)) + (readlane64(v, 32) + readlane64(v, 48));
 }
+template <int CTRL>
+__device__ __forceinline__ u64 shifted(u64 v) {            // within the rows of 16 lanes; 0 from outside
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xF, 0xF, false);
+    return (u64)hi << 32 | lo;
+}
 __device__ __forceinline__ u64 wave_prefix_u64(u64 v, int lane) {
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const u64 o = (u64)(uint32_t)__shfl_up((int)(uint32_t)v, s) | (u64)(uint32_t)__shfl_up((int)(uint32_t)(v >> 32), s) << 32;
-        if (lane >= s) v += o;
-    }
-    return v;
+    v += shifted<0x111>(v);                                // row_shr:1, 2, 4, 8
+    v += shifted<0x112>(v);
+    v += shifted<0x114>(v);
+    v += shifted<0x118>(v);
+    const u64 a = readlane64(v, 15), b = readlane64(v, 31), c = readlane64(v, 47);
+    return v + (lane >= 16 ? a : 0) + (lane >= 32 ? b : 0) + (lane >= 48 ? c : 0);
 }
 __device__ __forceinline__ u64 block_add(u64 v, Shared& s, int wave, int lane) {
     v = wave_add_u64(v);
     if (lane == 0) s.wave[0][wave] = v;
     __syncthreads();
     v = 0;
+#pragma unroll
     for (int i = 0; i < kWaves; ++i) v += s.wave[0][i];
     __syncthreads();
     return v;
@@ -223,9 +231,10 @@ __device__ __forceinline__ int pick_bin(int bins, u64 limit, Cut& cut, Shared& s
     }
     __syncthreads();
     u64 cx = cut.count + cp - c0 - c1, wx = cut.weight + wp - w0 - w1;     // before this thread's bins
-    for (int i = 0; i < wave; ++i) {
-        cx += s.wave[0][i];
-        wx += s.wave[1][i];
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i) {
+        cx += i < wave ? s.wave[0][i] : 0;
+        if (BY_WEIGHT) wx += i < wave ? s.wave[1][i] : 0;
     }
     const u64 m0 = BY_WEIGHT ? wx : cx, m1 = m0 + (BY_WEIGHT ? w0 : c0), m2 = m1 + (BY_WEIGHT ? w1 : c1);
     const bool in0 = m0 < limit && m1 >= limit, in1 = m1 < limit && m2 >= limit;
@@ -439,6 +448,54 @@ __device__ __forceinline__ int draw_listed(const List& list, const Ask& ask, con
     return (int)(((1u << ask.id_bits) - 1) - c.key);
 }
 
+// The same as find_edge and draw_listed, from a short list that holds all that
+// stays: every pair of its tokens is compared, 1024 / 256 threads a token.
+__device__ __forceinline__ int draw_short(const List& list, const Ask& ask, u64* total, Shared& s, int wave, int lane) {
+    constexpr int kParts = kThreads / kShort;
+    const int tid = wave * 64 + lane, i = tid / kParts, part = tid % kParts;
+    const bool mine = i < list.n;
+    const float x = mine ? s.list[i] : -INFINITY;
+    const int id = mine ? s.ids[i] : INT32_MAX;
+    const u64 w = mine ? ask.weights(x) : 0;
+    if (mine && part == 0) s.weight[i] = w;
+    __syncthreads();
+    // those before it in the order: their number and weight
+    uint32_t rank = 0;
+    u64 before = 0;
+    for (int j = part; j < list.n; j += kParts) {
+        const float y = s.list[j];
+        const bool first = y > x || (y == x && s.ids[j] < id);
+        rank += first;
+        before += first ? s.weight[j] : 0;
+    }
+#pragma unroll
+    for (int d = 1; d < kParts; d <<= 1) {
+        rank += __shfl_xor((int)rank, d);
+        before += (u64)(uint32_t)__shfl_xor((int)(uint32_t)before, d) | (u64)(uint32_t)__shfl_xor((int)(uint32_t)(before >> 32), d) << 32;
+    }
+    bool stays = mine && (ask.top_k == 0 || rank < (uint32_t)ask.top_k);
+    if (ask.top_p < 1) {
+        const u64 all = block_add(stays && part == 0 ? w : 0, s, wave, lane);
+        stays = stays && before < limit_of(ask.top_p, all);
+    }
+    stays = stays && (w >= ask.least || id == ask.first);
+    const u64 kept = stays ? w : 0;
+    *total = block_add(part == 0 ? kept : 0, s, wave, lane);
+    if (*total == 0) return ask.first;
+    if (mine && part == 0) s.weight[i] = kept;
+    __syncthreads();
+    // those before it by id
+    u64 upto = 0;
+    for (int j = part; j < list.n; j += kParts) upto += s.ids[j] < id ? s.weight[j] : 0;
+#pragma unroll
+    for (int d = 1; d < kParts; d <<= 1)
+        upto += (u64)(uint32_t)__shfl_xor((int)(uint32_t)upto, d) | (u64)(uint32_t)__shfl_xor((int)(uint32_t)(upto >> 32), d) << 32;
+    const u64 target = target_of(ask.u, *total);
+    if (part == 0 && upto <= target && target < upto + kept) s.found[0] = (u64)id;
+    __syncthreads();
+    return (int)s.found[0];
+}
+
 // All tokens for which wanted(x) into the list; whether they fit.  wanted sees
 // every logit on the way, -inf and NaN among them.
 template <class E, class F>
@@ -593,7 +650,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
         n = (int)s.listed;
     }
     const List list{s, n};
-    if (by_p || ask.top_k > 0) {
+    if (holds == kAll && n <= kShort && !(by_p && ask.top_k == 0)) {
+        // (top_p alone goes by the weight of the whole row)
+        token = draw_short(list, ask, &total, s, wave, lane);
+    } else if (by_p || ask.top_k > 0) {
         if (holds != kNothing) {
             const int bits = 32 - __clz((low ^ (uint32_t)top_key) | 1);
             edge = find_edge<E>(list, ask, n, all, above, low, bits, s, wave, lane);
@@ -609,7 +669,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
             edge = find_edge<E>(row, ask, (int)there, all, 0, 0, 32, s, wave, lane);
         }
     }
-    if (holds == kAll) {
+    if (token >= 0) {
+    } else if (holds == kAll) {
         token = draw_listed(list, ask, edge, &total, s, wave, lane);
     } else {
         token = locate(row, [&](int id, float x) { return kept_weight(ask, edge, id, x); },
