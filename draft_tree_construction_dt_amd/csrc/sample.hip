@@ -24,6 +24,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "pass.h"
 #include "wave.h"
 
@@ -155,6 +157,18 @@ struct Row {
         scan(g0, g0 + per < groups ? g0 + per : groups, lane, f);
     }
 };
+
+// Weights of the 16-bit type's values, a word each: 19 binades of magnitudes (of
+// 128 values) that reach past every logit that weighs anything, positive ones and,
+// 32 KiB on, negative ones; and how often they occur.
+constexpr int kMagnitudes = 19 * 128;
+struct Values {
+    u64 weight[4096 + kMagnitudes];
+    uint32_t count[4096 + kMagnitudes];
+    u64 tiny_weight;               // smaller magnitudes than those
+    uint32_t tiny_count;
+};
+struct NoValues {};
 
 struct Shared {
     double table[kTable];
@@ -496,6 +510,169 @@ __device__ __forceinline__ int draw_short(const List& list, const Ask& ask, u64*
     return (int)s.found[0];
 }
 
+typedef __attribute__((address_space(3))) char* Lds;
+
+// Weights of 16-bit logits by their bits: a read of LDS in place of some thirty
+// instructions.
+struct ByValue {
+    Values& v;
+    int base;                      // bits of the smallest magnitude there
+
+    // exponents up to one past those of the largest logit and of the smallest that
+    // weighs anything
+    __device__ __forceinline__ ByValue(Values& v_, float top, float low) : v(v_) {
+        const uint32_t m = __float_as_uint(fmaxf(fabsf(top), fabsf(low))) >> 23;   // (inf: 255)
+        const int first = (int)m + 1 - 18;
+        base = (first < 0 ? 0 : (first > 237 ? 237 : first)) << 7;
+    }
+    __device__ __forceinline__ float value(int i, int negative) const {
+        return __uint_as_float((uint32_t)(base + i + (negative ? 0x8000 : 0)) << 16);
+    }
+    // (below 0: a tiny one; past the end, NaN and infinities: the last, which weighs nothing)
+    __device__ __forceinline__ int index(float x) const {
+        const int i = (int)((__float_as_uint(x) >> 16) & 0x7FFF) - base;
+        return i < kMagnitudes - 1 ? i : kMagnitudes - 1;
+    }
+    __device__ __forceinline__ u64 weight(float x, int i) const {
+        const uint32_t at = (uint32_t)(i < 0 ? 0 : i) * 8 + ((__float_as_uint(x) >> 16) & 0x8000);
+        return *(__attribute__((address_space(3))) const u64*)((Lds)v.weight + at);
+    }
+    __device__ __forceinline__ void count(float x, int i) const {
+        atomicAdd((uint32_t*)((char*)v.count + i * 4 + ((__float_as_uint(x) >> 17) & 0x4000)), 1u);
+    }
+    __device__ __forceinline__ void fill(const Ask& ask, const Edge& edge, int tid) const {
+        for (int i = tid; i < kMagnitudes; i += kThreads)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float x = value(i, n);
+                const bool stays = i < kMagnitudes - 1 && x <= (float)ask.weights.top && x >= edge.value;
+                const u64 w = stays ? ask.weights(x) : 0;
+                v.weight[n * 4096 + i] = w >= ask.least ? w : 0;
+            }
+        __syncthreads();
+    }
+    // the order's beginning that reaches `limit` in number (or weight): its last
+    // value's, false where that is a tiny one
+    template <bool BY_WEIGHT>
+    __device__ __forceinline__ bool cut(u64 limit, float& x, Cut& c, Shared& s, int wave, int lane) const {
+        // from the top: positive values, the tiny ones, negative values; five a thread
+        constexpr int kEach = 5;
+        static_assert(kEach * kThreads >= 2 * kMagnitudes + 1, "every value has a thread");
+        const int q0 = (wave * 64 + lane) * kEach;
+        const auto bin = [&](int q, u64& n, u64& w) {
+            n = w = 0;
+            if (q < kMagnitudes) {
+                n = v.count[kMagnitudes - 1 - q];
+                w = n * v.weight[kMagnitudes - 1 - q];
+            } else if (q == kMagnitudes) {
+                n = v.tiny_count;
+                w = v.tiny_weight;
+            } else if (q <= 2 * kMagnitudes) {
+                n = v.count[4096 + q - kMagnitudes - 1];
+                w = n * v.weight[4096 + q - kMagnitudes - 1];
+            }
+        };
+        u64 n = 0, w = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            u64 ni, wi;
+            bin(q0 + i, ni, wi);
+            n += ni;
+            w += wi;
+        }
+        const u64 np = wave_prefix_u64(n, lane), wp = wave_prefix_u64(w, lane);
+        if (lane == 63) {
+            s.wave[0][wave] = np;
+            s.wave[1][wave] = wp;
+        }
+        if (wave == 0 && lane == 0) s.found[0] = (u64)kMagnitudes;
+        __syncthreads();
+        u64 nx = np - n, wx = wp - w;
+#pragma unroll
+        for (int i = 0; i < kWaves - 1; ++i) {
+            nx += i < wave ? s.wave[0][i] : 0;
+            wx += i < wave ? s.wave[1][i] : 0;
+        }
+        for (int i = 0; i < kEach; ++i) {
+            u64 ni, wi;
+            bin(q0 + i, ni, wi);
+            const u64 m = BY_WEIGHT ? wx : nx;
+            if (m < limit && m + (BY_WEIGHT ? wi : ni) >= limit) {
+                s.found[0] = (u64)(q0 + i);
+                s.found[1] = nx;
+                s.found[2] = wx;
+                s.found[3] = ni;
+            }
+            nx += ni;
+            wx += wi;
+        }
+        __syncthreads();
+        const int q = (int)s.found[0];
+        c.count = (uint32_t)s.found[1];
+        c.weight = s.found[2];
+        c.ties = (uint32_t)s.found[3];
+        x = q < kMagnitudes ? value(kMagnitudes - 1 - q, 0) : value(q - kMagnitudes - 1, 1);
+        __syncthreads();
+        return q != kMagnitudes;
+    }
+};
+
+// Counts every value of the row.
+template <class E>
+__device__ __forceinline__ void count_values(const Row<E>& row, const ByValue& by, const Ask& ask, int wave, int lane) {
+    const int tid = wave * 64 + lane;
+    for (int i = tid; i < kMagnitudes; i += kThreads) by.v.count[i] = by.v.count[4096 + i] = 0;
+    if (tid == 0) {
+        by.v.tiny_weight = 0;
+        by.v.tiny_count = 0;
+    }
+    __syncthreads();
+    row.each(wave, lane, [&](int, float x) {
+        const int i = by.index(x);
+        if (i >= 0 && i < kMagnitudes - 1) by.count(x, i);
+        if (i < 0) {
+            atomicAdd(&by.v.tiny_count, 1u);
+            atomicAdd(&by.v.tiny_weight, ask.weights(x));
+        }
+    });
+    __syncthreads();
+}
+
+// The edge of top_k and top_p by the counted values; false where it is not to be
+// had so.  `tied` of the tokens at it stay, if `part`.
+__device__ __forceinline__ bool edge_by_value(const ByValue& by, const Ask& ask, Edge& edge, u64& tied, bool& part, Shared& s,
+                                              int wave, int lane) {
+    Cut c;
+    float x;
+    u64 total = 0, n = 0;
+    for (int i = wave * 64 + lane; i < kMagnitudes; i += kThreads) {
+        total += by.v.count[i] * by.v.weight[i] + by.v.count[4096 + i] * by.v.weight[4096 + i];
+        n += (u64)by.v.count[i] + by.v.count[4096 + i];
+    }
+    n = block_add(n, s, wave, lane) + by.v.tiny_count;
+    total = block_add(total, s, wave, lane) + by.v.tiny_weight;
+    if (ask.top_k > 0 && n > (u64)ask.top_k) {             // (what is not counted weighs nothing)
+        if (!by.cut<false>((u64)ask.top_k, x, c, s, wave, lane)) return false;
+        edge.value = x;
+        tied = (u64)ask.top_k - c.count;
+        part = tied < c.ties;
+        total = c.weight + tied * ask.weights(x);
+    }
+    if (ask.top_p < 1) {
+        const u64 limit = limit_of(ask.top_p, total);
+        if (!by.cut<true>(limit, x, c, s, wave, lane)) return false;
+        const u64 w = ask.weights(x), need = w ? (limit - c.weight + w - 1) / w : 0;
+        if (x == edge.value && part) {
+            tied = need < tied ? need : tied;
+        } else {
+            tied = need < c.ties ? need : c.ties;
+            part = tied < c.ties;
+        }
+        edge.value = x;
+    }
+    return true;
+}
+
 // All tokens for which wanted(x) into the list; whether they fit.  wanted sees
 // every logit on the way, -inf and NaN among them.
 template <class E, class F>
@@ -534,7 +711,10 @@ struct Largest {
 
 template <class E>
 __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shift) {
+    // 16-bit logits have few values: each one's weight is made once
+    constexpr bool kValues = sizeof(E) == 2;
     __shared__ Shared s;
+    __shared__ std::conditional_t<kValues, Values, NoValues> values;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t at = blockIdx.x;
     const int b = (int)(at / a.rows), r = (int)(at - (int64_t)b * a.rows);
@@ -601,7 +781,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
     // what the list holds: nothing, all that stays, or the tokens around the edge
     enum { kNothing, kAll, kEdge } holds = kNothing;
     uint32_t low = 0;                                      // the smallest key there
-    if (ask.top_k <= kMostK && (by_p || ask.top_k > 0)) {
+    bool edged = false, part = false;
+    u64 tied = 0;
+    if constexpr (kValues) {
+        if (ask.top_k > kMostK || (by_p && ask.top_k == 0)) {
+            const ByValue by(values, top, top - (shift + 2) * 0.6931472f * temperature);
+            Ask any = ask;
+            any.least = 0;
+            by.fill(any, edge, tid);
+            count_values(row, by, ask, wave, lane);
+            edged = edge_by_value(by, ask, edge, tied, part, s, wave, lane);
+            if (!edged) {
+                edge = {-INFINITY, INT32_MAX};
+                part = false;
+            }
+        }
+    }
+    if (edged) {
+        // the row itself, below
+    } else if (ask.top_k <= kMostK && ((by_p && !kValues) || ask.top_k > 0)) {
         // the logit that j threads' largest reach (its upper 22 bits)
         const u64 j = ask.top_k > 0 ? ask.top_k : kForP;
         const Largest largest{mine};
@@ -642,7 +840,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
                 low = 0;
             }
         }
-    } else if (ask.top_k == 0 && ask.least > 0) {
+    } else if (!by_p && ask.top_k == 0 && ask.least > 0) {
         // what min_p leaves, and a little more for the roundings of this limit
         const double below = (double)temperature * fmin(log((double)min_p), 0.0);
         const float limit = fmaxf((float)((double)top + below - 1e-6 * (fabs((double)top) - below) - 1e-37), -FLT_MAX);
@@ -653,7 +851,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
     if (holds == kAll && n <= kShort && !(by_p && ask.top_k == 0)) {
         // (top_p alone goes by the weight of the whole row)
         token = draw_short(list, ask, &total, s, wave, lane);
-    } else if (by_p || ask.top_k > 0) {
+    } else if (!edged && (by_p || ask.top_k > 0)) {
         if (holds != kNothing) {
             const int bits = 32 - __clz((low ^ (uint32_t)top_key) | 1);
             edge = find_edge<E>(list, ask, n, all, above, low, bits, s, wave, lane);
@@ -673,8 +871,27 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
     } else if (holds == kAll) {
         token = draw_listed(list, ask, edge, &total, s, wave, lane);
     } else {
-        token = locate(row, [&](int id, float x) { return kept_weight(ask, edge, id, x); },
-                       [&](u64 sum) { return target_of(ask.u, sum); }, &total, s, wave, lane);
+        const auto of = [&](u64 sum) { return target_of(ask.u, sum); };
+        if constexpr (kValues) {
+            u64 unused;
+            if (part)
+                edge.last = locate(row, [&](int, float x) { return (u64)(x == edge.value); }, [&](u64) { return tied - 1; },
+                                   &unused, s, wave, lane);
+            const ByValue by(values, top, top - (shift + 2) * 0.6931472f * temperature);
+            by.fill(ask, edge, tid);
+            // (min_p above 1: `first` alone)
+            const float at_edge = edge.last < INT32_MAX ? edge.value : INFINITY;
+            const int last = edge.last;
+            token = ask.least > 1ull << shift ? -1 : locate(row, [&](int id, float x) {
+                const int i = by.index(x);
+                u64 w = by.weight(x, i);
+                if (i < 0) w = kept_weight(ask, edge, id, x);
+                return x == at_edge && id > last ? 0 : w;
+            }, of, &total, s, wave, lane);
+            if (ask.least > 1ull << shift) total = 1ull << shift;
+        } else {
+            token = locate(row, [&](int id, float x) { return kept_weight(ask, edge, id, x); }, of, &total, s, wave, lane);
+        }
     }
     if (tid == 0) {
         token = token < 0 || token >= a.V ? ask.first : token;

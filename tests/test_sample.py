@@ -177,6 +177,26 @@ def test_all_settings_and_sizes(device, dtype, V):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("shift", [0.0, 300.0, -300.0])
+def test_logits_of_all_magnitudes(device, dtype, shift):
+    """Magnitudes from 2^-40 to 2^4, so that cuts fall among tiny logits, too;
+    limits of more tokens than a list holds; hot and cold rows."""
+    rs = np.random.RandomState(21)
+    how = [dict(), dict(top_p=0.3), dict(top_p=0.5), dict(top_p=0.9), dict(top_k=5000), dict(top_k=12000, top_p=0.7),
+           dict(top_k=1500, min_p=0.3), dict(top_p=0.8, min_p=0.02), dict(temperature=50.0, top_p=0.6),
+           dict(temperature=0.02, top_p=0.9), dict(temperature=1e4), dict(temperature=50.0, min_p=0.999)]
+    B, rows, V = len(how), 3, 20011
+    x = np.exp2(rs.uniform(-40, 4, (B, rows, V))) * rs.choice([-1, 1], (B, rows, V))
+    x[:, 1] = np.exp2(rs.uniform(-40, -20, (B, V))) * rs.choice([-1, 1], (B, V))      # nothing but tiny ones
+    x[:, 2, ::2] = 0.0                                            # thousands of ties in the middle
+    x = torch.from_numpy(x + shift).to(dtype)
+    u = torch.from_numpy(rs.rand(B, rows).astype(np.float32))
+    how = {k: [dict(OFF, **h)[k] for h in how] for k in OFF}
+    check(x, u, *draw(device, x, u, **how), **how)
+
+
+@pytest.mark.gpu
 def test_trees_and_rows_behind_the_last_node(device):
     rs = np.random.RandomState(1)
     B, rows, V = 5, 9, 777
