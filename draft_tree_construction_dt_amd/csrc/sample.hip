@@ -300,59 +300,96 @@ __device__ __forceinline__ Cut descend(const Source& from, u64 limit, uint32_t p
     return cut;
 }
 
-// The first id with which the sum of m(id, x) over the row passes `target`,
-// which all of it does; target = of(the sum of all).
+// The first id with which the sum of m.one(id, x) over the row passes `target`,
+// which all of it does; target = of(the sum of all).  m.group(g, v) is the sum of
+// a group.
 template <class E, class M, class Of>
-__device__ __forceinline__ int locate(const Row<E>& row, M m, Of of, u64* total, Shared& s, int wave, int lane) {
+__device__ __forceinline__ int locate(const Row<E>& row, const M& m, Of of, u64* total, Shared& s, int wave, int lane) {
     int g0 = 0, g1 = row.groups;
     u64 before = 0, target = 0;
-    for (int level = 0; level < 3; ++level) {
+    bool whole = true;
+    do {
         // all waves, a part each; the part in which the target lies goes on
         const int per = (g1 - g0 + kWaves - 1) / kWaves;
         const int from = g0 + wave * per < g1 ? g0 + wave * per : g1, to = from + per < g1 ? from + per : g1;
         u64 sum = 0;
-        row.scan(from, to, lane, [&](int id, float x) { sum += m(id, x); });
+        row.groups_of(from, to, lane, [&](int g, const u32x4& v) { sum += m.group(g, v); });
         sum = wave_add_u64(sum);
         if (lane == 0) s.wave[0][wave] = sum;
         __syncthreads();
-        if (level == 0) {
+        if (whole) {
             u64 all = 0;
+#pragma unroll
             for (int i = 0; i < kWaves; ++i) all += s.wave[0][i];
             *total = all;
             target = of(all);
+            whole = false;
         }
+        u64 upto = before;
         int at = 0;
-        for (; at < kWaves - 1 && before + s.wave[0][at] <= target; ++at) before += s.wave[0][at];
+#pragma unroll
+        for (int i = 0; i < kWaves - 1; ++i) {
+            upto += s.wave[0][i];
+            if (upto <= target) {
+                at = i + 1;
+                before = upto;
+            }
+        }
         const int n0 = g0 + at * per < g1 ? g0 + at * per : g1;
         g1 = n0 + per < g1 ? n0 + per : g1;
         g0 = n0;
         __syncthreads();
-    }
-    // what is left: 1/4096 of the row, element by element
-    int found = -1;
-    for (int g = g0; g < g1 && found < 0; g += 64) {
-        // lanes hold groups: a group's sum first
-        u64 sum = 0;
-        row.scan(g, g + 64 < g1 ? g + 64 : g1, lane, [&](int id, float x) { sum += m(id, x); });
-        const u64 upto = wave_prefix_u64(sum, lane);
-        const u64 hit = __ballot(before + upto > target);
-        if (!hit) {
-            before += readlane64(upto, 63);
-            continue;
-        }
-        const int l = __builtin_ctzll(hit);
-        u64 sofar = before + readlane64(upto, l) - readlane64(sum, l);
-        row.scan(g + l, g + l + 1, lane, [&](int id, float x) {
-            const u64 w = m(id, x);                        // (lane 0's: the others have no group)
-            if (lane == 0 && found < 0 && w > 0) {
-                sofar += w;
-                if (sofar > target) found = id;
+    } while (g1 - g0 > 4 * kThreads);
+    // a thread a run of up to four groups
+    const int per = (g1 - g0 + kThreads - 1) / kThreads, mine = g0 + (wave * 64 + lane) * per;
+    u64 sum = 0;
+    for (int i = 0; i < per; ++i)
+        if (mine + i < g1) sum += m.group(mine + i, row.load(mine + i));
+    const u64 upto = wave_prefix_u64(sum, lane);
+    if (lane == 63) s.wave[0][wave] = upto;
+    if (wave == 0 && lane == 0) s.found[0] = ~0ull;
+    __syncthreads();
+    u64 sofar = before + upto - sum;
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i) sofar += i < wave ? s.wave[0][i] : 0;
+    if (sofar <= target && sofar + sum > target) {
+        int found = -1;
+        for (int i = 0; i < per; ++i) {
+            if (mine + i >= g1) break;
+            const u32x4 v = row.load(mine + i);
+#pragma unroll
+            for (int e = 0; e < Row<E>::kEach; ++e) {
+                const int id = (mine + i) * Row<E>::kEach - row.before + e;
+                const float x = Row<E>::at(v, e);
+                sofar += m.one(id, x == x ? x : -INFINITY);
+                if (found < 0 && sofar > target) found = id;
             }
-        });
-        found = __builtin_amdgcn_readlane(found, 0);
+        }
+        s.found[0] = (u64)found;
     }
-    return found;
+    __syncthreads();
+    return (int)s.found[0];
 }
+
+// Of a function of id and logit.
+template <class E, class F>
+struct Each {
+    const Row<E>& row;
+    F f;
+
+    __device__ __forceinline__ u64 one(int id, float x) const { return f(id, x); }
+    __device__ __forceinline__ u64 group(int g, const u32x4& v) const {
+        u64 sum = 0;
+#pragma unroll
+        for (int e = 0; e < Row<E>::kEach; ++e) {
+            const float x = Row<E>::at(v, e);
+            sum += f(g * Row<E>::kEach - row.before + e, x == x ? x : -INFINITY);
+        }
+        return sum;
+    }
+};
+template <class E, class F>
+__device__ __forceinline__ Each<E, F> each_of(const Row<E>& row, F f) { return {row, f}; }
 
 // What a request asks for, and the row's own measures.
 struct Ask {
@@ -617,22 +654,74 @@ struct ByValue {
     }
 };
 
+// What is kept of a row, by the weights that fill() has left of the values.
+template <class E>
+struct KeptByValue {
+    const Row<E>& row;
+    const ByValue& by;
+    const Ask& ask;
+    const Edge& edge;
+
+    __device__ __forceinline__ u64 one(int id, float x) const {
+        const int i = by.index(x);
+        if (i < 0) return kept_weight(ask, edge, id, x);
+        return x == edge.value && id > edge.last ? 0 : by.weight(x, i);
+    }
+    // the reads of LDS side by side; tiny logits, which are few, one by one
+    __device__ __forceinline__ u64 group(int g, const u32x4& v) const {
+        u64 w[Row<E>::kEach], sum = 0;
+        int least = 0;
+#pragma unroll
+        for (int e = 0; e < Row<E>::kEach; ++e) {
+            const float x = Row<E>::at(v, e);
+            const int i = by.index(x);
+            least = i < least ? i : least;
+            w[e] = by.weight(x, i);
+        }
+        if (__any(least < 0) || edge.last < INT32_MAX) {
+#pragma unroll
+            for (int e = 0; e < Row<E>::kEach; ++e) {
+                const float x = Row<E>::at(v, e);
+                const int id = g * Row<E>::kEach - row.before + e;
+                if (x == edge.value && id > edge.last) w[e] = 0;
+                if (by.index(x) < 0) w[e] = kept_weight(ask, edge, id, x);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < Row<E>::kEach; ++e) sum += w[e];
+        return sum;
+    }
+};
+
 // Counts every value of the row.
 template <class E>
 __device__ __forceinline__ void count_values(const Row<E>& row, const ByValue& by, const Ask& ask, int wave, int lane) {
-    const int tid = wave * 64 + lane;
+    const int tid = wave * 64 + lane, per = (row.groups + kWaves - 1) / kWaves;
+    const int g0 = wave * per < row.groups ? wave * per : row.groups, g1 = g0 + per < row.groups ? g0 + per : row.groups;
     for (int i = tid; i < kMagnitudes; i += kThreads) by.v.count[i] = by.v.count[4096 + i] = 0;
     if (tid == 0) {
         by.v.tiny_weight = 0;
         by.v.tiny_count = 0;
     }
     __syncthreads();
-    row.each(wave, lane, [&](int, float x) {
-        const int i = by.index(x);
-        if (i >= 0 && i < kMagnitudes - 1) by.count(x, i);
-        if (i < 0) {
-            atomicAdd(&by.v.tiny_count, 1u);
-            atomicAdd(&by.v.tiny_weight, ask.weights(x));
+    row.groups_of(g0, g1, lane, [&](int, const u32x4& v) {
+        int least = 0;
+#pragma unroll
+        for (int e = 0; e < Row<E>::kEach; ++e) {
+            const float x = Row<E>::at(v, e);
+            const int i = by.index(x);
+            least = i < least ? i : least;
+            if ((unsigned)i < (unsigned)kMagnitudes - 1) by.count(x, i);
+        }
+        if (least < 0) {
+#pragma unroll
+            for (int e = 0; e < Row<E>::kEach; ++e) {
+                const float x = Row<E>::at(v, e);
+                if (by.index(x) < 0) {
+                    atomicAdd(&by.v.tiny_count, 1u);
+                    atomicAdd(&by.v.tiny_weight, ask.weights(x));
+                }
+            }
         }
     });
     __syncthreads();
@@ -684,16 +773,22 @@ __device__ __forceinline__ bool make_list(const Row<E>& row, F wanted, Shared& s
         uint32_t mine = 0;
 #pragma unroll
         for (int e = 0; e < Row<E>::kEach; ++e) mine |= wanted(Row<E>::at(v, e)) ? 1u << e : 0u;
-        if (mine) {
-            uint32_t to = atomicAdd(&s.listed, (uint32_t)__popc(mine));
+        if (__any(mine != 0)) {
+            uint32_t all = 0, to[Row<E>::kEach];
+#pragma unroll
+            for (int e = 0; e < Row<E>::kEach; ++e) {
+                const u64 hit = __ballot(mine >> e & 1);
+                to[e] = all + __builtin_amdgcn_mbcnt_hi((uint32_t)(hit >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hit, 0));
+                all += (uint32_t)__popcll(hit);
+            }
+            uint32_t at = 0;
+            if (lane == 0) at = atomicAdd(&s.listed, all);
+            at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
 #pragma unroll
             for (int e = 0; e < Row<E>::kEach; ++e)
-                if (mine >> e & 1) {
-                    if (to < kList) {
-                        s.list[to] = Row<E>::at(v, e);
-                        s.ids[to] = g * Row<E>::kEach - row.before + e;
-                    }
-                    ++to;
+                if ((mine >> e & 1) && at + to[e] < kList) {
+                    s.list[at + to[e]] = Row<E>::at(v, e);
+                    s.ids[at + to[e]] = g * Row<E>::kEach - row.before + e;
                 }
         }
     });
@@ -875,22 +970,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
         if constexpr (kValues) {
             u64 unused;
             if (part)
-                edge.last = locate(row, [&](int, float x) { return (u64)(x == edge.value); }, [&](u64) { return tied - 1; },
-                                   &unused, s, wave, lane);
+                edge.last = locate(row, each_of(row, [&](int, float x) { return (u64)(x == edge.value); }),
+                                   [&](u64) { return tied - 1; }, &unused, s, wave, lane);
             const ByValue by(values, top, top - (shift + 2) * 0.6931472f * temperature);
             by.fill(ask, edge, tid);
             // (min_p above 1: `first` alone)
-            const float at_edge = edge.last < INT32_MAX ? edge.value : INFINITY;
-            const int last = edge.last;
-            token = ask.least > 1ull << shift ? -1 : locate(row, [&](int id, float x) {
-                const int i = by.index(x);
-                u64 w = by.weight(x, i);
-                if (i < 0) w = kept_weight(ask, edge, id, x);
-                return x == at_edge && id > last ? 0 : w;
-            }, of, &total, s, wave, lane);
+            token = ask.least > 1ull << shift ? -1
+                                              : locate(row, KeptByValue<E>{row, by, ask, edge}, of, &total, s, wave, lane);
             if (ask.least > 1ull << shift) total = 1ull << shift;
         } else {
-            token = locate(row, [&](int id, float x) { return kept_weight(ask, edge, id, x); }, of, &total, s, wave, lane);
+            token = locate(row, each_of(row, [&](int id, float x) { return kept_weight(ask, edge, id, x); }), of, &total, s,
+                           wave, lane);
         }
     }
     if (tid == 0) {
