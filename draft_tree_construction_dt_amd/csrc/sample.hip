@@ -9,7 +9,7 @@
 // neither ever meets two sums that should agree and do not.
 //
 // A workgroup takes a row.  It reads it for the largest logit, and keeps each
-// thread's own largest: the j-th of those is a limit that j tokens at least
+// thread's own two largest: the j-th of those is a limit that j tokens at least
 // reach.  Then, by what the request asks for:
 //   top-k       the tokens at or above that limit go to a list in LDS, once
 //               through the row, and all else happens there;
@@ -24,8 +24,6 @@
 #include <float.h>
 #include <math.h>
 
-#include <type_traits>
-
 #include "pass.h"
 #include "wave.h"
 
@@ -34,13 +32,12 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kThreads = 512, kWaves = kThreads / 64;      // two workgroups on a compute unit
 constexpr int kBits = 11, kBins = 1 << kBits;              // of a histogram
 constexpr int kDeep = 4;           // 16-byte loads of a lane in flight
 constexpr int kList = 6144;        // tokens of the list
-// Threads whose largest logit reaches the list's limit.  For top_k as many as
-// that, up to 1000 (of 148 logits a thread, V = 151936, about 3800 tokens in no
-// order reach what 1000 of 1024 threads do); for top_p alone 896 (2100 tokens).
+// How many of the threads' two largest logits reach the list's limit.  For top_k
+// as many as that, up to 1000; for top_p alone 896.
 constexpr int kMostK = 1000;
 constexpr int kForP = 896;
 constexpr int kTable = 64;
@@ -158,28 +155,33 @@ struct Row {
     }
 };
 
-// Weights of the 16-bit type's values, a word each: 19 binades of magnitudes (of
-// 128 values) that reach past every logit that weighs anything, positive ones and,
-// 32 KiB on, negative ones; and how often they occur.
-constexpr int kMagnitudes = 19 * 128;
+// Weights of the 16-bit type's values, and how often they occur: 22 binades of
+// magnitudes (of 128 values) that reach past every logit that weighs anything,
+// positive ones, then negative ones.
+constexpr int kBinades = 22, kMagnitudes = kBinades * 128;
 struct Values {
-    u64 weight[4096 + kMagnitudes];
-    uint32_t count[4096 + kMagnitudes];
-    u64 tiny_weight;               // smaller magnitudes than those
-    uint32_t tiny_count;
+    u64 weight[2 * kMagnitudes];
+    uint32_t count[2 * kMagnitudes];
 };
-struct NoValues {};
-
-struct Shared {
-    double table[kTable];
+struct Histogram {
     u64 weight[kBins];
     uint32_t count[kBins];
     float list[kList];
     int ids[kList];
+};
+struct Shared {
+    union {                        // a row goes by one or the other
+        Histogram h;
+        Values v;
+    };
+    double table[kTable];
     u64 wave[2][kWaves];
     u64 found[4];
+    u64 tiny_weight;               // of magnitudes smaller than those of `v`
+    uint32_t tiny_count;
     uint32_t listed;
 };
+static_assert(sizeof(Shared) <= 80 * 1024, "two workgroups on a compute unit");
 
 // The list, once it is complete.
 struct List {
@@ -188,7 +190,7 @@ struct List {
 
     template <class F>
     __device__ __forceinline__ void each(int wave, int lane, F f) const {
-        for (int i = wave * 64 + lane; i < n; i += kThreads) f(s.ids[i], s.list[i]);
+        for (int i = wave * 64 + lane; i < n; i += kThreads) f(s.h.ids[i], s.h.list[i]);
     }
 };
 
@@ -234,29 +236,40 @@ struct Cut {
 // `limit`, which all of them do; counts and weights before it go to `cut`.
 template <bool BY_WEIGHT>
 __device__ __forceinline__ int pick_bin(int bins, u64 limit, Cut& cut, Shared& s, int wave, int lane) {
-    // thread t's bins are the t-th pair from the top
-    const int b0 = bins - 1 - 2 * (wave * 64 + lane), b1 = b0 - 1;
-    const u64 c0 = b0 >= 0 ? s.count[b0] : 0, c1 = b1 >= 0 ? s.count[b1] : 0;
-    const u64 w0 = BY_WEIGHT && b0 >= 0 ? s.weight[b0] : 0, w1 = BY_WEIGHT && b1 >= 0 ? s.weight[b1] : 0;
-    const u64 cp = wave_prefix_u64(c0 + c1, lane), wp = BY_WEIGHT ? wave_prefix_u64(w0 + w1, lane) : 0;
+    // thread t's bins are the t-th kMine from the top
+    constexpr int kMine = kBins / kThreads;
+    const int top = bins - 1 - kMine * (wave * 64 + lane);
+    u64 c[kMine], w[kMine], cs = 0, ws = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        c[i] = top - i >= 0 ? s.h.count[top - i] : 0;
+        w[i] = BY_WEIGHT && top - i >= 0 ? s.h.weight[top - i] : 0;
+        cs += c[i];
+        ws += w[i];
+    }
+    const u64 cp = wave_prefix_u64(cs, lane), wp = BY_WEIGHT ? wave_prefix_u64(ws, lane) : 0;
     if (lane == 63) {
         s.wave[0][wave] = cp;
         s.wave[1][wave] = wp;
     }
     __syncthreads();
-    u64 cx = cut.count + cp - c0 - c1, wx = cut.weight + wp - w0 - w1;     // before this thread's bins
+    u64 cx = cut.count + cp - cs, wx = cut.weight + wp - ws;       // before this thread's bins
 #pragma unroll
     for (int i = 0; i < kWaves - 1; ++i) {
         cx += i < wave ? s.wave[0][i] : 0;
         if (BY_WEIGHT) wx += i < wave ? s.wave[1][i] : 0;
     }
-    const u64 m0 = BY_WEIGHT ? wx : cx, m1 = m0 + (BY_WEIGHT ? w0 : c0), m2 = m1 + (BY_WEIGHT ? w1 : c1);
-    const bool in0 = m0 < limit && m1 >= limit, in1 = m1 < limit && m2 >= limit;
-    if (in0 || in1) {
-        s.found[0] = (u64)(in0 ? b0 : b1);
-        s.found[1] = in0 ? cx : cx + c0;
-        s.found[2] = in0 ? wx : wx + w0;
-        s.found[3] = in0 ? c0 : c1;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const u64 m = BY_WEIGHT ? wx : cx;
+        if (m < limit && m + (BY_WEIGHT ? w[i] : c[i]) >= limit) {
+            s.found[0] = (u64)(top - i);
+            s.found[1] = cx;
+            s.found[2] = wx;
+            s.found[3] = c[i];
+        }
+        cx += c[i];
+        wx += w[i];
     }
     __syncthreads();
     cut.count = (uint32_t)s.found[1];
@@ -267,8 +280,8 @@ __device__ __forceinline__ int pick_bin(int bins, u64 limit, Cut& cut, Shared& s
 
 __device__ __forceinline__ void clear_bins(int bins, Shared& s, int tid) {
     for (int i = tid; i < bins; i += kThreads) {
-        s.count[i] = 0;
-        s.weight[i] = 0;
+        s.h.count[i] = 0;
+        s.h.weight[i] = 0;
     }
     __syncthreads();
 }
@@ -289,8 +302,8 @@ __device__ __forceinline__ Cut descend(const Source& from, u64 limit, uint32_t p
             u64 w;
             if (!of(id, x, k, w) || (bits < 32 && (k >> bits) != (cut.key >> bits))) return;
             const int bin = (k >> shift) & ((1 << take) - 1);
-            atomicAdd(&s.count[bin], 1u);
-            if (BY_WEIGHT && w) atomicAdd(&s.weight[bin], w);
+            atomicAdd(&s.h.count[bin], 1u);
+            if (BY_WEIGHT && w) atomicAdd(&s.h.weight[bin], w);
         });
         __syncthreads();
         cut.key |= (uint32_t)pick_bin<BY_WEIGHT>(1 << take, limit, cut, s, wave, lane) << shift;
@@ -500,24 +513,24 @@ __device__ __forceinline__ int draw_listed(const List& list, const Ask& ask, con
 }
 
 // The same as find_edge and draw_listed, from a short list that holds all that
-// stays: every pair of its tokens is compared, 1024 / 256 threads a token.
+// stays: every pair of its tokens is compared, two threads a token.
 __device__ __forceinline__ int draw_short(const List& list, const Ask& ask, u64* total, Shared& s, int wave, int lane) {
     constexpr int kParts = kThreads / kShort;
     const int tid = wave * 64 + lane, i = tid / kParts, part = tid % kParts;
     const bool mine = i < list.n;
-    const float x = mine ? s.list[i] : -INFINITY;
-    const int id = mine ? s.ids[i] : INT32_MAX;
+    const float x = mine ? s.h.list[i] : -INFINITY;
+    const int id = mine ? s.h.ids[i] : INT32_MAX;
     const u64 w = mine ? ask.weights(x) : 0;
-    if (mine && part == 0) s.weight[i] = w;
+    if (mine && part == 0) s.h.weight[i] = w;
     __syncthreads();
     // those before it in the order: their number and weight
     uint32_t rank = 0;
     u64 before = 0;
     for (int j = part; j < list.n; j += kParts) {
-        const float y = s.list[j];
-        const bool first = y > x || (y == x && s.ids[j] < id);
+        const float y = s.h.list[j];
+        const bool first = y > x || (y == x && s.h.ids[j] < id);
         rank += first;
-        before += first ? s.weight[j] : 0;
+        before += first ? s.h.weight[j] : 0;
     }
 #pragma unroll
     for (int d = 1; d < kParts; d <<= 1) {
@@ -533,11 +546,11 @@ __device__ __forceinline__ int draw_short(const List& list, const Ask& ask, u64*
     const u64 kept = stays ? w : 0;
     *total = block_add(part == 0 ? kept : 0, s, wave, lane);
     if (*total == 0) return ask.first;
-    if (mine && part == 0) s.weight[i] = kept;
+    if (mine && part == 0) s.h.weight[i] = kept;
     __syncthreads();
     // those before it by id
     u64 upto = 0;
-    for (int j = part; j < list.n; j += kParts) upto += s.ids[j] < id ? s.weight[j] : 0;
+    for (int j = part; j < list.n; j += kParts) upto += s.h.ids[j] < id ? s.h.weight[j] : 0;
 #pragma unroll
     for (int d = 1; d < kParts; d <<= 1)
         upto += (u64)(uint32_t)__shfl_xor((int)(uint32_t)upto, d) | (u64)(uint32_t)__shfl_xor((int)(uint32_t)(upto >> 32), d) << 32;
@@ -552,15 +565,15 @@ typedef __attribute__((address_space(3))) char* Lds;
 // Weights of 16-bit logits by their bits: a read of LDS in place of some thirty
 // instructions.
 struct ByValue {
-    Values& v;
+    Shared& s;
     int base;                      // bits of the smallest magnitude there
 
     // exponents up to one past those of the largest logit and of the smallest that
     // weighs anything
-    __device__ __forceinline__ ByValue(Values& v_, float top, float low) : v(v_) {
-        const uint32_t m = __float_as_uint(fmaxf(fabsf(top), fabsf(low))) >> 23;   // (inf: 255)
-        const int first = (int)m + 1 - 18;
-        base = (first < 0 ? 0 : (first > 237 ? 237 : first)) << 7;
+    __device__ __forceinline__ ByValue(Shared& s_, float top, float low) : s(s_) {
+        const int m = (int)(__float_as_uint(fmaxf(fabsf(top), fabsf(low))) >> 23);     // (inf: 255)
+        const int first = m + 2 - kBinades;
+        base = (first < 0 ? 0 : (first > 256 - kBinades ? 256 - kBinades : first)) << 7;
     }
     __device__ __forceinline__ float value(int i, int negative) const {
         return __uint_as_float((uint32_t)(base + i + (negative ? 0x8000 : 0)) << 16);
@@ -570,13 +583,11 @@ struct ByValue {
         const int i = (int)((__float_as_uint(x) >> 16) & 0x7FFF) - base;
         return i < kMagnitudes - 1 ? i : kMagnitudes - 1;
     }
-    __device__ __forceinline__ u64 weight(float x, int i) const {
-        const uint32_t at = (uint32_t)(i < 0 ? 0 : i) * 8 + ((__float_as_uint(x) >> 16) & 0x8000);
-        return *(__attribute__((address_space(3))) const u64*)((Lds)v.weight + at);
+    static __device__ __forceinline__ int place(float x, int i) {  // in the arrays
+        return i + ((__float_as_int(x) >> 31) & kMagnitudes);
     }
-    __device__ __forceinline__ void count(float x, int i) const {
-        atomicAdd((uint32_t*)((char*)v.count + i * 4 + ((__float_as_uint(x) >> 17) & 0x4000)), 1u);
-    }
+    __device__ __forceinline__ u64 weight(float x, int i) const { return s.v.weight[place(x, i < 0 ? 0 : i)]; }
+    __device__ __forceinline__ void count(float x, int i) const { atomicAdd(&s.v.count[place(x, i)], 1u); }
     __device__ __forceinline__ void fill(const Ask& ask, const Edge& edge, int tid) const {
         for (int i = tid; i < kMagnitudes; i += kThreads)
 #pragma unroll
@@ -584,29 +595,26 @@ struct ByValue {
                 const float x = value(i, n);
                 const bool stays = i < kMagnitudes - 1 && x <= (float)ask.weights.top && x >= edge.value;
                 const u64 w = stays ? ask.weights(x) : 0;
-                v.weight[n * 4096 + i] = w >= ask.least ? w : 0;
+                s.v.weight[n * kMagnitudes + i] = w >= ask.least ? w : 0;
             }
         __syncthreads();
     }
     // the order's beginning that reaches `limit` in number (or weight): its last
     // value's, false where that is a tiny one
     template <bool BY_WEIGHT>
-    __device__ __forceinline__ bool cut(u64 limit, float& x, Cut& c, Shared& s, int wave, int lane) const {
-        // from the top: positive values, the tiny ones, negative values; five a thread
-        constexpr int kEach = 5;
-        static_assert(kEach * kThreads >= 2 * kMagnitudes + 1, "every value has a thread");
+    __device__ __forceinline__ bool cut(u64 limit, float& x, Cut& c, int wave, int lane) const {
+        // from the top: positive values, the tiny ones, negative values; so many a thread
+        constexpr int kEach = (2 * kMagnitudes + kThreads) / kThreads;
         const int q0 = (wave * 64 + lane) * kEach;
         const auto bin = [&](int q, u64& n, u64& w) {
             n = w = 0;
-            if (q < kMagnitudes) {
-                n = v.count[kMagnitudes - 1 - q];
-                w = n * v.weight[kMagnitudes - 1 - q];
-            } else if (q == kMagnitudes) {
-                n = v.tiny_count;
-                w = v.tiny_weight;
+            if (q == kMagnitudes) {
+                n = s.tiny_count;
+                w = s.tiny_weight;
             } else if (q <= 2 * kMagnitudes) {
-                n = v.count[4096 + q - kMagnitudes - 1];
-                w = n * v.weight[4096 + q - kMagnitudes - 1];
+                const int at = q < kMagnitudes ? kMagnitudes - 1 - q : q - 1;
+                n = s.v.count[at];
+                w = n * s.v.weight[at];
             }
         };
         u64 n = 0, w = 0;
@@ -698,10 +706,10 @@ template <class E>
 __device__ __forceinline__ void count_values(const Row<E>& row, const ByValue& by, const Ask& ask, int wave, int lane) {
     const int tid = wave * 64 + lane, per = (row.groups + kWaves - 1) / kWaves;
     const int g0 = wave * per < row.groups ? wave * per : row.groups, g1 = g0 + per < row.groups ? g0 + per : row.groups;
-    for (int i = tid; i < kMagnitudes; i += kThreads) by.v.count[i] = by.v.count[4096 + i] = 0;
+    for (int i = tid; i < 2 * kMagnitudes; i += kThreads) by.s.v.count[i] = 0;
     if (tid == 0) {
-        by.v.tiny_weight = 0;
-        by.v.tiny_count = 0;
+        by.s.tiny_weight = 0;
+        by.s.tiny_count = 0;
     }
     __syncthreads();
     row.groups_of(g0, g1, lane, [&](int, const u32x4& v) {
@@ -718,8 +726,8 @@ __device__ __forceinline__ void count_values(const Row<E>& row, const ByValue& b
             for (int e = 0; e < Row<E>::kEach; ++e) {
                 const float x = Row<E>::at(v, e);
                 if (by.index(x) < 0) {
-                    atomicAdd(&by.v.tiny_count, 1u);
-                    atomicAdd(&by.v.tiny_weight, ask.weights(x));
+                    atomicAdd(&by.s.tiny_count, 1u);
+                    atomicAdd(&by.s.tiny_weight, ask.weights(x));
                 }
             }
         }
@@ -734,14 +742,14 @@ __device__ __forceinline__ bool edge_by_value(const ByValue& by, const Ask& ask,
     Cut c;
     float x;
     u64 total = 0, n = 0;
-    for (int i = wave * 64 + lane; i < kMagnitudes; i += kThreads) {
-        total += by.v.count[i] * by.v.weight[i] + by.v.count[4096 + i] * by.v.weight[4096 + i];
-        n += (u64)by.v.count[i] + by.v.count[4096 + i];
+    for (int i = wave * 64 + lane; i < 2 * kMagnitudes; i += kThreads) {
+        total += s.v.count[i] * s.v.weight[i];
+        n += s.v.count[i];
     }
-    n = block_add(n, s, wave, lane) + by.v.tiny_count;
-    total = block_add(total, s, wave, lane) + by.v.tiny_weight;
+    n = block_add(n, s, wave, lane) + by.s.tiny_count;
+    total = block_add(total, s, wave, lane) + by.s.tiny_weight;
     if (ask.top_k > 0 && n > (u64)ask.top_k) {             // (what is not counted weighs nothing)
-        if (!by.cut<false>((u64)ask.top_k, x, c, s, wave, lane)) return false;
+        if (!by.cut<false>((u64)ask.top_k, x, c, wave, lane)) return false;
         edge.value = x;
         tied = (u64)ask.top_k - c.count;
         part = tied < c.ties;
@@ -749,7 +757,7 @@ __device__ __forceinline__ bool edge_by_value(const ByValue& by, const Ask& ask,
     }
     if (ask.top_p < 1) {
         const u64 limit = limit_of(ask.top_p, total);
-        if (!by.cut<true>(limit, x, c, s, wave, lane)) return false;
+        if (!by.cut<true>(limit, x, c, wave, lane)) return false;
         const u64 w = ask.weights(x), need = w ? (limit - c.weight + w - 1) / w : 0;
         if (x == edge.value && part) {
             tied = need < tied ? need : tied;
@@ -787,8 +795,8 @@ __device__ __forceinline__ bool make_list(const Row<E>& row, F wanted, Shared& s
 #pragma unroll
             for (int e = 0; e < Row<E>::kEach; ++e)
                 if ((mine >> e & 1) && at + to[e] < kList) {
-                    s.list[at + to[e]] = Row<E>::at(v, e);
-                    s.ids[at + to[e]] = g * Row<E>::kEach - row.before + e;
+                    s.h.list[at + to[e]] = Row<E>::at(v, e);
+                    s.h.ids[at + to[e]] = g * Row<E>::kEach - row.before + e;
                 }
         }
     });
@@ -796,20 +804,22 @@ __device__ __forceinline__ bool make_list(const Row<E>& row, F wanted, Shared& s
     return s.listed <= kList;
 }
 
-// Each thread's largest logit.
+// Each thread's two largest logits (of different groups).
 struct Largest {
-    float mine;
+    float mine, second;
 
     template <class F>
-    __device__ __forceinline__ void each(int, int, F f) const { f(0, mine); }
+    __device__ __forceinline__ void each(int, int, F f) const {
+        f(0, mine);
+        f(0, second);
+    }
 };
 
 template <class E>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shift) {
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int shift) {
     // 16-bit logits have few values: each one's weight is made once
     constexpr bool kValues = sizeof(E) == 2;
     __shared__ Shared s;
-    __shared__ std::conditional_t<kValues, Values, NoValues> values;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t at = blockIdx.x;
     const int b = (int)(at / a.rows), r = (int)(at - (int64_t)b * a.rows);
@@ -819,12 +829,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
 
     // the largest logit and its first id: each lane's largest, and where it was met first
     const int per = (row.groups + kWaves - 1) / kWaves, g0 = wave * per < row.groups ? wave * per : row.groups;
-    float mine = -INFINITY;
+    float mine = -INFINITY, second = -INFINITY;
     int where = 0;
     row.groups_of(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
         float x = Row<E>::at(v, 0);
 #pragma unroll
         for (int e = 1; e < Row<E>::kEach; ++e) x = fmaxf(x, Row<E>::at(v, e));
+        second = fmaxf(second, fminf(mine, x));
         where = x > mine ? g : where;
         mine = x > mine ? x : mine;
     });
@@ -880,7 +891,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
     u64 tied = 0;
     if constexpr (kValues) {
         if (ask.top_k > kMostK || (by_p && ask.top_k == 0)) {
-            const ByValue by(values, top, top - (shift + 2) * 0.6931472f * temperature);
+            const ByValue by(s, top, top - (shift + 2) * 0.6931472f * temperature);
             Ask any = ask;
             any.least = 0;
             by.fill(any, edge, tid);
@@ -897,9 +908,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
     } else if (ask.top_k <= kMostK && ((by_p && !kValues) || ask.top_k > 0)) {
         // the logit that j threads' largest reach (its upper 22 bits)
         const u64 j = ask.top_k > 0 ? ask.top_k : kForP;
-        const Largest largest{mine};
+        const Largest largest{mine, second};
         float limit = -FLT_MAX;
-        if (block_add(mine > -INFINITY, s, wave, lane) >= j) {
+        if (block_add((u64)(mine > -INFINITY) + (second > -INFINITY), s, wave, lane) >= j) {
             const Cut c = descend<false>(largest, j, 0, 22, [&](int, float x, uint32_t& k, u64&) {
                 k = key_of(x) >> 10;
                 return x > -INFINITY;
@@ -917,11 +928,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
             clear_bins(kBins, s, tid);
             const bool fits = make_list(row, [&](float x) {
                 const u64 w = ask.weights(x);
-                if (w) atomicAdd(&s.weight[bin_of(x)], w);
+                if (w) atomicAdd(&s.h.weight[bin_of(x)], w);
                 return x >= limit;
             }, s, wave, lane);
             n = (int)s.listed;
-            for (int i = tid; i < kBins; i += kThreads) all += s.weight[i];
+            for (int i = tid; i < kBins; i += kThreads) all += s.h.weight[i];
             all = block_add(all, s, wave, lane);
             Cut c = {0, 0, 0, 0};
             const int bin = pick_bin<true>(kBins, limit_of(ask.top_p, all), c, s, wave, lane);
@@ -972,7 +983,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int shif
             if (part)
                 edge.last = locate(row, each_of(row, [&](int, float x) { return (u64)(x == edge.value); }),
                                    [&](u64) { return tied - 1; }, &unused, s, wave, lane);
-            const ByValue by(values, top, top - (shift + 2) * 0.6931472f * temperature);
+            const ByValue by(s, top, top - (shift + 2) * 0.6931472f * temperature);
             by.fill(ask, edge, tid);
             // (min_p above 1: `first` alone)
             token = ask.least > 1ull << shift ? -1
