@@ -34,7 +34,6 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;      // two workgroups on a compute unit
 constexpr int kBits = 11, kBins = 1 << kBits;              // of a histogram
-constexpr int kDeep = 4;           // 16-byte loads of a lane in flight
 constexpr int kList = 6144;        // tokens of the list
 // How many of the threads' two largest logits reach the list's limit.  For top_k
 // as many as that, up to 1000; for top_p alone 896.
@@ -119,18 +118,19 @@ struct Row {
     }
     // f(g, v) for groups g0 .. g1 - 1 by one wave, whose lanes stay together
     // (f may use the whole wave; lanes without a group get -inf).
-    template <class F>
+    // DEEP loads of a lane are in flight.
+    template <int DEEP, class F>
     __device__ __forceinline__ void groups_of(int g0, int g1, int lane, F f) const {
-        for (int64_t first = g0; first < g1; first += kDeep * 64) {
-            u32x4 v[kDeep];
+        for (int64_t first = g0; first < g1; first += DEEP * 64) {
+            u32x4 v[DEEP];
 #pragma unroll
-            for (int i = 0; i < kDeep; ++i) {
+            for (int i = 0; i < DEEP; ++i) {
                 const int64_t g = first + i * 64 + lane;
                 v[i] = u32x4{kNone, kNone, kNone, kNone};
                 if (g < g1) v[i] = load((int)g);
             }
 #pragma unroll
-            for (int i = 0; i < kDeep; ++i) {
+            for (int i = 0; i < DEEP; ++i) {
                 if (first + i * 64 >= g1) break;
                 f((int)(first + i * 64) + lane, v[i]);
             }
@@ -139,7 +139,7 @@ struct Row {
     // f(id, x) for every element of them.
     template <class F>
     __device__ __forceinline__ void scan(int g0, int g1, int lane, F f) const {
-        groups_of(g0, g1, lane, [&](int g, const u32x4& v) {
+        groups_of<4>(g0, g1, lane, [&](int g, const u32x4& v) {
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
                 const float x = at(v, e);
@@ -313,39 +313,65 @@ __device__ __forceinline__ Cut descend(const Source& from, u64 limit, uint32_t p
     return cut;
 }
 
-// The first id with which the sum of m.one(id, x) over the row passes `target`,
-// which all of it does; target = of(the sum of all).  m.group(g, v) is the sum of
-// a group.
+// A sum of weights, and a number of tokens at the edge, of which the first
+// `tied` of the row weigh `each`.
+struct Sum {
+    u64 weight, ties;
+};
+struct Tied {
+    u64 tied, each;
+
+    // the weight of a part behind `before` tokens at the edge
+    __device__ __forceinline__ u64 weight(const Sum& part, u64 before) const {
+        const u64 upto = before + part.ties;
+        return part.weight + ((upto < tied ? upto : tied) - (before < tied ? before : tied)) * each;
+    }
+};
+
+// The first id with which the weight of what m.one(id, x, sum) adds up over the
+// row passes `target`, which all of it does; target = of(the weight of all).
+// m.group(g, v, sum) adds a group.
 template <class E, class M, class Of>
-__device__ __forceinline__ int locate(const Row<E>& row, const M& m, Of of, u64* total, Shared& s, int wave, int lane) {
+__device__ __forceinline__ int locate(const Row<E>& row, const M& m, const Tied& tied, Of of, u64* total, Shared& s, int wave,
+                                      int lane) {
     int g0 = 0, g1 = row.groups;
-    u64 before = 0, target = 0;
+    u64 before = 0, ties = 0, target = 0;                  // weight and ties before group g0
     bool whole = true;
     do {
         // all waves, a part each; the part in which the target lies goes on
         const int per = (g1 - g0 + kWaves - 1) / kWaves;
         const int from = g0 + wave * per < g1 ? g0 + wave * per : g1, to = from + per < g1 ? from + per : g1;
-        u64 sum = 0;
-        row.groups_of(from, to, lane, [&](int g, const u32x4& v) { sum += m.group(g, v); });
-        sum = wave_add_u64(sum);
-        if (lane == 0) s.wave[0][wave] = sum;
+        Sum sum = {0, 0};
+        row.template groups_of<2>(from, to, lane, [&](int g, const u32x4& v) { m.group(g, v, sum); });
+        sum.weight = wave_add_u64(sum.weight);
+        sum.ties = wave_add_u64(sum.ties);
+        if (lane == 0) {
+            s.wave[0][wave] = sum.weight;
+            s.wave[1][wave] = sum.ties;
+        }
         __syncthreads();
         if (whole) {
-            u64 all = 0;
+            Sum all = {0, 0};
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) all += s.wave[0][i];
-            *total = all;
-            target = of(all);
+            for (int i = 0; i < kWaves; ++i) {
+                all.weight += s.wave[0][i];
+                all.ties += s.wave[1][i];
+            }
+            *total = tied.weight(all, 0);
+            target = of(*total);
             whole = false;
         }
-        u64 upto = before;
+        u64 upto = before, upto_ties = ties;
         int at = 0;
 #pragma unroll
         for (int i = 0; i < kWaves - 1; ++i) {
-            upto += s.wave[0][i];
+            const Sum part = {s.wave[0][i], s.wave[1][i]};
+            upto += tied.weight(part, upto_ties);
+            upto_ties += part.ties;
             if (upto <= target) {
                 at = i + 1;
                 before = upto;
+                ties = upto_ties;
             }
         }
         const int n0 = g0 + at * per < g1 ? g0 + at * per : g1;
@@ -355,18 +381,27 @@ __device__ __forceinline__ int locate(const Row<E>& row, const M& m, Of of, u64*
     } while (g1 - g0 > 4 * kThreads);
     // a thread a run of up to four groups
     const int per = (g1 - g0 + kThreads - 1) / kThreads, mine = g0 + (wave * 64 + lane) * per;
-    u64 sum = 0;
+    Sum sum = {0, 0};
     for (int i = 0; i < per; ++i)
-        if (mine + i < g1) sum += m.group(mine + i, row.load(mine + i));
-    const u64 upto = wave_prefix_u64(sum, lane);
-    if (lane == 63) s.wave[0][wave] = upto;
+        if (mine + i < g1) m.group(mine + i, row.load(mine + i), sum);
+    const u64 upto = wave_prefix_u64(sum.weight, lane), upto_ties = wave_prefix_u64(sum.ties, lane);
+    if (lane == 63) {
+        s.wave[0][wave] = upto;
+        s.wave[1][wave] = upto_ties;
+    }
     if (wave == 0 && lane == 0) s.found[0] = ~0ull;
     __syncthreads();
-    u64 sofar = before + upto - sum;
+    Sum part = {upto - sum.weight, upto_ties - sum.ties};  // before this thread's run
 #pragma unroll
-    for (int i = 0; i < kWaves - 1; ++i) sofar += i < wave ? s.wave[0][i] : 0;
-    if (sofar <= target && sofar + sum > target) {
+    for (int i = 0; i < kWaves - 1; ++i) {
+        part.weight += i < wave ? s.wave[0][i] : 0;
+        part.ties += i < wave ? s.wave[1][i] : 0;
+    }
+    const u64 sofar = before + tied.weight(part, ties);
+    ties += part.ties;
+    if (sofar <= target && sofar + tied.weight(sum, ties) > target) {
         int found = -1;
+        Sum run = {0, 0};
         for (int i = 0; i < per; ++i) {
             if (mine + i >= g1) break;
             const u32x4 v = row.load(mine + i);
@@ -374,8 +409,8 @@ __device__ __forceinline__ int locate(const Row<E>& row, const M& m, Of of, u64*
             for (int e = 0; e < Row<E>::kEach; ++e) {
                 const int id = (mine + i) * Row<E>::kEach - row.before + e;
                 const float x = Row<E>::at(v, e);
-                sofar += m.one(id, x == x ? x : -INFINITY);
-                if (found < 0 && sofar > target) found = id;
+                m.one(id, x == x ? x : -INFINITY, run);
+                if (found < 0 && sofar + tied.weight(run, ties) > target) found = id;
             }
         }
         s.found[0] = (u64)found;
@@ -384,21 +419,19 @@ __device__ __forceinline__ int locate(const Row<E>& row, const M& m, Of of, u64*
     return (int)s.found[0];
 }
 
-// Of a function of id and logit.
+// Of a weight of id and logit.
 template <class E, class F>
 struct Each {
     const Row<E>& row;
     F f;
 
-    __device__ __forceinline__ u64 one(int id, float x) const { return f(id, x); }
-    __device__ __forceinline__ u64 group(int g, const u32x4& v) const {
-        u64 sum = 0;
+    __device__ __forceinline__ void one(int id, float x, Sum& sum) const { sum.weight += f(id, x); }
+    __device__ __forceinline__ void group(int g, const u32x4& v, Sum& sum) const {
 #pragma unroll
         for (int e = 0; e < Row<E>::kEach; ++e) {
             const float x = Row<E>::at(v, e);
-            sum += f(g * Row<E>::kEach - row.before + e, x == x ? x : -INFINITY);
+            sum.weight += f(g * Row<E>::kEach - row.before + e, x == x ? x : -INFINITY);
         }
-        return sum;
     }
 };
 template <class E, class F>
@@ -578,22 +611,40 @@ struct ByValue {
     __device__ __forceinline__ float value(int i, int negative) const {
         return __uint_as_float((uint32_t)(base + i + (negative ? 0x8000 : 0)) << 16);
     }
-    // (below 0: a tiny one; past the end, NaN and infinities: the last, which weighs nothing)
-    __device__ __forceinline__ int index(float x) const {
+    // Places in the arrays of a group's eight logits, two at a time.  NaN,
+    // infinities and others past the end go to the last one, which weighs nothing;
+    // whether there are any, and whether there are tiny ones.
+    __device__ __forceinline__ void places(const u32x4& v, uint32_t (&at)[8], bool& past, bool& tiny) const {
+        typedef short i16x2 __attribute__((ext_vector_type(2)));
+        constexpr short kLast = kMagnitudes - 1;
+        const i16x2 from = {(short)base, (short)base}, last = {kLast, kLast}, none = {0, 0};
+        i16x2 least = none, most = none;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const i16x2 i = __builtin_bit_cast(i16x2, v[d] & 0x7FFF7FFFu) - from;
+            least = __builtin_elementwise_min(least, i);
+            most = __builtin_elementwise_max(most, i);
+            const i16x2 in = __builtin_elementwise_max(__builtin_elementwise_min(i, last), none);
+            // (both halves at once: a sum stays below 2^16)
+            const uint32_t p = __umul24(v[d] >> 15 & 0x10001u, kMagnitudes) + __builtin_bit_cast(uint32_t, in);
+            at[2 * d] = p & 0xFFFF;
+            at[2 * d + 1] = p >> 16;
+        }
+        past = most[0] >= kLast || most[1] >= kLast;
+        tiny = least[0] < 0 || least[1] < 0;
+    }
+    __device__ __forceinline__ bool is_tiny(float x) const { return (int)((__float_as_uint(x) >> 16) & 0x7FFF) < base; }
+    __device__ __forceinline__ u64 weight(float x) const { // not of tiny ones
         const int i = (int)((__float_as_uint(x) >> 16) & 0x7FFF) - base;
-        return i < kMagnitudes - 1 ? i : kMagnitudes - 1;
+        return s.v.weight[(i < kMagnitudes - 1 ? i : kMagnitudes - 1) + ((__float_as_int(x) >> 31) & kMagnitudes)];
     }
-    static __device__ __forceinline__ int place(float x, int i) {  // in the arrays
-        return i + ((__float_as_int(x) >> 31) & kMagnitudes);
-    }
-    __device__ __forceinline__ u64 weight(float x, int i) const { return s.v.weight[place(x, i < 0 ? 0 : i)]; }
-    __device__ __forceinline__ void count(float x, int i) const { atomicAdd(&s.v.count[place(x, i)], 1u); }
-    __device__ __forceinline__ void fill(const Ask& ask, const Edge& edge, int tid) const {
+    // `ties`: those at the edge are counted apart, and weigh nothing here
+    __device__ __forceinline__ void fill(const Ask& ask, const Edge& edge, bool ties, int tid) const {
         for (int i = tid; i < kMagnitudes; i += kThreads)
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const float x = value(i, n);
-                const bool stays = i < kMagnitudes - 1 && x <= (float)ask.weights.top && x >= edge.value;
+                const bool stays = i < kMagnitudes - 1 && x <= (float)ask.weights.top && (ties ? x > edge.value : x >= edge.value);
                 const u64 w = stays ? ask.weights(x) : 0;
                 s.v.weight[n * kMagnitudes + i] = w >= ask.least ? w : 0;
             }
@@ -669,35 +720,38 @@ struct KeptByValue {
     const ByValue& by;
     const Ask& ask;
     const Edge& edge;
+    bool ties;
 
-    __device__ __forceinline__ u64 one(int id, float x) const {
-        const int i = by.index(x);
-        if (i < 0) return kept_weight(ask, edge, id, x);
-        return x == edge.value && id > edge.last ? 0 : by.weight(x, i);
+    __device__ __forceinline__ void one(int id, float x, Sum& sum) const {
+        if (ties && x == edge.value) ++sum.ties;
+        else if (by.is_tiny(x)) sum.weight += kept_weight(ask, edge, id, x);
+        else if (x != edge.value || id <= edge.last) sum.weight += by.weight(x);
     }
     // the reads of LDS side by side; tiny logits, which are few, one by one
-    __device__ __forceinline__ u64 group(int g, const u32x4& v) const {
-        u64 w[Row<E>::kEach], sum = 0;
-        int least = 0;
+    __device__ __forceinline__ void group(int g, const u32x4& v, Sum& sum) const {
+        uint32_t at[8];
+        u64 w[8];
+        bool past, tiny;
+        by.places(v, at, past, tiny);
 #pragma unroll
-        for (int e = 0; e < Row<E>::kEach; ++e) {
-            const float x = Row<E>::at(v, e);
-            const int i = by.index(x);
-            least = i < least ? i : least;
-            w[e] = by.weight(x, i);
+        for (int e = 0; e < 8; ++e) w[e] = by.s.v.weight[at[e]];
+        if (ties) {
+            uint32_t n = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) n += Row<E>::at(v, e) == edge.value;
+            sum.ties += n;
         }
-        if (__any(least < 0) || edge.last < INT32_MAX) {
+        if (__any(tiny) || edge.last < INT32_MAX) {
 #pragma unroll
-            for (int e = 0; e < Row<E>::kEach; ++e) {
+            for (int e = 0; e < 8; ++e) {
                 const float x = Row<E>::at(v, e);
-                const int id = g * Row<E>::kEach - row.before + e;
+                const int id = g * 8 - row.before + e;
                 if (x == edge.value && id > edge.last) w[e] = 0;
-                if (by.index(x) < 0) w[e] = kept_weight(ask, edge, id, x);
+                if (by.is_tiny(x)) w[e] = ties && x == edge.value ? 0 : kept_weight(ask, edge, id, x);
             }
         }
 #pragma unroll
-        for (int e = 0; e < Row<E>::kEach; ++e) sum += w[e];
-        return sum;
+        for (int e = 0; e < 8; ++e) sum.weight += w[e];
     }
 };
 
@@ -712,24 +766,30 @@ __device__ __forceinline__ void count_values(const Row<E>& row, const ByValue& b
         by.s.tiny_count = 0;
     }
     __syncthreads();
-    row.groups_of(g0, g1, lane, [&](int, const u32x4& v) {
-        int least = 0;
-#pragma unroll
-        for (int e = 0; e < Row<E>::kEach; ++e) {
-            const float x = Row<E>::at(v, e);
-            const int i = by.index(x);
-            least = i < least ? i : least;
-            if ((unsigned)i < (unsigned)kMagnitudes - 1) by.count(x, i);
-        }
-        if (least < 0) {
-#pragma unroll
-            for (int e = 0; e < Row<E>::kEach; ++e) {
-                const float x = Row<E>::at(v, e);
-                if (by.index(x) < 0) {
-                    atomicAdd(&by.s.tiny_count, 1u);
-                    atomicAdd(&by.s.tiny_weight, ask.weights(x));
-                }
+    row.template groups_of<2>(g0, g1, lane, [&](int, const u32x4& v) {
+        uint32_t at[8];
+        bool past, tiny;
+        by.places(v, at, past, tiny);
+        if (__any(tiny)) {
+            // (counted at the smallest magnitude, too, and taken out there)
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t word = e < 2 ? v[0] : (e < 4 ? v[1] : (e < 6 ? v[2] : v[3]));
+                const float x = __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
+                if (!by.is_tiny(x)) continue;
+                atomicAdd(&by.s.tiny_count, 1u);
+                atomicAdd(&by.s.tiny_weight, ask.weights(x));
+                atomicSub(&by.s.v.count[(word >> (16 * (e & 1)) & 0x8000) ? kMagnitudes : 0], 1u);
             }
+        }
+        if (__any(past)) {
+            // what weighs nothing is not counted: half of a row may be -inf, all at one place
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at[e] != kMagnitudes - 1 && at[e] != 2 * kMagnitudes - 1) atomicAdd(&by.s.v.count[at[e]], 1u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) atomicAdd(&by.s.v.count[at[e]], 1u);
         }
     });
     __syncthreads();
@@ -777,7 +837,7 @@ __device__ __forceinline__ bool make_list(const Row<E>& row, F wanted, Shared& s
     if (wave == 0 && lane == 0) s.listed = 0;
     __syncthreads();
     const int per = (row.groups + kWaves - 1) / kWaves, g0 = wave * per < row.groups ? wave * per : row.groups;
-    row.groups_of(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
+    row.template groups_of<4>(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
         uint32_t mine = 0;
 #pragma unroll
         for (int e = 0; e < Row<E>::kEach; ++e) mine |= wanted(Row<E>::at(v, e)) ? 1u << e : 0u;
@@ -831,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
     const int per = (row.groups + kWaves - 1) / kWaves, g0 = wave * per < row.groups ? wave * per : row.groups;
     float mine = -INFINITY, second = -INFINITY;
     int where = 0;
-    row.groups_of(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
+    row.template groups_of<4>(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
         float x = Row<E>::at(v, 0);
 #pragma unroll
         for (int e = 1; e < Row<E>::kEach; ++e) x = fmaxf(x, Row<E>::at(v, e));
@@ -894,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
             const ByValue by(s, top, top - (shift + 2) * 0.6931472f * temperature);
             Ask any = ask;
             any.least = 0;
-            by.fill(any, edge, tid);
+            by.fill(any, edge, false, tid);
             count_values(row, by, ask, wave, lane);
             edged = edge_by_value(by, ask, edge, tied, part, s, wave, lane);
             if (!edged) {
@@ -979,19 +1039,17 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
     } else {
         const auto of = [&](u64 sum) { return target_of(ask.u, sum); };
         if constexpr (kValues) {
-            u64 unused;
-            if (part)
-                edge.last = locate(row, each_of(row, [&](int, float x) { return (u64)(x == edge.value); }),
-                                   [&](u64) { return tied - 1; }, &unused, s, wave, lane);
             const ByValue by(s, top, top - (shift + 2) * 0.6931472f * temperature);
-            by.fill(ask, edge, tid);
+            by.fill(ask, edge, part, tid);
+            const u64 each = part ? ask.weights(edge.value) : 0;
+            const Tied at_edge = {tied, each >= ask.least ? each : 0};
             // (min_p above 1: `first` alone)
             token = ask.least > 1ull << shift ? -1
-                                              : locate(row, KeptByValue<E>{row, by, ask, edge}, of, &total, s, wave, lane);
+                                              : locate(row, KeptByValue<E>{row, by, ask, edge, part}, at_edge, of, &total, s, wave, lane);
             if (ask.least > 1ull << shift) total = 1ull << shift;
         } else {
-            token = locate(row, each_of(row, [&](int id, float x) { return kept_weight(ask, edge, id, x); }), of, &total, s,
-                           wave, lane);
+            token = locate(row, each_of(row, [&](int id, float x) { return kept_weight(ask, edge, id, x); }), Tied{0, 0}, of,
+                           &total, s, wave, lane);
         }
     }
     if (tid == 0) {
