@@ -1061,6 +1061,11 @@ static dt_status latent_attention(const dt_latent_cache* cache, const dt_chunk* 
     a.out_stride = p->out_stride;
     a.Hq = a.G = p->Hq;
     a.by8 = cache->page_size % 8 == 0 && a.kv.slot_stride < (1 << 26);
+    // keys are below 2^30: with 2^rsh = 2^30 times the power of two from the page's
+    // size on, the product's excess stays below one part in 2^30
+    a.page_rsh = 30;
+    while ((1ll << (a.page_rsh - 30)) < cache->page_size) ++a.page_rsh;
+    a.page_mul = (uint32_t)(((1ull << a.page_rsh) + cache->page_size - 1) / cache->page_size);
     a.scale_log2 = (float)(p->scale * 1.4426950408889634074);
     a.lse = p->lse;
     return DT_OK;

@@ -50,7 +50,8 @@ struct Latent {
     static constexpr int kWeights = kBuffers * kTile;      // where the weights' two buffers begin
     static constexpr int kMaxima = kWeights + 2 * kRows * kWeightRow;      // [2][2 waves][rows] floats
     static constexpr int kOdd = kMaxima + 2 * 2 * kRows * 4;               // [4] words
-    static constexpr int kLds = kOdd + 16;
+    static constexpr int kThere = kOdd + 16;                               // [buffers][4 waves] bytes
+    static constexpr int kLds = kThere + 16;
     static constexpr int kPartial = kRows * (C + 2);       // floats of a split's partial result
     static_assert(kLds * kPerCu <= 160 * 1024, "LDS of a compute unit");
 };
@@ -75,24 +76,23 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
     const int m0 = (first_block + wr) * kRowsPerWave;
 
     // the rows whose scores this lane holds
-    struct Query {
-        int r;
-        bool node;
-        const uint32_t* mask;
-    } query[2];
+    int chunk_row[2];
     s16x8 qf[KS][2];
+    // of step 4 n + i a lane takes piece 16 n + 4 quad + i: eight lanes of four
+    // rows and two quads, as the LDS reads them at once, lie in different banks
+    const auto element = [&](int s) __attribute__((always_inline)) {
+        return s < C / 32 ? (s / 4 * 16 + 4 * quad + s % 4) * 8 : C + (4 * (s - C / 32) + quad) * 8;
+    };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int mrow = m0 + 16 * i + col;
         const bool live = wr < blocks && mrow < mrows;
         const int r = live ? mrow / a.Hq : 0, h = live ? mrow - r * a.Hq : 0;
         const int64_t row = (int64_t)b * a.c.rows + r;
-        query[i].r = r;
-        query[i].node = a.c.mask && r >= lead;
-        query[i].mask = query[i].node ? a.c.mask + ((int64_t)b * a.c.n_max + r - lead) * a.c.mask_words : nullptr;
+        chunk_row[i] = r;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-            qf[s][i] = *(const s16x8*)(a.q + row * a.q_stride + (int64_t)h * kQ + 32 * s + 8 * quad);
+            qf[s][i] = *(const s16x8*)(a.q + row * a.q_stride + (int64_t)h * kQ + element(s));
     }
 
     // the tiles of the workgroup's rows, and how many of them every row sees in full
@@ -111,85 +111,72 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
 
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
 
-    // Where the keys of a tile lie, a round before their copies are issued.  Eight
-    // keys that begin at a multiple of 8 lie in one page (by8): the wave's own, and
-    // four a tile to know which are there, read by scalar loads, which the copies'
-    // counter does not wait for.  Otherwise lane l looks up key l.
+    // Where the wave's eight keys of a tile lie, a round before their copies are
+    // issued.  Eight keys that begin at a multiple of 8 lie in one page (by8), read
+    // by a scalar load, which the copies' counter does not wait for.  Otherwise
+    // lane l looks up key l mod 8.  Behind the last key it is the last one's page.
     struct Place {
-        int page, in;                                      // of the wave's eight keys (this lane's key)
-        int pages[4];                                      // of the tile's, eight each
+        int page, in;
     };
     typedef const __attribute__((address_space(4))) int32_t* Table;
     const Table table = (Table)(uintptr_t)(a.kv.page_table + (int64_t)b * a.kv.max_pages);
     const auto look_up = [&](int t) __attribute__((always_inline)) {
-        Place p = {-1, 0, {-1, -1, -1, -1}};
-        if (t >= tiles) return p;
-        const int k0 = k_first + t * S::kKeys;
-        const auto number = [&](int key) __attribute__((always_inline)) {
-            return a.kv.page_shift >= 0 ? key >> a.kv.page_shift : key / a.kv.page_size;
-        };
-        const int mine = BY8 ? k0 + 8 * wave : k0 + row32;
-        if (mine < k_end) {
-            const int at = number(mine);
-            p.page = table[at];
-            p.in = mine - at * a.kv.page_size;
-        }
-        if constexpr (BY8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (k0 + 8 * i < k_end) p.pages[i] = table[number(k0 + 8 * i)];
-        }
-        return p;
-    };
-    const auto there = [&](int page) __attribute__((always_inline)) { return page >= 0 && page < a.kv.num_pages; };
-    const auto valid_keys = [&](const Place& p, int t) __attribute__((always_inline)) {
-        if constexpr (!BY8) return (uint32_t)__ballot(there(p.page));
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w |= there(p.pages[i]) ? 0xFFu << (8 * i) : 0u;
-        const int left = k_end - (k_first + t * S::kKeys);
-        return left >= 32 ? w : (left <= 0 ? 0u : w & ((1u << left) - 1));
+        const int k0 = k_first + t * S::kKeys + 8 * wave, own = BY8 ? k0 : k0 + (lane & 7);
+        const int last = BY8 ? (k_end - 1) & ~7 : k_end - 1, key = own < last ? own : last;
+        const int at = (int)((uint64_t)(uint32_t)key * a.page_mul >> a.page_rsh);
+        return Place{table[at], key - at * a.kv.page_size};
     };
     // The copies of a tile: rows 8 wave .. 8 wave + 7; a key that is not there
-    // comes from the first slot (of its page), its score is dropped below.
+    // comes from the first slot (of its page), its score is dropped below.  They
+    // are issued one by one, between other work: the unit that takes them needs 16
+    // cycles each, and holds up a wave that issues them in a row.
     constexpr int kRotPieces = R / 8;
     const uint32_t slot_bytes = (uint32_t)(a.kv.slot_stride * 2);
     const int rot_row = lane / kRotPieces & 7, rot_piece = (lane % kRotPieces) ^ L::swizzle_rot(wave * 8 + rot_row);
-    const auto issue = [&](const Place& p, int buf) __attribute__((always_inline)) {
-        const uint32_t to = lds0 + buf * S::kTile, to_rot = to + S::kKeyTile + wave * 8 * R * 2;
+    struct Copies {
+        const char* base;                                  // BY8: of the wave's keys
+        int lo, hi;                                        // else the offset of this lane's key
+        uint32_t to, to_rot;
+    };
+    const auto begin_copies = [&](const Place& p, int t, int buf) __attribute__((always_inline)) {
+        Copies c{};
+        c.to = lds0 + buf * S::kTile;
+        c.to_rot = c.to + S::kKeyTile + wave * 8 * R * 2;
+        const bool there = p.page >= 0 && p.page < a.kv.num_pages;
+        const int64_t off = there ? p.page * a.kv.page_stride + p.in * a.kv.slot_stride : 0;
+        const int left = k_end - (k_first + t * S::kKeys + 8 * wave);      // of the wave's keys
+        uint32_t valid = left >= 8 ? 0xFFu : (left <= 0 ? 0u : (1u << left) - 1);
         if constexpr (BY8) {
-            const int64_t off = there(p.page) ? p.page * a.kv.page_stride + p.in * a.kv.slot_stride : 0;
             // (the last page's slots behind the last key are the cache's own)
-            const char* const base = (const char*)(a.kv.k + off);
-#pragma unroll
-            for (int i = 0; i < kCopies - 1; ++i) {
-                const int at = wave * (kCopies - 1) + i, row8 = i * kRpc + lane / kPieces;
-                const uint32_t piece = (lane % kPieces) ^ L::swizzle_key(wave * 8 + row8);
-                copy_to_lds(base, row8 * slot_bytes + piece * 16, to + at * 1024);
-            }
-            if (lane < 8 * kRotPieces) copy_to_lds(base + C * 2, rot_row * slot_bytes + rot_piece * 16, to_rot);
+            c.base = (const char*)(a.kv.k + off);
+            if (!there) valid = 0;
         } else {
-            const int64_t off = there(p.page) ? p.page * a.kv.page_stride + p.in * a.kv.slot_stride : 0;
-            const int lo = (int)off, hi = (int)(off >> 32);
-            const auto offset_of = [&](int trow) __attribute__((always_inline)) {
-                return (int64_t)((u64)(uint32_t)__shfl(lo, trow) | (u64)(uint32_t)__shfl(hi, trow) << 32);
-            };
-#pragma unroll
-            for (int i = 0; i < kCopies - 1; ++i) {
-                const int at = wave * (kCopies - 1) + i, trow = at * kRpc + lane / kPieces;
-                copy_to_lds(a.kv.k + offset_of(trow) + ((lane % kPieces) ^ L::swizzle_key(trow)) * 8, to + at * 1024);
-            }
-            const int64_t o = offset_of(wave * 8 + rot_row);
-            if (lane < 8 * kRotPieces) copy_to_lds(a.kv.v + o + rot_piece * 8, to_rot);
+            c.lo = (int)off;
+            c.hi = (int)(off >> 32);
+            valid &= (uint32_t)__ballot(there) & 0xFFu;
+        }
+        if (lane == 0) ((uint8_t*)(lds + S::kThere))[buf * 4 + wave] = (uint8_t)valid;
+        return c;
+    };
+    const auto copy = [&](const Copies& c, int i) __attribute__((always_inline)) {
+        const bool rot = i == kCopies - 1;
+        const int at = wave * (kCopies - 1) + i, row8 = rot ? rot_row : i * kRpc + lane / kPieces;
+        const uint32_t piece = (lane % kPieces) ^ L::swizzle_key(wave * 8 + row8);
+        if constexpr (BY8) {
+            if (!rot) copy_to_lds(c.base, row8 * slot_bytes + piece * 16, c.to + at * 1024);
+            else if (lane < 8 * kRotPieces) copy_to_lds(c.base + C * 2, rot_row * slot_bytes + rot_piece * 16, c.to_rot);
+        } else {
+            const int64_t o = (int64_t)((u64)(uint32_t)__shfl(c.lo, row8) | (u64)(uint32_t)__shfl(c.hi, row8) << 32);
+            if (!rot) copy_to_lds(a.kv.k + o + piece * 8, c.to + at * 1024);
+            else if (lane < 8 * kRotPieces) copy_to_lds(a.kv.v + o + rot_piece * 8, c.to_rot);
         }
     };
 
     // LDS addresses of this lane's pieces within a tile
     const int krow = 16 * wd + col;
-    constexpr int kKeyAddr = 4;                            // the permutation's low four bits repeat after 4 x 32 elements
-    int kaddr[kKeyAddr], raddr[R / 32];
+    int kaddr[4], raddr[R / 32];                           // (a permutation changes the low four bits of a piece's number)
 #pragma unroll
-    for (int s = 0; s < kKeyAddr; ++s) kaddr[s] = krow * C * 2 + ((4 * s + quad) ^ L::swizzle_key(krow)) * 16;
+    for (int s = 0; s < 4; ++s) kaddr[s] = krow * C * 2 + ((4 * quad + s) ^ L::swizzle_key(krow)) * 16;
 #pragma unroll
     for (int s = 0; s < R / 32; ++s) raddr[s] = S::kKeyTile + krow * R * 2 + ((4 * s + quad) ^ L::swizzle_rot(krow)) * 16;
     int vaddr[4], vaddr4[4];                               // of keys 8 half .. + 3, and of the next four
@@ -225,89 +212,102 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         return to == -INFINITY ? 1.0f : exp2f(from - to);
     };
 
-    // The tile's scores, then its weights into LDS.
-    const auto scores = [&](const char* kt, f32x4 (&s)[2]) __attribute__((always_inline)) {
+    // A tile's scores, with another tile's copies between them.  The keys are read
+    // kAhead steps (of 32 cycles) before their products.  The order is held as
+    // written: left to itself the compiler saves registers and waits for each read
+    // (64 requests' tokens of 128 heads: 290 us).
+    const auto scores = [&](const char* kt, f32x4 (&s)[2], const Copies& c) __attribute__((always_inline)) {
+        constexpr int kAhead = 6;
+        const auto key = [&](int x) __attribute__((always_inline)) {
+            return *(const s16x8*)(kt + (x < C / 32 ? kaddr[x % 4] + x / 4 * 256 : raddr[x < C / 32 ? 0 : x - C / 32]));
+        };
+        s16x8 k[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) k[x] = key(x);
         s[0] = s[1] = f32x4{};
 #pragma unroll
         for (int x = 0; x < KS; ++x) {
-            const s16x8 k = *(const s16x8*)(kt + (x < C / 32 ? kaddr[x % 4] + x / 4 * 256 : raddr[x < C / 32 ? 0 : x - C / 32]));
 #pragma unroll
-            for (int i = 0; i < 2; ++i) s[i] = mfma16(T(), k, qf[x][i], s[i]);
+            for (int i = 0; i < 2; ++i) s[i] = mfma16(T(), k[x % kAhead], qf[x][i], s[i]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (x + kAhead < KS) k[x % kAhead] = key(x + kAhead);
+            if (x % 2 == 0 && x / 2 < kCopies) copy(c, x / 2);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // a few pieces ahead, no more: the queries need the registers
-        constexpr int kAhead = 6;
-        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-        for (int x = 0; x < KS - kAhead; ++x) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, 2 * kAhead, 0);
+        static_assert((KS + 1) / 2 >= kCopies, "a copy every other step");
     };
-    const auto see_bits = [&](const Query& q, int k0) __attribute__((always_inline)) {
-        if (!q.node) {
-            const int64_t left = (int64_t)ctx + q.r + 1 - k0;
+    // Which of the 32 keys from k0 on chunk row r sees.
+    const auto see_bits = [&](int r, int k0) __attribute__((always_inline)) {
+        if (!a.c.mask || r < lead) {
+            const int64_t left = (int64_t)ctx + r + 1 - k0;
             return left <= 0 ? 0u : (left >= 32 ? ~0u : (1u << left) - 1);
         }
-        const int64_t off = (int64_t)k0 - ctx - lead;      // of the tile's first key, as a node's number
+        const int64_t off = (int64_t)k0 - ctx - lead;      // of the first key, as a node's number
         if (off <= -32) return ~0u;
+        const uint32_t* const mask = a.c.mask + ((int64_t)b * a.c.n_max + r - lead) * a.c.mask_words;
         const int64_t from = off < 0 ? 0 : off;
         const int at = (int)(from >> 5), sh = (int)(from & 31);
-        const uint32_t w0 = at < a.c.mask_words ? q.mask[at] : 0u;
-        const uint32_t w1 = at + 1 < a.c.mask_words ? q.mask[at + 1] : 0u;
+        const uint32_t w0 = at < a.c.mask_words ? mask[at] : 0u;
+        const uint32_t w1 = at + 1 < a.c.mask_words ? mask[at + 1] : 0u;
         uint32_t w = (uint32_t)(((u64)w1 << 32 | w0) >> sh);
         const int64_t left = nn - from;
         w = left <= 0 ? 0u : (left >= 32 ? w : w & ((1u << left) - 1));
         if (off < 0) w = w << -off | ((1u << -off) - 1);
         return w;
     };
-    // The largest of the tile's scores; far above what the weights are relative
-    // to, it takes its place (seldom: m may lag).
-    const auto raise = [&](const f32x4 (&s)[2]) __attribute__((always_inline)) {
-        float top[2];
-        bool far = false;
+    // Scores into weights, in kParts parts that stand between products.  The
+    // largest score, where it is far above what the weights are relative to, takes
+    // its place (m may lag, no branch).  The weights are rounded to the cache's
+    // type for the second product and summed unrounded.
+    constexpr int kParts = 8;
+    struct Weighing {
+        float top[2], base[2], sum[2];
+    };
+    const auto weigh = [&](int part, f32x4 (&s)[2], Weighing& w, int buf) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float x = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
-            const auto p16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-            x = fmaxf(__uint_as_float(p16[0]), __uint_as_float(p16[1]));
-            const auto p32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-            top[i] = fmaxf(__uint_as_float(p32[0]), __uint_as_float(p32[1])) * a.scale_log2;
-            far |= top[i] > m[i] + room(T(), m[i]);
-        }
-        if (__any(far)) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float mm = fmaxf(m[i], top[i] - lift(T(), top[i]));
-                l[i] *= factor(m[i], mm);
+            if (part == 0) {
+                w.top[i] = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+            } else if (part == 1) {
+                const auto p16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(w.top[i]), __float_as_uint(w.top[i]), false, false);
+                w.top[i] = fmaxf(__uint_as_float(p16[0]), __uint_as_float(p16[1]));
+            } else if (part == 2) {
+                const auto p32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(w.top[i]), __float_as_uint(w.top[i]), false, false);
+                w.top[i] = fmaxf(__uint_as_float(p32[0]), __uint_as_float(p32[1])) * a.scale_log2;
+            } else if (part == 3) {
+                const float mm = w.top[i] > m[i] + room(T(), m[i]) ? fmaxf(m[i], w.top[i] - lift(T(), w.top[i])) : m[i];
+                l[i] *= mm == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mm);
                 m[i] = mm;
+                w.base[i] = mm == -INFINITY ? 0.0f : mm;
+                if (quad == 0) max_of(buf, wd, 16 * i + col) = mm;
+            } else if (part < 6) {
+#pragma unroll
+                for (int x = 2 * (part - 4); x < 2 * (part - 4) + 2; ++x)
+                    s[i][x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][x], a.scale_log2, -w.base[i]));
+            } else if (part == 6) {
+                l[i] += (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
+            } else {
+                s16x4 p;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) p[x] = (short)T::put(s[i][x]);
+                *(s16x4*)(weights + buf * S::kRows * S::kWeightRow + (16 * i + col) * S::kWeightRow + 32 * wd + 8 * quad) = p;
             }
         }
     };
-    const auto weigh = [&](const f32x4 (&s)[2], int buf) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float base = m[i] == -INFINITY ? 0.0f : m[i];
-            s16x4 p;
-            float sum = 0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][x], a.scale_log2, -base));
-                sum += e;
-                p[x] = (short)T::put(e);
-            }
-            l[i] += sum;
-            *(s16x4*)(weights + buf * S::kRows * S::kWeightRow + (16 * i + col) * S::kWeightRow + 32 * wd + 8 * quad) = p;
-            if (quad == 0) max_of(buf, wd, 16 * i + col) = m[i];
-        }
+    // Tile t's weights, and what they are relative to, as the row's two waves made them.
+    struct Met {
+        s16x8 p[2];
+        float m0, m1;
     };
-    // What the two waves of a row made tile t's weights relative to becomes one,
-    // the larger: for this wave's sums and outputs, and the weights as read.
-    const auto agree = [&](int buf, s16x8 (&p)[2]) __attribute__((always_inline)) {
+    const auto meet = [&](int buf) __attribute__((always_inline)) {
         const char* const at = weights + buf * S::kRows * S::kWeightRow + row32 * S::kWeightRow + 16 * half;
-        p[0] = *(const s16x8*)at;
-        p[1] = *(const s16x8*)(at + 32);
-        const float m0 = max_of(buf, 0, row32), m1 = max_of(buf, 1, row32), mm = fmaxf(m0, m1);
+        return Met{{*(const s16x8*)at, *(const s16x8*)(at + 32)}, max_of(buf, 0, row32), max_of(buf, 1, row32)};
+    };
+    // That becomes one, the larger: for this wave's sums and outputs, and the
+    // weights as read.
+    const auto agree = [&](int buf, Met& met) __attribute__((always_inline)) {
+        s16x8 (&p)[2] = met.p;
+        const float m0 = met.m0, m1 = met.m1, mm = fmaxf(m0, m1);
         if (__any(mm > m_out || m0 != m1)) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -334,112 +334,119 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
             }
         }
     };
-    const auto products = [&](const char* vt, const s16x8 (&p)[2]) __attribute__((always_inline)) {
+    // Tile t's products, with the next tile's weights made between them (`weighs`
+    // is a type).  Neighbours are products of different sums: none waits for the
+    // one before.  Values are read kAhead products before theirs, in this order.
+    const auto products = [&](const char* vt, const s16x8 (&p)[2], f32x4 (&s)[2], int buf, auto weighs) __attribute__((always_inline)) {
+        constexpr int kAhead = 4, kSteps = 2 * ND, kEvery = kSteps >= 2 * kParts ? 2 : 1;
+        s16x8 v[kAhead];
+        Weighing w{};
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+        for (int i = 0; i < kAhead; ++i) v[i] = value(vt, i % ND, i / ND);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) o[d] = mfma(T(), value(vt, d, x), p[x], o[d]);
-    };
-    // The products with the next tile's weights (vector work) between them.
-    const auto mix = [&]() __attribute__((always_inline)) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+        for (int i = 0; i < kSteps; ++i) {
+            o[i % ND] = mfma(T(), v[i % kAhead], p[i / ND], o[i % ND]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (i + kAhead < kSteps) v[i % kAhead] = value(vt, (i + kAhead) % ND, (i + kAhead) / ND);
+            if constexpr (decltype(weighs)::value) {
+                if (i % kEvery == 0 && i / kEvery < kParts) weigh(i / kEvery, s, w, buf);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (decltype(weighs)::value) {
 #pragma unroll
-        for (int x = 0; x < 2 * ND; ++x) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+            for (int i = kSteps / kEvery; i < kParts; ++i) weigh(i, s, w, buf);
         }
     };
 
-    uint32_t valid[S::kBuffers - 2];                       // keys of the tiles whose copies are in flight, next tile first
-    Place place = look_up(0);
-#pragma unroll
-    for (int i = 0; i < S::kBuffers - 2; ++i) {
-        valid[i] = valid_keys(place, i);
-        if (i < tiles) issue(place, i);
-        place = look_up(i + 1);
-    }
+    Place place{};
     int buf = S::kBuffers - 1;                             // of tile t; t + 1 has the next one
     const auto next = [](int i) __attribute__((always_inline)) { return i + 1 == S::kBuffers ? 0 : i + 1; };
     // tile t's products and tile t + 1's weights
-    const auto round = [&](int t, auto is_masked, auto is_started) __attribute__((always_inline)) {
-        constexpr bool masked = decltype(is_masked)::value, started = decltype(is_started)::value;
-        if (S::kBuffers == 4 && t + 2 < tiles) wait_copies<kCopies>();
-        else wait_copies<0>();
+    const auto round = [&](int t, auto is_started) __attribute__((always_inline)) {
+        constexpr bool started = decltype(is_started)::value;
+        wait_copies<(S::kBuffers - 3) * kCopies>();
         __syncthreads();
-        const uint32_t now = valid[0];
         const int b1 = next(buf);
-        {
-            // the buffer that tile t - 1 has left
-            const int ahead = t + S::kBuffers - 1;
-#pragma unroll
-            for (int i = 0; i + 1 < S::kBuffers - 2; ++i) valid[i] = valid[i + 1];
-            valid[S::kBuffers - 3] = valid_keys(place, ahead);
-            if (ahead < tiles) issue(place, buf == 0 ? S::kBuffers - 1 : buf - 1);
-            place = look_up(ahead + 1);
-        }
+        Met met{};
+        if (started) met = meet(t & 1);
+        // into the buffer that tile t - 1 has left; behind the last tile, what nobody
+        // reads: every round has as many copies
+        const int ahead = t + S::kBuffers - 1;
+        const Copies c = begin_copies(place, ahead, buf == 0 ? S::kBuffers - 1 : buf - 1);
+        place = look_up(ahead + 1);
+        const uint32_t flags = ((const uint32_t*)(lds + S::kThere))[b1];
         f32x4 s[2];
-        const bool more = !masked || t + 1 < tiles;
-        if (more) scores(lds + b1 * S::kTile, s);
-        if constexpr (masked) {
-            if (more) {
-                // A row's weight for a key it does not see is 0, but 0 times an
-                // infinity or NaN is not: latents with such elements are found,
-                // rows that see them become NaN, and the elements 0 (the scores
-                // of all waves have been made by then).
-                char* const tile = lds + b1 * S::kTile;
-                uint32_t odd = 0;
+        scores(lds + b1 * S::kTile, s, c);
+        const uint32_t now = (uint32_t)__builtin_amdgcn_readfirstlane((int)flags);
+        if (t + 1 >= whole || now != ~0u) {
+            // A row's weight for a key it does not see is 0, but 0 times an
+            // infinity or NaN is not: latents with such elements are found,
+            // rows that see them become NaN, and the elements 0 (the scores
+            // of all waves have been made by then).
+            char* const tile = lds + b1 * S::kTile;
+            uint32_t odd = 0;
+#pragma unroll 1
+            for (int i = 0; i < 8; i += kRpc) {
+                const u32x4 v = *(const u32x4*)(tile + (wave * 8 + i) * C * 2 + lane * 16);
+                const u64 hit = __ballot(odd_value<T>(v[0]) || odd_value<T>(v[1]) || odd_value<T>(v[2]) || odd_value<T>(v[3]));
+                if (kRpc == 1) odd |= (hit != 0 ? 1u : 0u) << i;
+                else odd |= ((uint32_t)hit != 0 ? 1u : 0u) << i | (hit >> 32 != 0 ? 2u : 0u) << i;
+            }
+            uint32_t* const odds = (uint32_t*)(lds + S::kOdd);
+            if (lane == 0) odds[wave] = odd;
+            __syncthreads();
+            const uint32_t any_odd = odds[0] | odds[1] << 8 | odds[2] << 16 | odds[3] << 24;
+            if (odd) {
 #pragma unroll 1
                 for (int i = 0; i < 8; i += kRpc) {
-                    const u32x4 v = *(const u32x4*)(tile + (wave * 8 + i) * C * 2 + lane * 16);
-                    const u64 hit = __ballot(odd_value<T>(v[0]) || odd_value<T>(v[1]) || odd_value<T>(v[2]) || odd_value<T>(v[3]));
-                    if (kRpc == 1) odd |= (hit != 0 ? 1u : 0u) << i;
-                    else odd |= ((uint32_t)hit != 0 ? 1u : 0u) << i | (hit >> 32 != 0 ? 2u : 0u) << i;
+                    uint16_t* const v = (uint16_t*)(tile + (wave * 8 + i) * C * 2 + lane * 16);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if ((v[e] & T::kExponent) == T::kExponent) v[e] = 0;
                 }
-                uint32_t* const odds = (uint32_t*)(lds + S::kOdd);
-                if (lane == 0) odds[wave] = odd;
-                __syncthreads();
-                const uint32_t any_odd = odds[0] | odds[1] << 8 | odds[2] << 16 | odds[3] << 24;
-                if (odd) {
-#pragma unroll 1
-                    for (int i = 0; i < 8; i += kRpc) {
-                        uint16_t* const v = (uint16_t*)(tile + (wave * 8 + i) * C * 2 + lane * 16);
+            }
+            const int k0 = k_first + (t + 1) * S::kKeys;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if ((v[e] & T::kExponent) == T::kExponent) v[e] = 0;
-                    }
-                }
-                const int k0 = k_first + (t + 1) * S::kKeys;
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t see = see_bits(chunk_row[i], k0) & now;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t see = see_bits(query[i], k0) & now;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int key = 16 * wd + 4 * quad + x;
-                        if (!(see >> key & 1)) s[i][x] = -INFINITY;
-                        else if (any_odd >> key & 1) s[i][x] = NAN;
-                    }
+                for (int x = 0; x < 4; ++x) {
+                    const int key = 16 * wd + 4 * quad + x;
+                    if (!(see >> key & 1)) s[i][x] = -INFINITY;
+                    else if (any_odd >> key & 1) s[i][x] = NAN;
                 }
             }
         }
-        s16x8 p[2];
-        if (started) agree(t & 1, p);
-        if (more) raise(s);
-        if (started) products(lds + buf * S::kTile, p);
-        if (more) weigh(s, (t + 1) & 1);
-        if (!masked && started) mix();
+        if (started) agree(t & 1, met);
+        if constexpr (started) {
+            products(lds + buf * S::kTile, met.p, s, (t + 1) & 1, True());
+        } else {
+            Weighing w{};
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) weigh(i, s, w, (t + 1) & 1);
+        }
         buf = b1;
     };
-    int t = -1;
     if (tiles > 0) {
-        if (whole > 0 && valid[0] == ~0u) {
-            round(t, False(), False());
-            for (++t; t + 1 < whole && valid[0] == ~0u; ++t) round(t, False(), True());
-        } else {
-            round(t, True(), False());
-            ++t;
+        place = look_up(0);
+#pragma unroll
+        for (int i = 0; i < S::kBuffers - 2; ++i) {
+            const Copies c = begin_copies(place, i, i);
+#pragma unroll
+            for (int x = 0; x < kCopies; ++x) copy(c, x);
+            place = look_up(i + 1);
         }
-        for (; t < tiles; ++t) round(t, True(), True());
+        round(-1, False());
+        for (int t = 0; t + 1 < tiles; ++t) round(t, True());
+        // the last tile's products
+        wait_copies<0>();
+        __syncthreads();
+        Met met = meet((tiles - 1) & 1);
+        agree((tiles - 1) & 1, met);
+        f32x4 none[2] = {};
+        products(lds + buf * S::kTile, met.p, none, 0, False());
     }
     // the sums of a row's weights: of the lanes, then of the two waves
 #pragma unroll

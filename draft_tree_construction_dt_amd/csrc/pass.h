@@ -59,6 +59,8 @@ struct AttentionArgs {
     // keys and values made from them, [B][Hq][made_keys][key, value]
     const uint16_t* made;
     int made_keys;
+    uint32_t page_mul;             // key / page_size = key * page_mul >> page_rsh
+    int page_rsh;
 };
 
 // One layer of a cache of latents: kv.k points at them, kv.v at their rotated parts.
