@@ -50,8 +50,8 @@ struct Latent {
     static constexpr int kWeights = kBuffers * kTile;      // where the weights' two buffers begin
     static constexpr int kMaxima = kWeights + 2 * kRows * kWeightRow;      // [2][2 waves][rows] floats
     static constexpr int kOdd = kMaxima + 2 * 2 * kRows * 4;               // [4] words
-    static constexpr int kThere = kOdd + 16;                               // [buffers][4 waves] bytes
-    static constexpr int kLds = kThere + 16;
+    static constexpr int kThere = kOdd + 16;                               // [2][up to 64 tiles][4 waves] bytes
+    static constexpr int kLds = kThere + 512;
     static constexpr int kPartial = kRows * (C + 2);       // floats of a split's partial result
     static_assert(kLds * kPerCu <= 160 * 1024, "LDS of a compute unit");
 };
@@ -111,20 +111,35 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
 
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
 
-    // Where the wave's eight keys of a tile lie, a round before their copies are
-    // issued.  Eight keys that begin at a multiple of 8 lie in one page (by8), read
-    // by a scalar load, which the copies' counter does not wait for.  Otherwise
-    // lane l looks up key l mod 8.  Behind the last key it is the last one's page.
-    struct Place {
-        int page, in;
-    };
-    typedef const __attribute__((address_space(4))) int32_t* Table;
-    const Table table = (Table)(uintptr_t)(a.kv.page_table + (int64_t)b * a.kv.max_pages);
-    const auto look_up = [&](int t) __attribute__((always_inline)) {
-        const int k0 = k_first + t * S::kKeys + 8 * wave, own = BY8 ? k0 : k0 + (lane & 7);
-        const int last = BY8 ? (k_end - 1) & ~7 : k_end - 1, key = own < last ? own : last;
+    // Where the wave's eight keys of a tile lie.  Eight keys that begin at a
+    // multiple of 8 lie in one page (BY8): a lane holds this for one of 64 tiles.
+    // Otherwise it does so for one key of 8 tiles.  The bytes in LDS say which keys
+    // are there; behind the last key the offset is the last one's.  (An entry a
+    // round, by a scalar load, made every round wait for it.)
+    constexpr int kNoLoads = 0x0F70;                       // s_waitcnt's vmcnt(0)
+    constexpr int kWindow = BY8 ? 64 : 8;
+    uint32_t off_lo = 0, off_hi = 0;
+    const auto look_up = [&](int window) __attribute__((always_inline)) {
+        const int k0 = k_first + (window * kWindow + (BY8 ? lane : lane >> 3)) * S::kKeys + 8 * wave;
+        const int own = BY8 ? k0 : k0 + (lane & 7), last = BY8 ? (k_end - 1) & ~7 : k_end - 1, key = own < last ? own : last;
         const int at = (int)((uint64_t)(uint32_t)key * a.page_mul >> a.page_rsh);
-        return Place{table[at], key - at * a.kv.page_size};
+        const int page = a.kv.page_table[(int64_t)b * a.kv.max_pages + at];
+        const bool there = page >= 0 && page < a.kv.num_pages;
+        const int64_t off = there ? page * a.kv.page_stride + (key - at * a.kv.page_size) * a.kv.slot_stride : 0;
+        off_lo = (uint32_t)off;
+        off_hi = (uint32_t)(off >> 32);
+        uint8_t* const to = (uint8_t*)(lds + S::kThere + (window & 1) * 256) + wave;
+        if constexpr (BY8) {
+            const int left = k_end - k0;                   // of the wave's keys
+            const uint32_t valid = left >= 8 ? 0xFFu : (left <= 0 ? 0u : (1u << left) - 1);
+            to[4 * lane] = there ? (uint8_t)valid : 0;     // (the last page's slots behind the last key are the cache's own)
+        } else {
+            const u64 valid = __ballot(there && own < k_end);
+            if ((lane & 7) == 0) to[4 * (lane >> 3)] = (uint8_t)(valid >> lane);
+        }
+    };
+    const auto there_of = [&](int t) __attribute__((always_inline)) {
+        return ((const uint32_t*)(lds + S::kThere))[(t / kWindow & 1) * 64 + t % kWindow];
     };
     // The copies of a tile: rows 8 wave .. 8 wave + 7; a key that is not there
     // comes from the first slot (of its page), its score is dropped below.  They
@@ -135,40 +150,32 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
     const int rot_row = lane / kRotPieces & 7, rot_piece = (lane % kRotPieces) ^ L::swizzle_rot(wave * 8 + rot_row);
     struct Copies {
         const char* base;                                  // BY8: of the wave's keys
-        int lo, hi;                                        // else the offset of this lane's key
-        uint32_t to, to_rot;
+        int in;                                            // else where in the window the tile is
+        uint32_t to;
     };
-    const auto begin_copies = [&](const Place& p, int t, int buf) __attribute__((always_inline)) {
+    const auto begin_copies = [&](int t, int buf) __attribute__((always_inline)) {
         Copies c{};
         c.to = lds0 + buf * S::kTile;
-        c.to_rot = c.to + S::kKeyTile + wave * 8 * R * 2;
-        const bool there = p.page >= 0 && p.page < a.kv.num_pages;
-        const int64_t off = there ? p.page * a.kv.page_stride + p.in * a.kv.slot_stride : 0;
-        const int left = k_end - (k_first + t * S::kKeys + 8 * wave);      // of the wave's keys
-        uint32_t valid = left >= 8 ? 0xFFu : (left <= 0 ? 0u : (1u << left) - 1);
+        c.in = t % kWindow;
         if constexpr (BY8) {
-            // (the last page's slots behind the last key are the cache's own)
-            c.base = (const char*)(a.kv.k + off);
-            if (!there) valid = 0;
-        } else {
-            c.lo = (int)off;
-            c.hi = (int)(off >> 32);
-            valid &= (uint32_t)__ballot(there) & 0xFFu;
+            const uint32_t lo = __builtin_amdgcn_readlane(off_lo, c.in), hi = __builtin_amdgcn_readlane(off_hi, c.in);
+            c.base = (const char*)(a.kv.k + (int64_t)((u64)hi << 32 | lo));
         }
-        if (lane == 0) ((uint8_t*)(lds + S::kThere))[buf * 4 + wave] = (uint8_t)valid;
         return c;
     };
     const auto copy = [&](const Copies& c, int i) __attribute__((always_inline)) {
         const bool rot = i == kCopies - 1;
         const int at = wave * (kCopies - 1) + i, row8 = rot ? rot_row : i * kRpc + lane / kPieces;
         const uint32_t piece = (lane % kPieces) ^ L::swizzle_key(wave * 8 + row8);
+        const uint32_t to = rot ? c.to + S::kKeyTile + wave * 8 * R * 2 : c.to + at * 1024;
         if constexpr (BY8) {
-            if (!rot) copy_to_lds(c.base, row8 * slot_bytes + piece * 16, c.to + at * 1024);
-            else if (lane < 8 * kRotPieces) copy_to_lds(c.base + C * 2, rot_row * slot_bytes + rot_piece * 16, c.to_rot);
+            if (!rot) copy_to_lds(c.base, row8 * slot_bytes + piece * 16, to);
+            else if (lane < 8 * kRotPieces) copy_to_lds(c.base + C * 2, rot_row * slot_bytes + rot_piece * 16, to);
         } else {
-            const int64_t o = (int64_t)((u64)(uint32_t)__shfl(c.lo, row8) | (u64)(uint32_t)__shfl(c.hi, row8) << 32);
-            if (!rot) copy_to_lds(a.kv.k + o + piece * 8, c.to + at * 1024);
-            else if (lane < 8 * kRotPieces) copy_to_lds(a.kv.v + o + rot_piece * 8, c.to_rot);
+            const int from = 8 * c.in + row8;
+            const int64_t o = (int64_t)((u64)(uint32_t)__shfl((int)off_lo, from) | (u64)(uint32_t)__shfl((int)off_hi, from) << 32);
+            if (!rot) copy_to_lds(a.kv.k + o + piece * 8, to);
+            else if (lane < 8 * kRotPieces) copy_to_lds(a.kv.v + o + rot_piece * 8, to);
         }
     };
 
@@ -212,10 +219,11 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         return to == -INFINITY ? 1.0f : exp2f(from - to);
     };
 
-    // A tile's scores, with another tile's copies between them.  The keys are read
+    // A tile's scores, with some of another tile's copies between them.  The keys are read
     // kAhead steps (of 32 cycles) before their products.  The order is held as
     // written: left to itself the compiler saves registers and waits for each read
     // (64 requests' tokens of 128 heads: 290 us).
+    constexpr int kEarly = (KS + 3) / 4 < kCopies ? (KS + 3) / 4 : kCopies;
     const auto scores = [&](const char* kt, f32x4 (&s)[2], const Copies& c) __attribute__((always_inline)) {
         constexpr int kAhead = 6;
         const auto key = [&](int x) __attribute__((always_inline)) {
@@ -231,10 +239,9 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
             for (int i = 0; i < 2; ++i) s[i] = mfma16(T(), k[x % kAhead], qf[x][i], s[i]);
             __builtin_amdgcn_sched_barrier(0);
             if (x + kAhead < KS) k[x % kAhead] = key(x + kAhead);
-            if (x % 2 == 0 && x / 2 < kCopies) copy(c, x / 2);
+            if (x % 4 == 0 && x / 4 < kEarly) copy(c, x / 4);
             __builtin_amdgcn_sched_barrier(0);
         }
-        static_assert((KS + 1) / 2 >= kCopies, "a copy every other step");
     };
     // Which of the 32 keys from k0 on chunk row r sees.
     const auto see_bits = [&](int r, int k0) __attribute__((always_inline)) {
@@ -337,7 +344,7 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
     // Tile t's products, with the next tile's weights made between them (`weighs`
     // is a type).  Neighbours are products of different sums: none waits for the
     // one before.  Values are read kAhead products before theirs, in this order.
-    const auto products = [&](const char* vt, const s16x8 (&p)[2], f32x4 (&s)[2], int buf, auto weighs) __attribute__((always_inline)) {
+    const auto products = [&](const char* vt, const s16x8 (&p)[2], f32x4 (&s)[2], int buf, const Copies& c, auto weighs) __attribute__((always_inline)) {
         constexpr int kAhead = 4, kSteps = 2 * ND, kEvery = kSteps >= 2 * kParts ? 2 : 1;
         s16x8 v[kAhead];
         Weighing w{};
@@ -351,6 +358,7 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
             if (i + kAhead < kSteps) v[i % kAhead] = value(vt, (i + kAhead) % ND, (i + kAhead) / ND);
             if constexpr (decltype(weighs)::value) {
                 if (i % kEvery == 0 && i / kEvery < kParts) weigh(i / kEvery, s, w, buf);
+                if (i % kEvery == kEvery - 1 && kEarly + i / kEvery < kCopies) copy(c, kEarly + i / kEvery);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -360,7 +368,6 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         }
     };
 
-    Place place{};
     int buf = S::kBuffers - 1;                             // of tile t; t + 1 has the next one
     const auto next = [](int i) __attribute__((always_inline)) { return i + 1 == S::kBuffers ? 0 : i + 1; };
     // tile t's products and tile t + 1's weights
@@ -368,15 +375,15 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         constexpr bool started = decltype(is_started)::value;
         wait_copies<(S::kBuffers - 3) * kCopies>();
         __syncthreads();
-        const int b1 = next(buf);
+        const int b1 = next(buf), before = buf == 0 ? S::kBuffers - 1 : buf - 1;
         Met met{};
         if (started) met = meet(t & 1);
         // into the buffer that tile t - 1 has left; behind the last tile, what nobody
         // reads: every round has as many copies
         const int ahead = t + S::kBuffers - 1;
-        const Copies c = begin_copies(place, ahead, buf == 0 ? S::kBuffers - 1 : buf - 1);
-        place = look_up(ahead + 1);
-        const uint32_t flags = ((const uint32_t*)(lds + S::kThere))[b1];
+        if (ahead % kWindow == 0) look_up(ahead / kWindow);
+        const Copies c = begin_copies(ahead, before);
+        const uint32_t flags = there_of(t + 1);
         f32x4 s[2];
         scores(lds + b1 * S::kTile, s, c);
         const uint32_t now = (uint32_t)__builtin_amdgcn_readfirstlane((int)flags);
@@ -418,11 +425,17 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
                     else if (any_odd >> key & 1) s[i][x] = NAN;
                 }
             }
+            // The loads of the mask end here: a path on which the compiler takes
+            // one to be under way has it wait for all copies behind this block, in
+            // every round (1100 cycles of 4000).
+            __builtin_amdgcn_s_waitcnt(kNoLoads);
         }
         if (started) agree(t & 1, met);
         if constexpr (started) {
-            products(lds + buf * S::kTile, met.p, s, (t + 1) & 1, True());
+            products(lds + buf * S::kTile, met.p, s, (t + 1) & 1, c, True());
         } else {
+#pragma unroll
+            for (int i = kEarly; i < kCopies; ++i) copy(c, i);
             Weighing w{};
 #pragma unroll
             for (int i = 0; i < kParts; ++i) weigh(i, s, w, (t + 1) & 1);
@@ -430,13 +443,12 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         buf = b1;
     };
     if (tiles > 0) {
-        place = look_up(0);
+        look_up(0);
 #pragma unroll
         for (int i = 0; i < S::kBuffers - 2; ++i) {
-            const Copies c = begin_copies(place, i, i);
+            const Copies c = begin_copies(i, i);
 #pragma unroll
             for (int x = 0; x < kCopies; ++x) copy(c, x);
-            place = look_up(i + 1);
         }
         round(-1, False());
         for (int t = 0; t + 1 < tiles; ++t) round(t, True());
@@ -446,7 +458,7 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         Met met = meet((tiles - 1) & 1);
         agree((tiles - 1) & 1, met);
         f32x4 none[2] = {};
-        products(lds + buf * S::kTile, met.p, none, 0, False());
+        products(lds + buf * S::kTile, met.p, none, 0, Copies{}, False());
     }
     // the sums of a row's weights: of the lanes, then of the two waves
 #pragma unroll
