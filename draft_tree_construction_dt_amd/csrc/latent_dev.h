@@ -214,7 +214,9 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d] = f32x16{};
     float m_out = -INFINITY;                               // what row32's outputs are relative to (units of log2)
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};    // the same for the scores' rows; sums of this lane's keys
+    // the same for the scores' rows, as it is taken from scores, and from where on
+    // it is raised; sums of this lane's keys
+    float m[2] = {-INFINITY, -INFINITY}, base[2] = {0, 0}, limit[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
     const auto factor = [](float from, float to) __attribute__((always_inline)) {      // 2^(from - to), from <= to
         return to == -INFINITY ? 1.0f : exp2f(from - to);
     };
@@ -232,16 +234,18 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         s16x8 k[kAhead];
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) k[x] = key(x);
-        s[0] = s[1] = f32x4{};
+        f32x4 part[2][2] = {};                             // (of even and odd steps: a product a chain is under way)
 #pragma unroll
         for (int x = 0; x < KS; ++x) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) s[i] = mfma16(T(), k[x % kAhead], qf[x][i], s[i]);
+            for (int i = 0; i < 2; ++i) part[x % 2][i] = mfma16(T(), k[x % kAhead], qf[x][i], part[x % 2][i]);
             __builtin_amdgcn_sched_barrier(0);
             if (x + kAhead < KS) k[x % kAhead] = key(x + kAhead);
             if (x % 4 == 0 && x / 4 < kEarly) copy(c, x / 4);
             __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s[i] = part[0][i] + part[1][i];
     };
     // Which of the 32 keys from k0 on chunk row r sees.
     const auto see_bits = [&](int r, int k0) __attribute__((always_inline)) {
@@ -262,43 +266,47 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         if (off < 0) w = w << -off | ((1u << -off) - 1);
         return w;
     };
-    // Scores into weights, in kParts parts that stand between products.  The
-    // largest score, where it is far above what the weights are relative to, takes
-    // its place (m may lag, no branch).  The weights are rounded to the cache's
-    // type for the second product and summed unrounded.
-    constexpr int kParts = 8;
-    struct Weighing {
-        float top[2], base[2], sum[2];
+    // What a row's weights are relative to lags behind its largest score, so that a
+    // tile of ordinary scores needs no maximum over lanes and no branch: a lane's
+    // four scores are compared with the limit, and where one passes it, in any
+    // row of the wave, the rows' largest scores take their place.
+    const auto top_of = [&](const f32x4& s) __attribute__((always_inline)) {
+        return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])) * a.scale_log2;
     };
-    const auto weigh = [&](int part, f32x4 (&s)[2], Weighing& w, int buf) __attribute__((always_inline)) {
+    const auto set = [&](int i, float to) __attribute__((always_inline)) {
+        m[i] = to;
+        base[i] = to == -INFINITY ? 0.0f : to;
+        limit[i] = to + room(T(), to);
+    };
+    const auto raise = [&](const f32x4 (&s)[2]) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (part == 0) {
-                w.top[i] = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
-            } else if (part == 1) {
-                const auto p16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(w.top[i]), __float_as_uint(w.top[i]), false, false);
-                w.top[i] = fmaxf(__uint_as_float(p16[0]), __uint_as_float(p16[1]));
-            } else if (part == 2) {
-                const auto p32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(w.top[i]), __float_as_uint(w.top[i]), false, false);
-                w.top[i] = fmaxf(__uint_as_float(p32[0]), __uint_as_float(p32[1])) * a.scale_log2;
-            } else if (part == 3) {
-                const float mm = w.top[i] > m[i] + room(T(), m[i]) ? fmaxf(m[i], w.top[i] - lift(T(), w.top[i])) : m[i];
-                l[i] *= mm == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mm);
-                m[i] = mm;
-                w.base[i] = mm == -INFINITY ? 0.0f : mm;
-                if (quad == 0) max_of(buf, wd, 16 * i + col) = mm;
-            } else if (part < 6) {
+            float top = top_of(s[i]);
+            const auto p16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+            top = fmaxf(__uint_as_float(p16[0]), __uint_as_float(p16[1]));
+            const auto p32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+            top = fmaxf(__uint_as_float(p32[0]), __uint_as_float(p32[1]));
+            const float to = top > limit[i] ? fmaxf(m[i], top - lift(T(), top)) : m[i];
+            l[i] *= factor(m[i], to);
+            set(i, to);
+        }
+    };
+    // Scores into weights, in kParts parts that stand between products.  The
+    // weights are rounded to the cache's type for the second product and summed
+    // unrounded.
+    constexpr int kParts = 12;
+    const auto weigh = [&](int part, f32x4 (&s)[2], int buf) __attribute__((always_inline)) {
+        const int i = part & 1, x = part >> 1, row = 16 * i + col;
+        if (part < 8) {
+            s[i][x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][x], a.scale_log2, -base[i]));
+        } else if (part < 10) {
+            l[i] += (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
+            max_of(buf, wd, row) = m[i];                   // (by four lanes)
+        } else {
+            s16x4 p;
 #pragma unroll
-                for (int x = 2 * (part - 4); x < 2 * (part - 4) + 2; ++x)
-                    s[i][x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][x], a.scale_log2, -w.base[i]));
-            } else if (part == 6) {
-                l[i] += (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
-            } else {
-                s16x4 p;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) p[x] = (short)T::put(s[i][x]);
-                *(s16x4*)(weights + buf * S::kRows * S::kWeightRow + (16 * i + col) * S::kWeightRow + 32 * wd + 8 * quad) = p;
-            }
+            for (int e = 0; e < 4; ++e) p[e] = (short)T::put(s[i][e]);
+            *(s16x4*)(weights + buf * S::kRows * S::kWeightRow + row * S::kWeightRow + 32 * wd + 8 * quad) = p;
         }
     };
     // Tile t's weights, and what they are relative to, as the row's two waves made them.
@@ -315,39 +323,37 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
     const auto agree = [&](int buf, Met& met) __attribute__((always_inline)) {
         s16x8 (&p)[2] = met.p;
         const float m0 = met.m0, m1 = met.m1, mm = fmaxf(m0, m1);
-        if (__any(mm > m_out || m0 != m1)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float both = fmaxf(max_of(buf, 0, 16 * i + col), max_of(buf, 1, 16 * i + col));
-                l[i] *= factor(m[i], both);
-                m[i] = both;
-            }
-            const float w = factor(m_out, mm);
-            m_out = mm;
+        for (int i = 0; i < 2; ++i) {
+            const float both = fmaxf(max_of(buf, 0, 16 * i + col), max_of(buf, 1, 16 * i + col));
+            l[i] *= factor(m[i], both);
+            set(i, both);
+        }
+        const float w = factor(m_out, mm);
+        m_out = mm;
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                // (an accumulator at a time through vector registers: the queries need the others)
-                if constexpr (S::kPerCu == 1) asm volatile("" : "+a"(o[d]));
+        for (int d = 0; d < ND; ++d) {
+            // (an accumulator at a time through vector registers: the queries need the others)
+            if constexpr (S::kPerCu == 1) asm volatile("" : "+a"(o[d]));
 #pragma unroll
-                for (int x = 0; x < 16; ++x) o[d][x] *= w;
-                if constexpr (S::kPerCu == 1) asm volatile("" : "+a"(o[d]));
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int x = 0; x < 16; ++x) o[d][x] *= w;
+            if constexpr (S::kPerCu == 1) asm volatile("" : "+a"(o[d]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float f = factor(x ? m1 : m0, mm);
+        for (int x = 0; x < 2; ++x) {
+            const float f = factor(x ? m1 : m0, mm);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[x][e] = (short)T::put(T::get((uint16_t)p[x][e]) * f);
-            }
+            for (int e = 0; e < 8; ++e) p[x][e] = (short)T::put(T::get((uint16_t)p[x][e]) * f);
         }
     };
     // Tile t's products, with the next tile's weights made between them (`weighs`
     // is a type).  Neighbours are products of different sums: none waits for the
     // one before.  Values are read kAhead products before theirs, in this order.
     const auto products = [&](const char* vt, const s16x8 (&p)[2], f32x4 (&s)[2], int buf, const Copies& c, auto weighs) __attribute__((always_inline)) {
-        constexpr int kAhead = 4, kSteps = 2 * ND, kEvery = kSteps >= 2 * kParts ? 2 : 1;
+        constexpr int kAhead = 4, kSteps = 2 * ND, kEach = (kParts + kSteps - 1) / kSteps, kEvery = kSteps / (kCopies - kEarly + 1);
+        static_assert(kEvery > 0, "a step for each copy");
         s16x8 v[kAhead];
-        Weighing w{};
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) v[i] = value(vt, i % ND, i / ND);
         __builtin_amdgcn_sched_barrier(0);
@@ -357,14 +363,11 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
             __builtin_amdgcn_sched_barrier(0);
             if (i + kAhead < kSteps) v[i % kAhead] = value(vt, (i + kAhead) % ND, (i + kAhead) / ND);
             if constexpr (decltype(weighs)::value) {
-                if (i % kEvery == 0 && i / kEvery < kParts) weigh(i / kEvery, s, w, buf);
+#pragma unroll
+                for (int part = i * kEach; part < (i + 1) * kEach && part < kParts; ++part) weigh(part, s, buf);
                 if (i % kEvery == kEvery - 1 && kEarly + i / kEvery < kCopies) copy(c, kEarly + i / kEvery);
             }
             __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (decltype(weighs)::value) {
-#pragma unroll
-            for (int i = kSteps / kEvery; i < kParts; ++i) weigh(i, s, w, buf);
         }
     };
 
@@ -381,64 +384,69 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         // into the buffer that tile t - 1 has left; behind the last tile, what nobody
         // reads: every round has as many copies
         const int ahead = t + S::kBuffers - 1;
-        if (ahead % kWindow == 0) look_up(ahead / kWindow);
+        if (__builtin_expect(ahead % kWindow == 0, 0)) look_up(ahead / kWindow);
         const Copies c = begin_copies(ahead, before);
         const uint32_t flags = there_of(t + 1);
         f32x4 s[2];
         scores(lds + b1 * S::kTile, s, c);
         const uint32_t now = (uint32_t)__builtin_amdgcn_readfirstlane((int)flags);
-        if (t + 1 >= whole || now != ~0u) {
-            // A row's weight for a key it does not see is 0, but 0 times an
-            // infinity or NaN is not: latents with such elements are found,
-            // rows that see them become NaN, and the elements 0 (the scores
-            // of all waves have been made by then).
-            char* const tile = lds + b1 * S::kTile;
-            uint32_t odd = 0;
-#pragma unroll 1
-            for (int i = 0; i < 8; i += kRpc) {
-                const u32x4 v = *(const u32x4*)(tile + (wave * 8 + i) * C * 2 + lane * 16);
-                const u64 hit = __ballot(odd_value<T>(v[0]) || odd_value<T>(v[1]) || odd_value<T>(v[2]) || odd_value<T>(v[3]));
-                if (kRpc == 1) odd |= (hit != 0 ? 1u : 0u) << i;
-                else odd |= ((uint32_t)hit != 0 ? 1u : 0u) << i | (hit >> 32 != 0 ? 2u : 0u) << i;
-            }
-            uint32_t* const odds = (uint32_t*)(lds + S::kOdd);
-            if (lane == 0) odds[wave] = odd;
-            __syncthreads();
-            const uint32_t any_odd = odds[0] | odds[1] << 8 | odds[2] << 16 | odds[3] << 24;
-            if (odd) {
+        // (one branch for all that a tile may need besides; __any's value is the wave's)
+        const bool masked = t + 1 >= whole || now != ~0u;
+        const bool moved = (met.m0 != met.m1) | (met.m0 > m_out) | (top_of(s[0]) > limit[0]) | (top_of(s[1]) > limit[1]);
+        if (__builtin_expect(masked || __any(moved), 0)) {
+            if (masked) {
+                // A row's weight for a key it does not see is 0, but 0 times an
+                // infinity or NaN is not: latents with such elements are found,
+                // rows that see them become NaN, and the elements 0 (the scores
+                // of all waves have been made by then).
+                char* const tile = lds + b1 * S::kTile;
+                uint32_t odd = 0;
 #pragma unroll 1
                 for (int i = 0; i < 8; i += kRpc) {
-                    uint16_t* const v = (uint16_t*)(tile + (wave * 8 + i) * C * 2 + lane * 16);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if ((v[e] & T::kExponent) == T::kExponent) v[e] = 0;
+                    const u32x4 v = *(const u32x4*)(tile + (wave * 8 + i) * C * 2 + lane * 16);
+                    const u64 hit = __ballot(odd_value<T>(v[0]) || odd_value<T>(v[1]) || odd_value<T>(v[2]) || odd_value<T>(v[3]));
+                    if (kRpc == 1) odd |= (hit != 0 ? 1u : 0u) << i;
+                    else odd |= ((uint32_t)hit != 0 ? 1u : 0u) << i | (hit >> 32 != 0 ? 2u : 0u) << i;
                 }
-            }
-            const int k0 = k_first + (t + 1) * S::kKeys;
+                uint32_t* const odds = (uint32_t*)(lds + S::kOdd);
+                if (lane == 0) odds[wave] = odd;
+                __syncthreads();
+                const uint32_t any_odd = odds[0] | odds[1] << 8 | odds[2] << 16 | odds[3] << 24;
+                if (odd) {
+#pragma unroll 1
+                    for (int i = 0; i < 8; i += kRpc) {
+                        uint16_t* const v = (uint16_t*)(tile + (wave * 8 + i) * C * 2 + lane * 16);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t see = see_bits(chunk_row[i], k0) & now;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int key = 16 * wd + 4 * quad + x;
-                    if (!(see >> key & 1)) s[i][x] = -INFINITY;
-                    else if (any_odd >> key & 1) s[i][x] = NAN;
+                        for (int e = 0; e < 8; ++e)
+                            if ((v[e] & T::kExponent) == T::kExponent) v[e] = 0;
+                    }
                 }
+                const int k0 = k_first + (t + 1) * S::kKeys;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t see = see_bits(chunk_row[i], k0) & now;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int key = 16 * wd + 4 * quad + x;
+                        if (!(see >> key & 1)) s[i][x] = -INFINITY;
+                        else if (any_odd >> key & 1) s[i][x] = NAN;
+                    }
+                }
+                // The loads of the mask end here: a path on which the compiler takes
+                // one to be under way has it wait for all copies behind this block, in
+                // every round (1100 cycles of 4000).
+                __builtin_amdgcn_s_waitcnt(kNoLoads);
             }
-            // The loads of the mask end here: a path on which the compiler takes
-            // one to be under way has it wait for all copies behind this block, in
-            // every round (1100 cycles of 4000).
-            __builtin_amdgcn_s_waitcnt(kNoLoads);
+            if (started) agree(t & 1, met);
+            raise(s);
         }
-        if (started) agree(t & 1, met);
         if constexpr (started) {
             products(lds + buf * S::kTile, met.p, s, (t + 1) & 1, c, True());
         } else {
 #pragma unroll
             for (int i = kEarly; i < kCopies; ++i) copy(c, i);
-            Weighing w{};
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) weigh(i, s, w, (t + 1) & 1);
+            for (int i = 0; i < kParts; ++i) weigh(i, s, (t + 1) & 1);
         }
         buf = b1;
     };
