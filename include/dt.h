@@ -612,8 +612,9 @@ typedef struct dt_latent_params {
  * Dc (to be multiplied by the head's value weight):
  *   out = sum_j softmax_j(scale * (q_c . c_j + q_r . r_j)) c_j
  * over the slots j that the row sees, as in dt_tree_attention, as are the
- * numerics, rows that see nothing, unseen infinities and NaN, and limits.
- * q may not overlap out.  Pointers 16-byte aligned (lse 4), strides multiples
+ * numerics, rows that see nothing, unseen infinities and NaN, and limits.  An
+ * infinity or NaN in a latent that a row sees makes NaN of some or all elements
+ * of that row's results.  q may not overlap out.  Pointers 16-byte aligned (lse 4), strides multiples
  * of 8 and at least Hq times a head's elements.
  * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above, or
  *   B * (lead + n_max) * Hq >= 2^31), DT_ERR_WORKSPACE, DT_ERR_HIP. */
@@ -631,7 +632,6 @@ size_t dt_latent_workspace(const dt_latent_cache* cache, const dt_chunk* chunk, 
  * for every head h.  The keys and values are made in the workspace, 4 * Dn bytes
  * a head, request and slot below max_keys: at least the longest request's
  * ctx_len + rows for all to be seen.  Of a request without rows none are made.
- * An infinity or NaN in a latent that is seen reaches the result as NaN.
  * The rest is as in dt_latent_attention; weight is contiguous, 16-byte aligned.
  * Errors: as dt_latent_attention, and DT_ERR_UNSUPPORTED for another Dn. */
 dt_status dt_latent_prefill(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_latent_params* p);
@@ -672,9 +672,9 @@ typedef struct dt_sample_params {
  *   min_p   a token stays iff w >= min_p (the first always).
  * The token drawn is the first BY ID, of those that stay, with which the sum of
  * their w so far exceeds u times the sum of them all.  logp is the logarithm
- * of its w over that sum.  Each w is rounded to a multiple of 2^(n - 62), 2^n
- * the power of two from V on (2^-44 for V = 151936), and summed exactly, so no
- * result depends on an order.  A row whose logits are all
+ * of its w over that sum.  Each w is rounded to a multiple of 2^-s and summed
+ * exactly, so no result depends on an order; s is 62 - n, 2^n the power of two
+ * from V on, and at most 50 (44 for V = 151936).  A row whose logits are all
  * -inf gives token -1 and logp -inf.  Logits are finite or -inf; NaN and +inf
  * give an unspecified token (but a memory-safe one, in -1..V-1), and u outside
  * [0, 1) the first or the last token that stays.  Rows behind the last node are

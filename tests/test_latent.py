@@ -206,6 +206,25 @@ def chunk_on(device, ctx, lead, n_max, nn, seen=None, depths=None):
                     None if seen is None else upload(ref.pack_bits(seen), device), upload(depths, device))
 
 
+def test_every_call_goes_through_its_device(monkeypatch):
+    """The entry points that launch are called by way of their tensors' device."""
+    seen = []
+    monkeypatch.setattr(bd, "_on_device", lambda index, call, *args: seen.append((index, call.__name__)) or 0)
+    cache = bd.LatentCache(torch.zeros(2, 16, 288, dtype=BF16), torch.zeros(1, 2, dtype=torch.int32), 32)
+    chunk = bd.Chunk(torch.zeros(1, dtype=torch.int32))
+    x, q = torch.zeros(1, 1, 288, dtype=BF16), torch.zeros(1, 1, 2, 288, dtype=BF16)
+    i32 = torch.zeros(1, 1, dtype=torch.int32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    bd.dt_latent_append(cache, chunk, x[..., :256], x[..., 256:])
+    bd.dt_latent_attention(cache, chunk, q, torch.empty(1, 1, 2, 256, dtype=BF16), 1.0, workspace=ws)
+    bd.dt_latent_prefill(cache, chunk, q[..., :96].contiguous(), torch.zeros(2, 128, 256, dtype=BF16),
+                         torch.empty(1, 1, 2, 64, dtype=BF16), 1.0, 32, workspace=ws)
+    bd.dt_latent_commit(cache, chunk, None, None, i32, i32.clone(), torch.zeros(1, dtype=torch.int32))
+    bd.dt_sample_rows(torch.zeros(1, 1, 32), torch.zeros(1, 1), i32)
+    assert seen == [(-1, name) for name in ("dt_latent_append", "dt_latent_attention", "dt_latent_prefill",
+                                            "dt_latent_commit", "dt_sample_rows")]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("case", [
     dict(dtype=BF16, Dc=512, Dr=64, Hq=16, lead=1, n_max=0, nn=None, ctx=[4000], P=16),
@@ -511,6 +530,20 @@ def test_large_scores(device, size):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("P", [16, 12])
+@pytest.mark.parametrize("size", [dict(dtype=BF16, Dc=512, Dr=64), dict(dtype=F16, Dc=256, Dr=32)], ids=str)
+def test_workgroups_with_thousands_of_keys(device, size, P):
+    """So many rows that a workgroup takes all keys of its own, in pages some of
+    which are missing (a call of few rows is cut into chunks of 256 keys)."""
+    case = dict(size, Hq=128, lead=0, n_max=160, nn=[160, 151], ctx=[3000, 2411], P=P, every=40)
+    _, c, table, q, w, seen, scale = problem(case)
+    table[0, 5] = table[1, 2100 // P] = table[0, 2900 // P] = -1
+    table[1, 1030 // P] = 1 << 30
+    out, lse = run_attention(device, case, c, table, q, w, seen, scale)
+    check_attention(case, c, table, q, w, seen, scale, out, lse)
+
+
+@pytest.mark.gpu
 def test_many_requests_of_all_lengths(device):
     rs = np.random.RandomState(5)
     ctx = [int(x) for x in 900 * rs.rand(150) ** 3]
@@ -553,6 +586,46 @@ def test_cache_beyond_32_bit_offsets(device, Dn):
     for b, n in enumerate((45, 20)):
         for r in range(4):
             assert torch.equal(big[int(moved[b, (n + r) // 16]), (n + r) % 16], x[b, r])
+
+
+@pytest.mark.gpu
+def test_calls_in_flight_on_two_streams(device):
+    """Both forms on two streams at once, a workspace each, the second in a graph
+    that is replayed: every call's results are its own."""
+    jobs = []
+    for Dn in (None, 128):
+        case = dict(dtype=BF16, Dc=512, Dr=64, Hq=16, lead=1, n_max=20, nn=[20, 7, 15], ctx=[4000, 35, 812], P=16, tree=True,
+                    Dn=Dn)
+        _, c, table, q, w, seen, scale = problem(case)
+        cache = bd.LatentCache(c.to(device), upload(table, device), 64)
+        chunk = chunk_on(device, case["ctx"], 1, 20, case["nn"], seen)
+        dq, dw = q.to(device), None if w is None else w.to(device)
+        size = bd.dt_latent_workspace(cache, chunk, 16) if Dn is None else \
+            bd.dt_latent_prefill_workspace(cache, chunk, 16, Dn, 4021)
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        out = torch.zeros(3, 21, 16, Dn or 512, dtype=BF16, device=device)
+
+        def call(Dn=Dn, cache=cache, chunk=chunk, dq=dq, dw=dw, out=out, ws=ws, scale=scale):
+            if Dn is None:
+                bd.dt_latent_attention(cache, chunk, dq, out, scale, workspace=ws)
+            else:
+                bd.dt_latent_prefill(cache, chunk, dq, dw, out, scale, 4021, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        jobs.append((call, out, out.clone(), torch.cuda.Stream()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        jobs[1][0]()
+    for _ in range(3):
+        for _, out, _, _ in jobs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for call, _, _, stream in jobs:
+            with torch.cuda.stream(stream):
+                call() if call is jobs[0][0] else graph.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _ in jobs:
+            assert torch.equal(out, want)
 
 
 # ---------------------------------------------------------------------------
