@@ -17,8 +17,8 @@
 // Both share its split of the work and its join.
 //
 // Measured, expanded (bf16, C = 512, R = 64, N = 128, 32 heads, two chunks of
-// 1801-2048 rows over 6-14 K keys, 1.08 T operations): 1285 us, 844 TFLOP/s of
-// the 1402 of a large matrix product; make_kernel 364 us of it, attention 1026
+// 1801-2048 rows over 6-14 K keys, 1.08 T operations): 1240 us, 875 TFLOP/s of
+// the 1402 of a large matrix product; make_kernel 324 us of it, attention 1017
 // (matrix and vector units in turn, as with heads' own keys), the join 26.  A
 // chunk of 300 rows over 511 keys and 16 heads 41 us, three dependent launches.
 // Keys, values and weights are rounded to the cache's type: the result's error
@@ -35,11 +35,12 @@ namespace {
 
 constexpr int kMakeTile = 128;     // keys, and rows of the weight, of a workgroup
 constexpr int kMakeStep = 64;      // elements of the latents a step
+constexpr int kMadeRow = kMakeTile * 2 + 16;   // bytes of a key's results in LDS, spread over the banks
 
 // out[key][n] = sum_i W[n][i] c[key][i] for 128 keys of one request and 128 rows
 // of the weight; four waves take 64 x 64 each.  The weight's rows are the left
-// operand, so a lane ends with one key and runs of its row.  Bound by the LDS
-// reads and the waits of two buffers: 364 us for 20 K keys of 32 heads.
+// operand, so a lane ends with one key and runs of its row.  Bound by the
+// waits of two buffers: 324 us for 20 K keys of 32 heads.
 template <class T, int C, int N>
 __global__ void __launch_bounds__(256) make_kernel(AttentionArgs a, const uint16_t* weight, uint16_t* made) {
     constexpr int kTile = kMakeTile * kMakeStep * 2, kCopies = kMakeTile / 8 / 4;
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(256) make_kernel(AttentionArgs a, const uint16
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int b = blockIdx.z, n0 = blockIdx.y * kMakeTile, k0 = blockIdx.x * kMakeTile;
-    const int total = a.Hq * 2 * N;
+    static_assert(2 * N % kMakeTile == 0, "a tile of the weight is one head's");
     const Request q = request_of(a, b, 1);
     if (q.rows == 0 || k0 >= q.keys) return;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
@@ -59,8 +60,7 @@ __global__ void __launch_bounds__(256) make_kernel(AttentionArgs a, const uint16
         const int row = (wave * kCopies + i) * 8 + (lane >> 3), at = (piece ^ ((row >> 1) & 7)) * 8;
         const int64_t off = k0 + row < q.keys ? slot_offset(a.kv, b, k0 + row) : -1;
         from[i] = a.kv.k + (off < 0 ? 0 : off) + at;       // a key that is not there is not read later
-        const int n = n0 + row < total ? n0 + row : total - 1;
-        weights[i] = weight + (int64_t)n * C + at;
+        weights[i] = weight + (int64_t)(n0 + row) * C + at;
     }
     const auto issue = [&](int s) __attribute__((always_inline)) {
         const uint32_t to = lds0 + (s & 1) * kTile + wave * kCopies * 1024;
@@ -96,24 +96,27 @@ __global__ void __launch_bounds__(256) make_kernel(AttentionArgs a, const uint16
                 for (int j = 0; j < 2; ++j) o[i][j] = mfma(T(), w[i], k[j], o[i][j]);
         }
     }
+    // through LDS, so that a key's 256 bytes leave together
+    static_assert(kMakeTile * kMadeRow <= (int)sizeof(lds), "the results' tile");
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int key = k0 + wk * 64 + j * 32 + col;
-        if (key >= q.keys) continue;
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = n0 + wn * 64 + i * 32;           // (2 N is a multiple of 64: one head's)
-            if (n >= total) continue;
-            const int h = n / (2 * N);
-            uint16_t* const to = made + (((int64_t)b * a.Hq + h) * a.made_keys + key) * (2 * N) + (n - h * 2 * N) + 4 * half;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 s16x4 y;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = (short)T::put(o[i][j][4 * x + e]);
-                *(s16x4*)(to + 8 * x) = y;
+                *(s16x4*)(lds + (wk * 64 + j * 32 + col) * kMadeRow + (wn * 64 + i * 32 + 8 * x + 4 * half) * 2) = y;
             }
-        }
+    __syncthreads();
+    const int h = n0 / (2 * N);                            // (the tile's rows of the weight are one head's)
+    uint16_t* const to = made + ((int64_t)b * a.Hq + h) * a.made_keys * (2 * N) + (n0 - h * 2 * N) + (threadIdx.x & 15) * 8;
+#pragma unroll
+    for (int i = 0; i < kMakeTile / 16; ++i) {
+        const int row = i * 16 + (threadIdx.x >> 4), key = k0 + row;
+        if (key < q.keys) *(u32x4*)(to + (int64_t)key * (2 * N)) = *(const u32x4*)(lds + row * kMadeRow + (threadIdx.x & 15) * 16);
     }
 }
 
