@@ -544,6 +544,31 @@ def test_workgroups_with_thousands_of_keys(device, size, P):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Dn", [None, 64])
+def test_strides(device, Dn):
+    """Queries, results and slots inside wider buffers give the packed ones'
+    results, bit by bit, and nothing beside the results is written."""
+    case = dict(dtype=F16, Dc=256, Dr=64, Hq=5, lead=1, n_max=20, nn=[20, 11], ctx=[700, 45], P=8, tree=True, Dn=Dn)
+    _, c, table, q, w, seen, scale = problem(case)
+    out, _ = run_attention(device, case, c, table, q, w, seen, scale)
+    pool = torch.full(c.shape[1:3] + (400,), math.nan, dtype=F16, device=device)
+    pool[..., 16:336] = c[0].to(device)
+    cache, chunk = bd.LatentCache(pool[..., 16:336], upload(table, device), 64), chunk_on(device, [700, 45], 1, 20, [20, 11], seen)
+    dq = torch.full((2, 21, 7, q.shape[-1]), math.nan, dtype=F16, device=device)
+    dq[:, :, 1:6] = q.to(device)
+    wide = torch.full((2, 21, 8, Dn or 256), SENTINEL, dtype=F16, device=device)
+    if Dn is None:
+        ws = torch.empty(bd.dt_latent_workspace(cache, chunk, 5), dtype=torch.uint8, device=device)
+        bd.dt_latent_attention(cache, chunk, dq[:, :, 1:6], wide[:, :, 2:7], scale, workspace=ws)
+    else:
+        ws = torch.empty(bd.dt_latent_prefill_workspace(cache, chunk, 5, Dn, 721), dtype=torch.uint8, device=device)
+        bd.dt_latent_prefill(cache, chunk, dq[:, :, 1:6], w.to(device), wide[:, :, 2:7], scale, 721, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(wide[:, :, 2:7].cpu(), out)
+    assert (wide[:, :, :2] == SENTINEL).all() and (wide[:, :, 7:] == SENTINEL).all()
+
+
+@pytest.mark.gpu
 def test_many_requests_of_all_lengths(device):
     rs = np.random.RandomState(5)
     ctx = [int(x) for x in 900 * rs.rand(150) ** 3]
