@@ -40,7 +40,8 @@ constexpr int kMadeRow = kMakeTile * 2 + 16;   // bytes of a key's results in LD
 // out[key][n] = sum_i W[n][i] c[key][i] for 128 keys of one request and 128 rows
 // of the weight; four waves take 64 x 64 each.  The weight's rows are the left
 // operand, so a lane ends with one key and runs of its row.  Bound by the
-// waits of two buffers: 324 us for 20 K keys of 32 heads.
+// way from L2 to LDS and its waits: 324 us for 24 K keys of 32 heads (four buffers
+// of 32 elements a step instead of two of 64: the same).
 template <class T, int C, int N>
 __global__ void __launch_bounds__(256) make_kernel(AttentionArgs a, const uint16_t* weight, uint16_t* made) {
     constexpr int kTile = kMakeTile * kMakeStep * 2, kCopies = kMakeTile / 8 / 4;
