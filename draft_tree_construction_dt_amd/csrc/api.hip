@@ -1107,8 +1107,9 @@ extern "C" dt_status dt_latent_prefill(const dt_latent_cache* cache, const dt_ch
     AttentionArgs a{};
     if ((st = latent_attention(cache, chunk, p, p->Dn + cache->Dr, p->Dn, a)) != DT_OK || chunk->B == 0) return st;
     if (!p->weight || misaligned(p->weight, 16)) return DT_ERR_INVALID_ARG;
-    if (no_workspace(p->workspace, p->workspace_bytes, prefill_workspace(a.c, p->Hq, p->Dn, p->max_keys)))
-        return DT_ERR_WORKSPACE;
+    const size_t need = prefill_workspace(a.c, p->Hq, p->Dn, p->max_keys);
+    if (need == SIZE_MAX) return DT_ERR_UNSUPPORTED;
+    if (no_workspace(p->workspace, p->workspace_bytes, need)) return DT_ERR_WORKSPACE;
     a.G = 1;
     a.kv.Hkv = p->Hq;
     a.made_keys = p->max_keys;

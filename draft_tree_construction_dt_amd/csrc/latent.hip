@@ -280,8 +280,11 @@ hipError_t run_latent(const AttentionArgs& a, void* workspace, hipStream_t strea
 int prefill_tile_rows(const ChunkArgs& c) { return c.rows <= 64 ? 64 : 128; }
 constexpr int kPrefillSlots = 2 * kCus;
 
+// -1: they pass 63 bits (B and Hq alone stay below 2^31)
 int64_t made_bytes(const ChunkArgs& c, int Hq, int N, int keys) {
-    return ((int64_t)c.B * Hq * keys * 2 * N * 2 + 255) / 256 * 256;
+    int64_t n;
+    if (__builtin_mul_overflow((int64_t)c.B * Hq * 2 * N * 2, (int64_t)keys, &n) || n > INT64_MAX - 255) return -1;
+    return (n + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -308,7 +311,9 @@ hipError_t launch_latent_attention(const AttentionArgs& a, int dtype, int C, int
 
 size_t prefill_workspace(const ChunkArgs& c, int Hq, int N, int keys) {
     const int mt = prefill_tile_rows(c);
-    return (size_t)made_bytes(c, Hq, N, keys) +
+    const int64_t made = made_bytes(c, Hq, N, keys);
+    if (made < 0) return SIZE_MAX;
+    return (size_t)made +
            partial_bytes((int64_t)c.B * Hq * ((c.rows + mt - 1) / mt), kPrefillSlots, mt, N);
 }
 

@@ -142,7 +142,7 @@ hipError_t launch_latent_attention(const AttentionArgs& a, int dtype, int C, int
 size_t latent_workspace(const ChunkArgs& c, int Hq, int C);
 hipError_t launch_latent_prefill(AttentionArgs a, const void* weight, int dtype, int C, int R, int N, void* workspace,
                                  hipStream_t stream);
-size_t prefill_workspace(const ChunkArgs& c, int Hq, int N, int keys);
+size_t prefill_workspace(const ChunkArgs& c, int Hq, int N, int keys);     // SIZE_MAX: more than a buffer can have
 hipError_t launch_logits(const LogitsArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_sample(const SampleArgs& a, int dtype, void* workspace, hipStream_t stream);
 size_t sample_workspace(int64_t rows, int V, int dtype);

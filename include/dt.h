@@ -633,10 +633,12 @@ size_t dt_latent_workspace(const dt_latent_cache* cache, const dt_chunk* chunk, 
  * a head, request and slot below max_keys: at least the longest request's
  * ctx_len + rows for all to be seen.  Of a request without rows none are made.
  * The rest is as in dt_latent_attention; weight is contiguous, 16-byte aligned.
- * Errors: as dt_latent_attention, and DT_ERR_UNSUPPORTED for another Dn. */
+ * Errors: as dt_latent_attention, and DT_ERR_UNSUPPORTED for another Dn and for
+ *   keys and values of 2^63 bytes and more. */
 dt_status dt_latent_prefill(const dt_latent_cache* cache, const dt_chunk* chunk, const dt_latent_params* p);
 
-/* Bytes of workspace dt_latent_prefill needs; 0 if a call would be refused. */
+/* Bytes of workspace dt_latent_prefill needs; 0 if a call would be refused for
+ * these, but SIZE_MAX where B, Hq, Dn and max_keys ask for 2^63 bytes and more. */
 size_t dt_latent_prefill_workspace(const dt_latent_cache* cache, const dt_chunk* chunk, int32_t Hq, int32_t Dn,
                                    int32_t max_keys);
 

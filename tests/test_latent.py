@@ -144,6 +144,27 @@ def test_workspaces_and_limits_of_a_call():
     assert lib.dt_latent_prefill_workspace(ctypes.byref(_cache()), ctypes.byref(c), 3000, 128, 1 << 30) > 1 << 56
 
 
+def test_prefill_workspaces_that_no_buffer_can_have():
+    """The made keys' and values' bytes are counted exactly, and a product that
+    passes 63 bits neither wraps to a small size nor lets a call through."""
+    lib, one = bd._load(), _chunk(B=65535, lead=1, n_max=0)
+
+    def size(chunk, Hq, Dn, keys):
+        return lib.dt_latent_prefill_workspace(ctypes.byref(_cache()), ctypes.byref(chunk), Hq, Dn, keys)
+    for keys in (1 << 20, (1 << 30) - 1):
+        assert size(one, 100, 64, keys) - size(one, 100, 64, 1) == 65535 * 100 * 4 * 64 * (keys - 1)
+    # bytes 2^63 - 2^49 (which fit), 2^63, 2^64, 2^64, and some that would wrap to a middling size
+    fits = _chunk(B=16383, lead=1, n_max=0)
+    assert size(fits, 1024, 128, 1 << 30) - size(fits, 1024, 128, 1) == 16383 * 1024 * 512 * ((1 << 30) - 1)
+    for B, Hq, Dn, keys in ((16384, 1024, 128, 1 << 30), (8192, 4096, 128, 1 << 30), (16384, 4096, 64, 1 << 30),
+                            (65535, 3000, 128, 1 << 30), (65535, 4096, 128, 2 ** 31 - 1)):
+        chunk = _chunk(B=B, lead=1, n_max=0)
+        assert size(chunk, Hq, Dn, keys) == 2 ** 64 - 1
+        for room in (1 << 40, 2 ** 64 - 1):
+            p = _attn(Hq=Hq, Dn=Dn, max_keys=keys, q_stride=Hq * (Dn + 64), out_stride=Hq * Dn, workspace_bytes=room)
+            assert call("dt_latent_prefill", _cache(), chunk, p) == LIMIT
+
+
 def test_empty_batches_and_null_structs():
     cache, none, full = _cache(c=None, page_table=None), _chunk(B=0, ctx_len=None), _chunk()
     assert call("dt_latent_append", cache, none, _append(latent=None)) == bd.DT_OK
