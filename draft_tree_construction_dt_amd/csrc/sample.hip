@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t at = blockIdx.x;
     const int b = (int)(at / a.rows), r = (int)(at - (int64_t)b * a.rows);
-    if (r >= a.lead && a.n_nodes && r >= a.lead + a.n_nodes[b]) return;
+    if (r >= a.lead && a.n_nodes && r - a.lead >= a.n_nodes[b]) return;    // (any number: a sum could pass 32 bits)
     const Row<E> row(a.logits, at, a.V);
     if (tid < kTable) s.table[tid] = ldexp(exp2((double)tid / kTable), shift);
 

@@ -360,3 +360,13 @@ def test_logits_behind_32_bits(device):
         got = tokens.cpu()[0]
         assert int(got[1]) == 12345 and int(got[2]) == mid and int(got[rows - 2]) == mid
         assert int(got[rows - 1]) == V - 2
+
+
+@pytest.mark.gpu
+def test_counts_of_nodes_at_the_ends_of_their_type(device):
+    rs = np.random.RandomState(31)
+    nn = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 3, -1, 8]
+    B, rows, V = len(nn), 9, 333
+    x, u = rows_of_all_kinds(rs, B * rows, V).view(B, rows, V).float(), torch.from_numpy(rs.rand(B, rows).astype(np.float32))
+    for lead in (1, 2, 9):
+        check(x, u, *draw(device, x, u, nn=nn, lead=lead), nn=nn, lead=lead)
