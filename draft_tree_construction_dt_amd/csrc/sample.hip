@@ -47,6 +47,7 @@ constexpr int kMostK = 1000;
 constexpr int kForP = 896;
 constexpr int kTable = 64;
 constexpr int kShort = 256;        // tokens of a list whose pairs are compared
+constexpr unsigned kMaxGridX = 1 << 20;
 
 // Bits whose order is that of the values (no NaN; -0 and 0 are one).
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -887,7 +888,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
     constexpr bool kValues = sizeof(E) == 2;
     __shared__ Shared s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t at = blockIdx.x;
+    const int64_t at = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (at >= (int64_t)a.B * a.rows) return;
     const int b = (int)(at / a.rows), r = (int)(at - (int64_t)b * a.rows);
     if (r >= a.lead && a.n_nodes && r - a.lead >= a.n_nodes[b]) return;    // (any number: a sum could pass 32 bits)
     const Row<E> row(a.logits, at, a.V);
@@ -1076,9 +1078,11 @@ hipError_t launch_sample(const SampleArgs& a, int dtype, void*, hipStream_t stre
     int n = 0;
     while ((1ll << n) < a.V) ++n;
     const int shift = 62 - n < 50 ? 62 - n : 50;
-    const unsigned rows = (unsigned)((int64_t)a.B * a.rows);
-    if (dtype == DT_DTYPE_BF16) sample_kernel<uint16_t><<<rows, kThreads, 0, stream>>>(a, shift);
-    else sample_kernel<uint32_t><<<rows, kThreads, 0, stream>>>(a, shift);
+    // threads along x count in 32 bits: 2^23 rows and more take several in y
+    const unsigned rows = (unsigned)((int64_t)a.B * a.rows), x = rows < kMaxGridX ? rows : kMaxGridX;
+    const dim3 grid(x, (rows + x - 1) / x);
+    if (dtype == DT_DTYPE_BF16) sample_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(a, shift);
+    else sample_kernel<uint32_t><<<grid, kThreads, 0, stream>>>(a, shift);
     return hipGetLastError();
 }
 

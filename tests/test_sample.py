@@ -370,3 +370,24 @@ def test_counts_of_nodes_at_the_ends_of_their_type(device):
     x, u = rows_of_all_kinds(rs, B * rows, V).view(B, rows, V).float(), torch.from_numpy(rs.rand(B, rows).astype(np.float32))
     for lead in (1, 2, 9):
         check(x, u, *draw(device, x, u, nn=nn, lead=lead), nn=nn, lead=lead)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [128, 131, 256])
+def test_calls_of_so_many_rows_that_their_threads_pass_32_bits(device, B):
+    """2^23 rows and more, up to the documented 2^24: tokens of two logits."""
+    rows, lead = 65536, 3
+    g = torch.Generator(device=device).manual_seed(B)
+    x = torch.randn(B, rows, 2, generator=g, device=device)
+    u = torch.rand(B, rows, generator=g, device=device)
+    nn = torch.randint(0, rows - lead + 1, (B,), generator=g, device=device, dtype=I32)
+    nn[-1] = rows - lead
+    tokens = torch.full((B, rows), NOT_DRAWN, dtype=I32, device=device)
+    bd.dt_sample_rows(x, u, tokens, lead=lead, n_nodes=nn)
+    torch.cuda.synchronize()
+    first = 1 / (1 + torch.exp(x[..., 1].double() - x[..., 0].double()))      # the first one's share
+    drawn = torch.arange(rows, device=device)[None] < lead + nn[:, None]
+    near = drawn & ((first - u.double()).abs() < 1e-12)           # (weights are off by 2^-43, shares by little more)
+    assert int(near.sum()) < 10
+    want = torch.where(drawn, (u.double() >= first).int(), NOT_DRAWN)
+    assert ((tokens == want) | near).all()
