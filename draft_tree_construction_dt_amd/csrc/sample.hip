@@ -81,7 +81,8 @@ struct Weights {
 };
 
 // One row in memory, in groups of 16 aligned bytes; what the first and the last
-// group hold beside the row comes as -inf, and so do NaN.
+// group hold beside the row comes as -inf.  NaN come as they are from load() and
+// groups_of(), and as -inf from scan() and each(): they count as -inf everywhere.
 template <class E>
 struct Row {
     static constexpr int kEach = 16 / sizeof(E);
@@ -900,9 +901,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
     float mine = -INFINITY, second = -INFINITY;
     int where = 0;
     row.template groups_of<4>(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
-        float x = Row<E>::at(v, 0);
+        // (comparisons: fmaxf of a number and a signalling NaN is NaN)
+        float x = -INFINITY, y = -INFINITY;
 #pragma unroll
-        for (int e = 1; e < Row<E>::kEach; ++e) x = fmaxf(x, Row<E>::at(v, e));
+        for (int e = 0; e < Row<E>::kEach; e += 2) {
+            x = Row<E>::at(v, e) > x ? Row<E>::at(v, e) : x;
+            y = Row<E>::at(v, e + 1) > y ? Row<E>::at(v, e + 1) : y;
+        }
+        x = fmaxf(x, y);
         second = fmaxf(second, fminf(mine, x));
         where = x > mine ? g : where;
         mine = x > mine ? x : mine;

@@ -677,9 +677,9 @@ typedef struct dt_sample_params {
  * of its w over that sum.  Each w is rounded to a multiple of 2^-s and summed
  * exactly, so no result depends on an order; s is 62 - n, 2^n the power of two
  * from V on, and at most 50 (44 for V = 151936).  A row whose logits are all
- * -inf gives token -1 and logp -inf.  Logits are finite or -inf; NaN and +inf
- * give an unspecified token (but a memory-safe one, in -1..V-1), and u outside
- * [0, 1) the first or the last token that stays.  Rows behind the last node are
+ * -inf gives token -1 and logp -inf, and NaN counts as -inf.  +inf gives an
+ * unspecified token (but a memory-safe one, in -1..V-1), and u outside [0, 1)
+ * the first or the last token that stays.  Rows behind the last node are
  * left as they were.
  * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above),
  *   DT_ERR_WORKSPACE, DT_ERR_HIP. */

@@ -391,3 +391,27 @@ def test_calls_of_so_many_rows_that_their_threads_pass_32_bits(device, B):
     assert int(near.sum()) < 10
     want = torch.where(drawn, (u.double() >= first).int(), NOT_DRAWN)
     assert ((tokens == want) | near).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+def test_nan_counts_as_minus_infinity(device, dtype):
+    """Rows masked with NaN of all kinds, whole 16-byte groups of them among
+    them, give the tokens of rows masked with -inf."""
+    rs = np.random.RandomState(33)
+    V, rows = 32000, 12
+    how = HOW + [dict(top_k=600), dict(top_k=900, top_p=0.99), dict(top_p=0.999, temperature=3.0), dict(top_k=5000)]
+    B = len(how)
+    x = torch.from_numpy(rs.standard_normal((B, rows, V))).to(dtype)
+    gone = torch.from_numpy(np.repeat(rs.rand(B, rows, V // 16) < 0.9, 16, -1) | (rs.rand(B, rows, V) < 0.05))
+    # an exponent of ones, any fraction but 0 and any sign: quiet and signalling ones
+    fraction, ints = (7, np.int16) if dtype == BF16 else (23, np.int32)
+    bits = (255 << fraction) + rs.randint(1, 1 << fraction, x.shape) - (rs.randint(0, 2, x.shape) << (fraction + 8))
+    nan = torch.from_numpy(bits.astype(ints)).view(dtype)
+    assert torch.isnan(nan).all() and (nan.view(torch.int16 if dtype == BF16 else I32) < 0).any()
+    u = torch.from_numpy(rs.rand(B, rows).astype(np.float32))
+    how = {k: [dict(OFF, **h)[k] for h in how] for k in OFF}
+    want = draw(device, x.masked_fill(gone, -math.inf), u, **how)
+    got = draw(device, torch.where(gone, nan, x), u, **how)
+    assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
+    assert draw(device, nan, u, **how)[0].max() == -1
