@@ -801,6 +801,12 @@ __device__ __forceinline__ void count_values(const Row<E>& row, const ByValue& b
         }
     });
     __syncthreads();
+    // -0 is 0 (where magnitudes begin at 0; otherwise both are tiny)
+    if (by.base == 0 && tid == 0) {
+        by.s.v.count[0] += by.s.v.count[kMagnitudes];
+        by.s.v.count[kMagnitudes] = 0;
+    }
+    __syncthreads();
 }
 
 // The edge of top_k and top_p by the counted values; false where it is not to be

@@ -415,3 +415,24 @@ def test_nan_counts_as_minus_infinity(device, dtype):
     got = draw(device, torch.where(gone, nan, x), u, **how)
     assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
     assert draw(device, nan, u, **how)[0].max() == -1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("temperature", [1.0, 1e-30, 1e-36])
+def test_zeros_of_both_signs_are_one_value(device, dtype, temperature):
+    """They tie by id, also where the temperature is so low that nothing but
+    zeros weighs anything."""
+    rs = np.random.RandomState(34)
+    V, rows = 6000, 16
+    how = [dict(top_p=0.6), dict(top_p=0.3), dict(top_k=1700), dict(top_k=1700, top_p=0.7), dict(top_k=1700, min_p=0.5),
+           dict(top_k=5), dict(min_p=0.5), dict(top_p=0.95)]
+    B = len(how)
+    x = torch.from_numpy(np.where(rs.rand(B, rows, V) < 0.5, 0.0, -1.0)).to(dtype)
+    signed = torch.where((x == 0) & torch.from_numpy(rs.rand(B, rows, V) < 0.5), -0.0, x.float()).to(dtype)
+    u = ((torch.arange(rows) + 0.5) / rows).expand(B, rows).contiguous()
+    how = dict({k: [dict(OFF, **h)[k] for h in how] for k in OFF}, temperature=[temperature] * B)
+    want = draw(device, x, u, **how)
+    got = draw(device, signed, u, **how)
+    assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
+    check(signed, u, *got, **how)
