@@ -564,6 +564,33 @@ def test_workgroups_with_thousands_of_keys(device, size, P):
     check_attention(case, c, table, q, w, seen, scale, out, lse)
 
 
+WIDE = [
+    dict(lead=1, n_max=64, nn=[64, 33, 0], ctx=[1500, 31, 2], P=16, tree=True, every=5),   # the benchmark's budget
+    dict(lead=1, n_max=64, nn=[63, 64, 32], ctx=[700, 15, 96], P=32, tree="odd", every=5),
+    dict(lead=3, n_max=100, nn=[100, 65], ctx=[29, 2111], P=24, tree="odd", every=9),      # four words
+    dict(lead=0, n_max=129, nn=[129, 96], ctx=[1, 333], P=12, tree="odd", every=11),       # five, of rows that see nothing, too
+    dict(lead=1, n_max=300, nn=[300, 257], ctx=[900, 0], P=16, tree=True, every=41),
+    dict(lead=2, n_max=1024, nn=[1024, 800], ctx=[61, 130], P=64, tree="odd", every=151),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [dict(dtype=BF16, Dc=512, Dr=64, Hq=128), dict(dtype=F16, Dc=256, Dr=32, Hq=7),
+                                  dict(dtype=BF16, Dc=512, Dr=64, Hq=6, Dn=128), dict(dtype=F16, Dc=256, Dr=32, Hq=3, Dn=64)],
+                         ids=str)
+@pytest.mark.parametrize("shape", range(len(WIDE)))
+def test_trees_whose_masks_have_many_words(device, size, shape):
+    """Tiles of keys that begin and end inside mask words, in the workgroups'
+    own tiles and in split ones."""
+    case = dict(size, **WIDE[shape])
+    if size["Hq"] == 128:
+        case["every"] *= 4
+    say(case)
+    _, c, table, q, w, seen, scale = problem(case)
+    out, lse = run_attention(device, case, c, table, q, w, seen, scale)
+    check_attention(case, c, table, q, w, seen, scale, out, lse)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("Dn", [None, 64])
 def test_strides(device, Dn):
