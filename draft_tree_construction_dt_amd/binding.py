@@ -794,7 +794,7 @@ def _sample_shape(logits: torch.Tensor, lead: Optional[int], where: str):
 
 
 def dt_sample_workspace(logits: torch.Tensor) -> int:
-    """Bytes of workspace that dt_sample_rows needs for these logits [B][rows][V]."""
+    """Bytes of workspace that dt_sample_rows needs for these logits [B][rows][V]: 0 at present."""
     B, rows, V, lead = _sample_shape(logits, None, "dt_sample_workspace")
     return int(_load().dt_sample_workspace(_pack_sample(
         0, B, lead, 0, V, _LOGIT_TYPES[logits.dtype], 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)))
@@ -810,7 +810,7 @@ def dt_sample_rows(logits: torch.Tensor, u: torch.Tensor, tokens: torch.Tensor,
     in dt.h).  lead defaults to every row (no tree).  u float32 [B][lead +
     n_max] in [0, 1); temperature, top_p and min_p float32 [B], top_k int32 [B];
     tokens int32 and logp float32 [B][lead + n_max] are written; workspace of
-    dt_sample_workspace() bytes (None where that is 0)."""
+    dt_sample_workspace() bytes, None as long as that is 0."""
     w, dev, i32, f32 = "dt_sample_rows", logits.get_device(), torch.int32, torch.float32
     B, rows, V, lead = _sample_shape(logits, lead, w)
     each, every = (B,), (B, rows)

@@ -1147,10 +1147,7 @@ static dt_status check_sample(const dt_sample_params* p) {
     return DT_OK;
 }
 
-extern "C" size_t dt_sample_workspace(const dt_sample_params* p) {
-    if (check_sample(p) != DT_OK) return 0;
-    return sample_workspace((int64_t)p->B * (p->lead + p->n_max), p->V, p->dtype);
-}
+extern "C" size_t dt_sample_workspace(const dt_sample_params*) { return 0; }     // a row's state is in LDS
 
 extern "C" dt_status dt_sample_rows(const dt_sample_params* p) {
     const dt_status st = check_sample(p);
@@ -1175,9 +1172,7 @@ extern "C" dt_status dt_sample_rows(const dt_sample_params* p) {
     a.min_p = p->min_p;
     a.tokens = p->tokens;
     a.logp = p->logp;
-    if (no_workspace(p->workspace, p->workspace_bytes, sample_workspace((int64_t)a.B * a.rows, a.V, p->dtype)))
-        return DT_ERR_WORKSPACE;
     const DeviceScope scope((hipStream_t)p->stream);
-    if (!scope.ok() || launch_sample(a, p->dtype, p->workspace, (hipStream_t)p->stream) != hipSuccess) return DT_ERR_HIP;
+    if (!scope.ok() || launch_sample(a, p->dtype, (hipStream_t)p->stream) != hipSuccess) return DT_ERR_HIP;
     return DT_OK;
 }

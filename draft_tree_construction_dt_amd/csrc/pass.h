@@ -144,8 +144,7 @@ hipError_t launch_latent_prefill(AttentionArgs a, const void* weight, int dtype,
                                  hipStream_t stream);
 size_t prefill_workspace(const ChunkArgs& c, int Hq, int N, int keys);     // SIZE_MAX: more than a buffer can have
 hipError_t launch_logits(const LogitsArgs& a, int dtype, hipStream_t stream);
-hipError_t launch_sample(const SampleArgs& a, int dtype, void* workspace, hipStream_t stream);
-size_t sample_workspace(int64_t rows, int V, int dtype);
+hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_commit(const CommitArgs& a, hipStream_t stream);
 
 #ifdef __HIPCC__

@@ -1084,9 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
 
 }  // namespace
 
-size_t sample_workspace(int64_t, int, int) { return 0; }
-
-hipError_t launch_sample(const SampleArgs& a, int dtype, void*, hipStream_t stream) {
+hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t stream) {
     int n = 0;
     while ((1ll << n) < a.V) ++n;
     const int shift = 62 - n < 50 ? 62 - n : 50;

@@ -660,7 +660,7 @@ typedef struct dt_sample_params {
     const float* min_p;        /* [B] or NULL; not above 0 (or NaN): off */
     int32_t* tokens;           /* [B][lead + n_max] */
     float* logp;               /* [B][lead + n_max] or NULL: log of the probability the token was drawn with */
-    void* workspace;           /* 16-byte aligned device scratch of dt_sample_workspace() bytes */
+    void* workspace;           /* not read: no call needs one at present */
     size_t workspace_bytes;
     void* stream;
 } dt_sample_params;
@@ -681,13 +681,10 @@ typedef struct dt_sample_params {
  * unspecified token (but a memory-safe one, in -1..V-1), and u outside [0, 1)
  * the first or the last token that stays.  Rows behind the last node are
  * left as they were.
- * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above),
- *   DT_ERR_WORKSPACE, DT_ERR_HIP. */
+ * Errors: DT_ERR_INVALID_ARG, DT_ERR_UNSUPPORTED (a limit above), DT_ERR_HIP. */
 dt_status dt_sample_rows(const dt_sample_params* p);
 
-/* Bytes of workspace dt_sample_rows needs (depends on B, lead, n_max, V and
- * dtype only); 0 if none is needed or a call would be refused for these.  Its
- * contents are meaningless between calls. */
+/* Bytes of workspace dt_sample_rows needs: 0 for every call at present. */
 size_t dt_sample_workspace(const dt_sample_params* p);
 
 #ifdef __cplusplus

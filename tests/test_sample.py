@@ -61,6 +61,12 @@ def test_empty_batches_null_and_workspace():
     bd.dt_sample_rows(x, torch.zeros(0, 3), torch.zeros(0, 3, dtype=I32))
 
 
+@pytest.mark.parametrize("dtype,V", [(0, 1), (0, 32000), (1, 151936), (1, (1 << 26) - 1)])
+def test_no_call_needs_a_workspace(dtype, V):
+    assert bd._load().dt_sample_workspace(ctypes.byref(_params(dtype=dtype, V=V, B=1, n_max=0))) == 0
+    assert bd.dt_sample_workspace(torch.empty(2, 3, V, dtype=(F32, BF16)[dtype], device="meta")) == 0
+
+
 def test_binding_checks_tensors():
     x, u, t = torch.zeros(2, 3, 50), torch.zeros(2, 3), torch.zeros(2, 3, dtype=I32)
     for bad in (dict(logits=x.half()), dict(logits=x[0]), dict(logits=x[..., ::2]), dict(u=u[:1]), dict(u=u.double()),
