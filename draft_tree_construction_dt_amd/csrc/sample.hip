@@ -907,14 +907,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
     float mine = -INFINITY, second = -INFINITY;
     int where = 0;
     row.template groups_of<4>(g0, g0 + per < row.groups ? g0 + per : row.groups, lane, [&](int g, const u32x4& v) {
-        // (comparisons: fmaxf of a number and a signalling NaN is NaN)
-        float x = -INFINITY, y = -INFINITY;
+        // (a sum's NaN is a quiet one, of which fmaxf takes the number beside it; of a signalling one it would not)
+        float x = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < Row<E>::kEach; e += 2) {
-            x = Row<E>::at(v, e) > x ? Row<E>::at(v, e) : x;
-            y = Row<E>::at(v, e + 1) > y ? Row<E>::at(v, e + 1) : y;
-        }
-        x = fmaxf(x, y);
+        for (int e = 0; e < Row<E>::kEach; ++e) x = fmaxf(x, Row<E>::at(v, e) + 0.0f);
         second = fmaxf(second, fminf(mine, x));
         where = x > mine ? g : where;
         mine = x > mine ? x : mine;
