@@ -17,10 +17,10 @@
 // Both share its split of the work and its join.
 //
 // Measured, expanded (bf16, C = 512, R = 64, N = 128, 32 heads, two chunks of
-// 1801-2048 rows over 6-14 K keys, 1.08 T operations): 1240 us, 875 TFLOP/s of
-// the 1402 of a large matrix product; make_kernel 324 us of it, attention 1017
-// (matrix and vector units in turn, as with heads' own keys), the join 26.  A
-// chunk of 300 rows over 511 keys and 16 heads 41 us, three dependent launches.
+// 1801-2048 rows over 6-14 K keys, 1.08 T operations): 1245 us, 870 TFLOP/s of
+// the 1402 of a large matrix product; make_kernel 298 us of it, attention 940
+// (matrix and vector units in turn, as with heads' own keys), the join 25.  A
+// chunk of 300 rows over 511 keys and 16 heads 40 us, three dependent launches.
 // Keys, values and weights are rounded to the cache's type: the result's error
 // against 64 bits is 0.0020-0.0030 in bf16 where fp32 ones leave 0.0017, most of
 // which is the result's own rounding.
@@ -40,7 +40,7 @@ constexpr int kMadeRow = kMakeTile * 2 + 16;   // bytes of a key's results in LD
 // out[key][n] = sum_i W[n][i] c[key][i] for 128 keys of one request and 128 rows
 // of the weight; four waves take 64 x 64 each.  The weight's rows are the left
 // operand, so a lane ends with one key and runs of its row.  Bound by the
-// way from L2 to LDS and its waits: 324 us for 24 K keys of 32 heads (four buffers
+// way from L2 to LDS and its waits: 298 us for 24 K keys of 32 heads (four buffers
 // of 32 elements a step instead of two of 64: the same).
 template <class T, int C, int N>
 __global__ void __launch_bounds__(256) make_kernel(AttentionArgs a, const uint16_t* weight, uint16_t* made) {

@@ -42,12 +42,12 @@ struct Latents : Rotated<R> {
 // between two barriers, with the copies of the tiles after that in flight.
 //
 // Measured (C = 512, R = 64, bf16, 64 requests over 33-16383 keys, 0.6 GB): one
-// token of 16 heads 153 us, 4.0 TB/s (a copy, read and written, 4.9); of 128
-// heads 238 us, 616 TFLOP/s, where memory alone would take 127 and the matrix
+// token of 16 heads 151 us, 4.0 TB/s (a copy, read and written, 4.9); of 128
+// heads 235 us, 624 TFLOP/s, where memory alone would take 127 and the matrix
 // cores 104.  What bounds the latter is one wave a SIMD: a round takes about 3000
 // cycles, 1088 of them the matrix core's, the rest the latencies and the issue
 // of a wave that nothing else covers.  Trees of 64 nodes, 28 heads, C = 256 over
-// 6-10 K keys 210 us, 570 TFLOP/s.  Tried and dropped: eight waves with 64 keys a
+// 6-10 K keys 206 us, 580 TFLOP/s.  Tried and dropped: eight waves with 64 keys a
 // tile (one token of one request 22 us instead of 24, 128 heads 285, trees 282);
 // all 64 rows and a quarter of the outputs a wave (half of the LDS reads of the
 // second product; 128 heads 252 where this took 254: it is not those reads).
@@ -330,7 +330,9 @@ __device__ __forceinline__ void attend_latents(const AttentionArgs& a, const Job
         return Met{{*(const s16x8*)at, *(const s16x8*)(at + 32)}, max_of(buf, 0, row32), max_of(buf, 1, row32)};
     };
     // That becomes one, the larger: for this wave's sums and outputs, and the
-    // weights as read.
+    // weights as read.  Weights of the wave that was behind are rounded a second
+    // time, in those tiles only: they are off by two half steps of the type at most.
+    // One rounding would take weights of 32 bits through LDS in every tile.
     const auto agree = [&](int buf, Met& met) __attribute__((always_inline)) {
         s16x8 (&p)[2] = met.p;
         const float m0 = met.m0, m1 = met.m1, mm = fmaxf(m0, m1);

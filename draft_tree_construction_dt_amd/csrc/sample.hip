@@ -22,9 +22,13 @@
 //               parts.
 // A list that overflows, or a larger top_k, narrows the cut over the row itself.
 //
-// Measured: 512 rows of 151936 bf16 (156 MB), every kind of setting among them,
-// 129 us, 1.2 TB/s (a copy's rate would take 32): the rows with top-p make every
-// weight and count values in LDS, and are bound by vector units; one row of 32000
+// Measured: 512 rows of 151936 bf16 (156 MB; a copy's rate would take 32 us) in
+// 28 us where all are greedy, 60-64 with top-k 20-50, 72 with temperature alone,
+// 85 with min-p, 93 with top-k 1000, 129-131 with top-p; every kind of setting
+// among them 126-129.  All of these rows are resident at once, two a compute unit, so a mixed
+// batch lasts as long as its slowest row: a compute unit has work 55% of the time
+// and vector units are busy 32% (77% and 52% where all rows have top-p, whose
+// waves spend 55% of their time waiting for memory and LDS).  One row of 32000
 // fp32 20 us, the latency of its passes.  A workgroup of 1024 threads a row took
 // 17 us for the one row and 164 for the 512.
 #include <float.h>
@@ -40,13 +44,23 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;      // two workgroups on a compute unit
 constexpr int kBits = 11, kBins = 1 << kBits;              // of a histogram
-constexpr int kList = 6144;        // tokens of the list
+// Tokens of the list: what the LDS of two workgroups leaves.  (512 rows of 151936
+// with top_k 1000: 94 us with 4096 as with 6144; 2048 overflow, 340 us and more.)
+constexpr int kList = 6144;
 // How many of the threads' two largest logits reach the list's limit.  For top_k
-// as many as that, up to 1000; for top_p alone 896.
+// as many as that; a workgroup has 1024 of them, and the largest usual top_k is
+// 1000.  Larger ones go by counted values or over the row (512 rows of 151936,
+// top_k 1000: 88 us by list, 130 by counted bf16 values; fp32 122 by list, 354 over
+// the row; one row of 32000: 26 and 28, fp32 29 and 53; smaller top_k gain more).
 constexpr int kMostK = 1000;
+// For top_p alone (fp32) a fixed number.  512 rows of 151936, top_p 0.9, with 224,
+// 448, 896, 1000: 325, 329, 338, 342 us; one row of 32000: 35, 36, 39, 41.
 constexpr int kForP = 896;
 constexpr int kTable = 64;
-constexpr int kShort = 256;        // tokens of a list whose pairs are compared
+// Tokens of a list whose pairs are compared.  512 rows of 151936 bf16 with 64, 128,
+// 256, 512: top_k 50 60, 61, 64, 67 us, 100 71, 65, 70, 78, 200 72, 72, 84, 98,
+// min_p 0.05 67, 67, 85, 152.
+constexpr int kShort = 256;
 constexpr unsigned kMaxGridX = 1 << 20;
 
 // Bits whose order is that of the values (no NaN; -0 and 0 are one).
@@ -735,7 +749,7 @@ struct KeptByValue {
         else if (by.is_tiny(x)) sum.weight += kept_weight(ask, edge, id, x);
         else if (x != edge.value || id <= edge.last) sum.weight += by.weight(x);
     }
-    // the reads of LDS side by side; tiny logits, which are few, one by one
+    // the reads of LDS side by side; tiny logits, usually few, one by one
     __device__ __forceinline__ void group(int g, const u32x4& v, Sum& sum) const {
         uint32_t at[8];
         u64 w[8];
@@ -763,7 +777,10 @@ struct KeptByValue {
     }
 };
 
-// Counts every value of the row.
+// Counts every value of the row.  Tiny logits (magnitudes below the 22 binades:
+// exact zeros at ordinary temperatures) take three atomics on the same words: 512
+// rows of 151936 bf16 with top_p 137 us, 244 where 1% of the logits are 0, 1410
+// where half are, 2430 where 99% are (one row 62, 140, 554 and 1590).
 template <class E>
 __device__ __forceinline__ void count_values(const Row<E>& row, const ByValue& by, const Ask& ask, int wave, int lane) {
     const int tid = wave * 64 + lane, per = (row.groups + kWaves - 1) / kWaves;
