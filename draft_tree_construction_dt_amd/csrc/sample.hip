@@ -1040,8 +1040,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, int s
             }
         }
     } else if (!by_p && ask.top_k == 0 && ask.least > 0) {
-        // what min_p leaves, and a little more for the roundings of this limit
-        const double below = (double)temperature * fmin(log((double)min_p), 0.0);
+        // what min_p leaves, weights that round up to it among them, and a little more
+        // for the roundings of weights (below 2^-43 of them) and of this limit
+        const double below = (double)temperature * (fmin(log(ldexp((double)ask.least - 0.5, -shift)), 0.0) - 1e-12);
         const float limit = fmaxf((float)((double)top + below - 1e-6 * (fabs((double)top) - below) - 1e-37), -FLT_MAX);
         if (make_list(row, [&](float x) { return x >= limit; }, s, wave, lane)) holds = kAll;
         n = (int)s.listed;

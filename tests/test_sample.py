@@ -442,3 +442,29 @@ def test_zeros_of_both_signs_are_one_value(device, dtype, temperature):
     got = draw(device, signed, u, **how)
     assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
     check(signed, u, *got, **how)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("temperature", [1.0, 1e4, 1e8, 1e15, 1e30, 3e38, math.inf])
+def test_min_p_goes_by_the_rounded_weights(device, dtype, temperature):
+    """Whichever way a row goes: a top_p that leaves everything with any weight
+    in its row (6000 alike are each above 2^-24 of the sum) takes another way than
+    min_p alone."""
+    rs = np.random.RandomState(35)
+    least = [1.0, 1 - 2.0 ** -24, 1 - 2.0 ** -22, 0.999, 0.5, 2.5]
+    B, rows, V = len(least), 8, 6000
+    x = rs.standard_normal((B, rows, V))
+    x[:, ::2] = np.maximum(x[:, ::2], 1.0)                        # (thousands of tokens, and rows with few of them)
+    x[:, 1, rs.rand(V) < 0.1] = -np.inf
+    x = torch.from_numpy(x).to(dtype)
+    u = ((torch.arange(rows) + 0.5) / rows).expand(B, rows).contiguous()
+    how = dict(temperature=[temperature] * B, min_p=least)
+    got = draw(device, x, u, **how)
+    want = draw(device, x, u, top_p=[1 - 2.0 ** -24] * B, **how)
+    assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
+    if temperature >= 1e30:                                       # all weights are 1
+        for b in range(B - 1):                                    # (and the last one asks for more)
+            for r in range(rows):
+                ids = np.flatnonzero(np.isfinite(x[b, r].float().numpy()))
+                assert got[0][b, r] == ids[int((r + 0.5) / rows * len(ids))]
