@@ -25,11 +25,11 @@
 // Measured: 512 rows of 151936 bf16 (156 MB; a copy's rate would take 32 us) in
 // 28 us where all are greedy, 60-64 with top-k 20-50, 72 with temperature alone,
 // 85 with min-p, 93 with top-k 1000, 129-131 with top-p; every kind of setting
-// among them 126-129.  All of these rows are resident at once, two a compute unit, so a mixed
-// batch lasts as long as its slowest row: a compute unit has work 55% of the time
-// and vector units are busy 32% (77% and 52% where all rows have top-p, whose
-// waves spend 55% of their time waiting for memory and LDS).  One row of 32000
-// fp32 20 us, the latency of its passes.  A workgroup of 1024 threads a row took
+// among them 126-129.  All of these rows are resident at once, two a compute
+// unit, so a mixed batch lasts as long as its slowest row: a compute unit has work
+// 55% of the time and vector units are busy 32% (77% and 52% where all rows have
+// top-p, whose waves spend 55% of their time waiting for memory and LDS).  One row
+// of 32000 fp32 20 us, the latency of its passes.  A workgroup of 1024 threads a row took
 // 17 us for the one row and 164 for the 512.
 #include <float.h>
 #include <math.h>
@@ -1102,7 +1102,7 @@ hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t stream) {
     int n = 0;
     while ((1ll << n) < a.V) ++n;
     const int shift = 62 - n < 50 ? 62 - n : 50;
-    // threads along x count in 32 bits: 2^23 rows and more take several in y
+    // threads along x count in 32 bits, fewer than 2^23 rows: from 2^20 on they go on in y
     const unsigned rows = (unsigned)((int64_t)a.B * a.rows), x = rows < kMaxGridX ? rows : kMaxGridX;
     const dim3 grid(x, (rows + x - 1) / x);
     if (dtype == DT_DTYPE_BF16) sample_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(a, shift);
